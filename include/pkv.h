@@ -229,6 +229,121 @@ pkv_status paged_attention(const void* q, int64_t q_token_stride, int64_t q_head
                            int32_t* err, void* stream);
 
 /*
+ * kv_append_fp8 -- quantise this step's K/V rows into an 8-bit paged cache.
+ *
+ * The cache holds e4m3 codes (one byte per element, the pool layout above with
+ * 1-byte elements) and, for K and V apart, one f32 scale for every page and
+ * K/V head: element = code * scale[page * scale_stride + head].  The rows and
+ * positions are those of paged_attention on the same arguments: sequence b's
+ * new tokens are source rows q_indptr[b] .. q_indptr[b] + q_real[b] - 1 and
+ * its last q_real[b] keys, at positions kv_lens[b] - q_real[b] + i; logical
+ * page position / 32 is block_table[b * block_table_stride + position / 32].
+ *
+ * For every (page, head) that receives rows:
+ *   need  = 2^e, the smallest e >= -126 with amax <= 448 * 2^e, amax the
+ *           largest |element| of the new rows of that page and head (0 if all
+ *           are 0; NaN does not count, infinities count as the largest finite
+ *           value of the source type)
+ *   scale = max(old scale, need) if the page also holds earlier tokens of the
+ *           sequence, else need: a page starts anew with its first slot
+ *   codes = the nearest e4m3 value of element / scale (ties to even; NaN stays
+ *           NaN).  Where the scale grew, the earlier slots' codes become the
+ *           nearest e4m3 values of code * old scale / scale: exact for scales
+ *           this call wrote, but for codes that become subnormal.
+ * With power-of-two scales the division is exact, so every element carries one
+ * rounding to e4m3 (half a unit in 4 significant bits) unless its page's scale
+ * grew later by more than its own magnitude allows.
+ *
+ * A page that receives rows must belong to one sequence (copy a shared last
+ * page first); slots past the last key, and pages that receive no row, keep
+ * their bytes and scale.  Padding rows, positions below 0 or at or past
+ * max_kv_len and block-table entries outside [0, num_pages) are skipped (the
+ * last two also set PKV_ERRBIT_LEN / PKV_ERRBIT_PAGE with PKV_FLAG_CHECKED).
+ * Calling it again with the same arguments writes the same bytes.
+ *
+ *  k_src, v_src   device, src_dtype (bf16, f16 or f32); source element
+ *                 (row, h, d) at row * src_token_stride + h * src_head_stride
+ *                 + d, 16-byte aligned rows and heads
+ *  k_pool, v_pool device e4m3 pools, 16-byte aligned; page_stride in bytes, a
+ *                 multiple of 16
+ *  k_scale, v_scale  device f32 [num_pages][scale_stride], scale_stride >=
+ *                 num_kv_heads
+ *  head_dim       64 or 128; page_size 32
+ */
+pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dtype,
+                         int64_t src_token_stride, int64_t src_head_stride,
+                         const int32_t* block_table, int64_t block_table_stride,
+                         const int32_t* kv_lens, const int32_t* q_indptr, const int32_t* q_real,
+                         int batch, int max_q_rows, int max_kv_len, int num_kv_heads, int head_dim,
+                         void* k_pool, void* v_pool, int64_t num_pages, int page_size,
+                         int64_t page_stride, float* k_scale, float* v_scale, int64_t scale_stride,
+                         unsigned flags, int32_t* err, void* stream);
+
+/*
+ * paged_attention_fp8 -- paged_attention over the 8-bit cache of kv_append_fp8,
+ * optionally with a sliding window and sinks.
+ *
+ * Same rows, masks, outputs and conventions as paged_attention, with
+ *   k_j = k_scale[page(j), head] * code,  v_j = v_scale[page(j), head] * code
+ * (any finite f32 scales >= 0).  window = 0 attends as `mask` says.  window > 0
+ * (mask PKV_MASK_CAUSAL only): the row at position p = kv_len - q_real + i sees
+ * the keys j <= p with j > p - window (its own key and the window - 1 before
+ * it) or j < num_sinks (the first tokens, which stay visible).
+ * num_sinks = 0 without a window.
+ *
+ * Pages whose keys no row of the call sees are not read: their block-table
+ * entries may hold anything (pages behind the window can be freed).  The bytes
+ * of slots past the last key, and the scores of masked keys, never reach a
+ * result, whatever they hold.  V of a key that one row sees and another row of
+ * the same sequence does not must be finite: a row's weight for it is zero, and
+ * zero times infinity or NaN is NaN.
+ *
+ * The softmax weights are rounded once before the P.V product: to f16 (2^-11
+ * relative) by the few-row kernel, to bf16 (2^-8 at most) by the tile kernel;
+ * sums, maxima and the LSE are f32.  Calls whose rows x grouped heads are many
+ * first expand the visible pages to bf16 in the workspace (code * scale, exact
+ * for the power-of-two scales kv_append_fp8 writes).
+ *
+ *  workspace      paged_attention_fp8_workspace_size(...) bytes, 256-byte
+ *                 aligned; one workspace must not serve two calls in flight
+ *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY
+ */
+size_t paged_attention_fp8_workspace_size(int batch, int max_q_rows, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int max_kv_len,
+                                          int window, int num_sinks, unsigned flags);
+pkv_status paged_attention_fp8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* k_pool, const void* v_pool, const float* k_scale,
+                               const float* v_scale, int64_t scale_stride, int64_t num_pages,
+                               int page_size, int64_t page_stride, const int32_t* block_table,
+                               int64_t block_table_stride, const int32_t* kv_lens,
+                               const int32_t* q_indptr, const int32_t* q_real, int batch,
+                               int max_q_rows, int max_kv_len, int num_q_heads, int num_kv_heads,
+                               int head_dim, pkv_mask mask, int causal_block, int window,
+                               int num_sinks, float scale, void* out, pkv_dtype out_dtype,
+                               float* lse, void* workspace, size_t workspace_bytes, unsigned flags,
+                               int32_t* err, void* stream);
+
+/*
+ * paged_attention_window -- causal paged_attention of bf16 pools with a sliding
+ * window and sinks: the row at position p sees the keys p - window + 1 .. p and
+ * the keys below num_sinks.  window >= 1; everything else as in
+ * paged_attention (causal) and paged_attention_fp8 (freed pages, masked slots).
+ */
+size_t paged_attention_window_workspace_size(int batch, int max_q_rows, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int max_kv_len,
+                                             int window, int num_sinks, unsigned flags);
+pkv_status paged_attention_window(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const void* k_pool, const void* v_pool, int64_t num_pages,
+                                  int page_size, int64_t page_stride, const int32_t* block_table,
+                                  int64_t block_table_stride, const int32_t* kv_lens,
+                                  const int32_t* q_indptr, const int32_t* q_real, int batch,
+                                  int max_q_rows, int max_kv_len, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int window, int num_sinks,
+                                  float scale, void* out, pkv_dtype out_dtype, float* lse,
+                                  void* workspace, size_t workspace_bytes, unsigned flags,
+                                  int32_t* err, void* stream);
+
+/*
  * rope_write_kv_paged -- rotary embedding of this step's queries (in place)
  * and keys, with the rotated keys and the values written into pool slots, in
  * one launch (the step that precedes paged_attention).

@@ -1,0 +1,233 @@
+// kv_append.cu -- kv_append_fp8: quantise new K/V rows into an 8-bit paged cache.
+//
+// An element is code * scale with an e4m3 code and one f32 scale per (32-token
+// page, K/V head), K and V apart.  The scale is a power of two, 2^e with the
+// smallest e for which the largest magnitude fits 448 * 2^e: dividing by it
+// changes no bit, so an element carries exactly one rounding, and when a later
+// token raises the scale of a page that already holds tokens, moving the old
+// codes to it only lowers their exponents -- no second rounding until a code
+// becomes subnormal.  e4m3 keeps 4 significant bits over 2^-6 .. 448 whatever
+// the scale, so the up-to-one bit of range a power of two gives away costs
+// nothing; an amax / 448 scale would round every old code again at each growth.
+//
+// One warp per (sequence, touched page, K/V head, K or V): it owns the page's
+// 32 slots of that head, so nothing is shared between warps and the result does
+// not depend on their order.  The warp's rows (16-byte vectors, D * size / 16
+// lanes of them a row) are loaded together and stay in registers between the
+// maximum and the conversion, so every source byte is read once.
+// Bound: HBM for chunks (2 bytes read and 1 written per bf16 element), launch
+// and one chain of dependent loads (lengths, page id, row, old scale) for one
+// token per sequence.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "pkv_common.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kPage = 32;
+constexpr int kWarps = 4;
+
+// two f32 -> two e4m3 codes (round to nearest even, saturating; NaN stays NaN)
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t pair) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+// The values of one 16-byte vector as f32, infinities brought to the type's
+// largest finite value.
+template <typename T>
+struct Src;
+template <>
+struct Src<__nv_bfloat16> {
+    static constexpr int kVec = 8;
+    __device__ static void widen(const uint4& v, float (&x)[kVec]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        constexpr float top = 3.3895313892515355e38f;  // 0x7f7f
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16lo(w[i]);
+            x[2 * i + 1] = bf16hi(w[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(top, x[i]);
+    }
+};
+template <>
+struct Src<__half> {
+    static constexpr int kVec = 8;
+    __device__ static void widen(const uint4& v, float (&x)[kVec]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(65504.f, x[i]);
+    }
+};
+template <>
+struct Src<float> {
+    static constexpr int kVec = 4;
+    __device__ static void widen(const uint4& v, float (&x)[kVec]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            x[i] = __uint_as_float(w[i]);
+            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(3.4028234663852886e38f, x[i]);
+        }
+    }
+};
+
+// 2^e, the smallest e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(e + 8); 0 for 0
+__device__ __forceinline__ float scale_for(float amax) {
+    if (!(amax > 0.f)) return 0.f;
+    const uint32_t u = __float_as_uint(amax);
+    const int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);
+    return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+}
+
+// x / scale: by the exact reciprocal where the scale is a power of two
+struct Divide {
+    float scale, inv;
+    bool exact;
+    __device__ explicit Divide(float s) : scale(s), inv(s > 0.f ? 1.0f / s : 0.f) {
+        exact = (__float_as_uint(s) & 0x7fffffu) == 0;
+    }
+    __device__ float operator()(float x) const { return exact ? x * inv : x / scale; }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) append_fp8_kernel(const AppendArgs a, int pages_bound) {
+    constexpr int kVec = Src<T>::kVec;          // elements of a lane's vector
+    constexpr int kLanes = D / kVec;            // lanes a row takes
+    constexpr int kRows = 32 / kLanes;          // rows of one warp-wide load
+    constexpr int kSteps = kPage / kRows;
+    const int lane = threadIdx.x & 31;
+    const int Hkv = a.num_kv_heads;
+    const int b = blockIdx.y;
+    const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (page, K or V, head), heads fastest
+    const int t = item / (2 * Hkv);
+    if (t >= pages_bound) return;
+    const int which = (item / Hkv) & 1, h = item % Hkv;
+
+    const int r0 = a.q_indptr[b];
+    const int rows = a.q_indptr[b + 1] - r0, nrows = min(rows, a.max_q_rows);
+    const int qreal = min(a.q_real ? a.q_real[b] : nrows, nrows);
+    int kv_len = a.kv_lens[b];
+    if (a.checked && item == 0 && lane == 0 &&
+        (kv_len > a.max_kv_len || kv_len < 0 || rows > a.max_q_rows || (a.q_real && a.q_real[b] > rows)))
+        set_err(a.err, PKV_ERRBIT_LEN);
+    kv_len = min(max(kv_len, 0), a.max_kv_len);
+    if (qreal <= 0) return;
+    const int first = kv_len - qreal;                 // position of the first new row (may be below 0)
+    const int pos0 = (max(first, 0) / kPage + t) * kPage;  // this page's first position
+    if (pos0 >= kv_len) return;
+    const int page = a.block_table[b * a.block_table_stride + pos0 / kPage];
+    if (page < 0 || page >= a.num_pages) {
+        if (a.checked && lane == 0) set_err(a.err, PKV_ERRBIT_PAGE);
+        return;
+    }
+    const int begin = max(first - pos0, 0), end = min(kv_len - pos0, kPage);  // slots that receive rows
+    float* sp = a.scale[which] + page * a.scale_stride + h;
+    const float had = begin > 0 ? *sp : 0.f;
+
+    const int sub = lane / kLanes, col = (lane % kLanes) * kVec;
+    const T* src = static_cast<const T*>(a.src[which]) + (static_cast<int64_t>(r0) - first + pos0) * a.src_token_stride +
+                   static_cast<int64_t>(h) * a.src_head_stride + col;
+    uint4 v[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int slot = s * kRows + sub;
+        v[s] = slot >= begin && slot < end
+                   ? __ldg(reinterpret_cast<const uint4*>(src + slot * a.src_token_stride))
+                   : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        float x[kVec];
+        Src<T>::widen(v[s], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf passes NaN over
+    }
+    const float scale = fmaxf(had, scale_for(warp_max(amax)));
+    const Divide div(scale);
+    uint8_t* dst = a.pool[which] + page * a.page_stride + static_cast<int64_t>(h) * D + col;
+    const int64_t slot_stride = static_cast<int64_t>(Hkv) * D;
+    auto store = [&](int slot, const float (&y)[kVec]) {
+        uint32_t w[kVec / 4];
+#pragma unroll
+        for (int i = 0; i < kVec / 4; ++i)
+            w[i] = to_e4m3x2(y[4 * i], y[4 * i + 1]) | (to_e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+        if constexpr (kVec == 8) *reinterpret_cast<uint2*>(dst + slot * slot_stride) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(dst + slot * slot_stride) = w[0];
+    };
+    // the scale grew: the page's earlier codes, to the new one
+    if (begin > 0 && scale != had) {
+        for (int slot = sub; slot < begin; slot += kRows) {
+            uint32_t w[kVec / 4];
+            if constexpr (kVec == 8) {
+                const uint2 c = *reinterpret_cast<const uint2*>(dst + slot * slot_stride);
+                w[0] = c.x;
+                w[1] = c.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t*>(dst + slot * slot_stride);
+            }
+            float y[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec / 4; ++i) {
+                const float2 lo = from_e4m3x2(w[i] & 0xffffu), hi = from_e4m3x2(w[i] >> 16);
+                y[4 * i] = div(lo.x * had);
+                y[4 * i + 1] = div(lo.y * had);
+                y[4 * i + 2] = div(hi.x * had);
+                y[4 * i + 3] = div(hi.y * had);
+            }
+            store(slot, y);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int slot = s * kRows + sub;
+        if (slot >= begin && slot < end) {
+            float x[kVec];
+            Src<T>::widen(v[s], x);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[i] = div(x[i]);
+            store(slot, x);
+        }
+    }
+    if (lane == 0) *sp = scale;
+}
+
+template <typename T>
+cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
+    // n rows touch at most (n + 30) / 32 + 1 pages, whatever slot they start at
+    const int pages = (a.max_q_rows + kPage - 2) / kPage + 1;
+    const int64_t items = static_cast<int64_t>(pages) * 2 * a.num_kv_heads;
+    const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps), a.batch);
+    if (a.head_dim == 128) append_fp8_kernel<T, 128><<<grid, kWarps * 32, 0, s>>>(a, pages);
+    else append_fp8_kernel<T, 64><<<grid, kWarps * 32, 0, s>>>(a, pages);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_fp8(const AppendArgs& a, cudaStream_t s) {
+    switch (a.src_dtype) {
+        case PKV_BF16: return launch_t<__nv_bfloat16>(a, s);
+        case PKV_F16: return launch_t<__half>(a, s);
+        default: return launch_t<float>(a, s);
+    }
+}
+
+}  // namespace pkv

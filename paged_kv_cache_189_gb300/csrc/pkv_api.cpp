@@ -658,6 +658,226 @@ pkv_status rope_write_kv_paged(void* q, int64_t q_token_stride, int64_t q_head_s
     return from_cuda(pkv::launch_rope_write(a, static_cast<cudaStream_t>(stream)), "rope launch");
 }
 
+pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dtype,
+                         int64_t src_token_stride, int64_t src_head_stride,
+                         const int32_t* block_table, int64_t block_table_stride,
+                         const int32_t* kv_lens, const int32_t* q_indptr, const int32_t* q_real,
+                         int batch, int max_q_rows, int max_kv_len, int num_kv_heads, int head_dim,
+                         void* k_pool, void* v_pool, int64_t num_pages, int page_size,
+                         int64_t page_stride, float* k_scale, float* v_scale, int64_t scale_stride,
+                         unsigned flags, int32_t* err, void* stream) {
+    const int esz = elem_size(src_dtype);
+    if (esz == 0) return fail(PKV_ERR_INVALID_ARG, "append: unknown source dtype %d", (int)src_dtype);
+    if (batch < 0 || max_q_rows < 0 || max_kv_len < 0 || num_kv_heads < 0 || num_pages < 0)
+        return fail(PKV_ERR_INVALID_ARG, "append: negative size");
+    if (batch == 0 || max_q_rows == 0 || max_kv_len == 0 || num_kv_heads == 0) return ok();
+    if (!k_src || !v_src || !block_table || !kv_lens || !q_indptr || !k_pool || !v_pool || !k_scale || !v_scale)
+        return fail(PKV_ERR_INVALID_ARG, "append: null pointer");
+    if (page_size != 32)
+        return fail(PKV_ERR_UNSUPPORTED, "append: page_size %d (only 32-token pages)", page_size);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "append: head_dim %d (64 or 128)", head_dim);
+    if (batch > 65535) return fail(PKV_ERR_UNSUPPORTED, "append: batch above 65535");
+    if (page_stride < static_cast<int64_t>(page_size) * num_kv_heads * head_dim || page_stride % 16)
+        return fail(PKV_ERR_INVALID_ARG, "append: page_stride %lld must cover a page and be a multiple of 16",
+                    (long long)page_stride);
+    if (scale_stride < num_kv_heads)
+        return fail(PKV_ERR_INVALID_ARG, "append: scale_stride %lld below %d K/V heads", (long long)scale_stride,
+                    num_kv_heads);
+    if (!aligned(k_src, 16) || !aligned(v_src, 16) || src_token_stride < 0 || src_head_stride < 0 ||
+        (src_token_stride * esz) % 16 || (src_head_stride * esz) % 16)
+        return fail(PKV_ERR_INVALID_ARG, "append: source rows and heads must be 16-byte aligned");
+    if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return fail(PKV_ERR_INVALID_ARG, "append: pools must be 16-byte, scales 4-byte aligned");
+    const int64_t pages_needed = (static_cast<int64_t>(max_kv_len) + page_size - 1) / page_size;
+    if (block_table_stride < pages_needed)
+        return fail(PKV_ERR_INVALID_ARG, "append: block_table_stride %lld < %lld pages for max_kv_len",
+                    (long long)block_table_stride, (long long)pages_needed);
+    if ((static_cast<int64_t>(max_q_rows) / 32 + 2) * 2 * num_kv_heads > 0x7fffffffLL)
+        return fail(PKV_ERR_UNSUPPORTED, "append: too many pages times K/V heads");
+    if ((flags & PKV_FLAG_CHECKED) && !err)
+        return fail(PKV_ERR_INVALID_ARG, "append: checked mode needs an error flag");
+    pkv::AppendArgs a{{k_src, v_src}, src_token_stride, src_head_stride, src_dtype, block_table,
+                      block_table_stride, kv_lens, q_indptr, q_real, batch, max_q_rows, max_kv_len,
+                      num_kv_heads, head_dim,
+                      {static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool)}, num_pages, page_stride,
+                      {k_scale, v_scale}, scale_stride, (flags & PKV_FLAG_CHECKED) != 0, err};
+    return from_cuda(pkv::launch_append_fp8(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+namespace {
+
+// Workspace of paged_attention_fp8 / paged_attention_window for these bounds.
+size_t ext_workspace(int, int, int, int, int, int, int, int, bool, unsigned) { return 0; }
+
+// The arguments paged_attention_fp8 and paged_attention_window share.
+struct ExtArgs {
+    const char* name;
+    bool fp8;
+    const void *q, *k_pool, *v_pool;
+    const float *k_scale, *v_scale;
+    int64_t q_token_stride, q_head_stride, scale_stride, num_pages, page_stride, block_table_stride;
+    int page_size;
+    const int32_t *block_table, *kv_lens, *q_indptr, *q_real;
+    int batch, max_q_rows, max_kv_len, num_q_heads, num_kv_heads, head_dim;
+    pkv_mask mask;
+    int causal_block, window, num_sinks;
+    float scale;
+    void* out;
+    pkv_dtype out_dtype;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+    int32_t* err;
+    cudaStream_t stream;
+};
+
+pkv_status ext_attention(const ExtArgs& a) {
+    const char* n = a.name;
+    if (a.batch < 0 || a.max_q_rows < 0 || a.max_kv_len < 0 || a.num_q_heads < 0 || a.num_kv_heads < 0 ||
+        a.num_pages < 0 || a.window < 0 || a.num_sinks < 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: negative size", n);
+    if (a.batch == 0 || a.max_q_rows == 0 || a.num_q_heads == 0) return ok();
+    if (a.num_kv_heads == 0 || a.num_q_heads % a.num_kv_heads != 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: %d query heads is not a multiple of %d K/V heads", n, a.num_q_heads,
+                    a.num_kv_heads);
+    if (!a.q || !a.k_pool || !a.v_pool || !a.block_table || !a.kv_lens || !a.q_indptr || !a.out ||
+        (a.fp8 && (!a.k_scale || !a.v_scale)))
+        return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", n);
+    if (a.page_size != 32)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: page_size %d (only 32-token pages)", n, a.page_size);
+    if (a.head_dim != 64 && a.head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: head_dim %d (64 or 128)", n, a.head_dim);
+    if (a.mask != PKV_MASK_NONE && a.mask != PKV_MASK_CAUSAL && a.mask != PKV_MASK_BLOCK_CAUSAL)
+        return fail(PKV_ERR_INVALID_ARG, "%s: unknown mask %d", n, (int)a.mask);
+    if (a.mask == PKV_MASK_BLOCK_CAUSAL && a.causal_block <= 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: block-causal mask needs causal_block > 0", n);
+    if (a.window > 0 && a.mask != PKV_MASK_CAUSAL)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: a window needs the causal mask", n);
+    if (a.window == 0 && a.num_sinks > 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: sinks need a window", n);
+    if (a.out_dtype != PKV_BF16 && a.out_dtype != PKV_F32)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: output dtype must be bf16 or f32", n);
+    if (a.batch > 65535 || a.num_kv_heads > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: batch or K/V heads above 65535", n);
+    const int esz = a.fp8 ? 1 : 2;
+    if (a.page_stride < static_cast<int64_t>(a.page_size) * a.num_kv_heads * a.head_dim ||
+        (a.page_stride * esz) % 16)
+        return fail(PKV_ERR_INVALID_ARG, "%s: page_stride %lld must cover a page and be a multiple of 16 bytes", n,
+                    (long long)a.page_stride);
+    if (a.fp8 && (a.scale_stride < a.num_kv_heads || !aligned(a.k_scale, 4) || !aligned(a.v_scale, 4)))
+        return fail(PKV_ERR_INVALID_ARG, "%s: scale_stride %lld below %d K/V heads, or misaligned scales", n,
+                    (long long)a.scale_stride, a.num_kv_heads);
+    if (!aligned(a.q, 16) || !aligned(a.k_pool, 16) || !aligned(a.v_pool, 16) || a.q_token_stride % 8 ||
+        a.q_head_stride % 8 || a.q_token_stride < 0 || a.q_head_stride < 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: q / pools must be 16-byte aligned with strides multiple of 8", n);
+    if (!aligned(a.out, 16) || (a.lse && !aligned(a.lse, 4)))
+        return fail(PKV_ERR_INVALID_ARG, "%s: output must be 16-byte aligned", n);
+    const int64_t pages_needed = (static_cast<int64_t>(a.max_kv_len) + a.page_size - 1) / a.page_size;
+    if (a.block_table_stride < pages_needed)
+        return fail(PKV_ERR_INVALID_ARG, "%s: block_table_stride %lld < %lld pages for max_kv_len", n,
+                    (long long)a.block_table_stride, (long long)pages_needed);
+    if (a.flags & ~(PKV_FLAG_CHECKED | PKV_FLAG_SIMT_ONLY))
+        return fail(PKV_ERR_UNSUPPORTED, "%s: flags 0x%x (only CHECKED and SIMT_ONLY)", n, a.flags);
+    if ((a.flags & PKV_FLAG_CHECKED) && !a.err)
+        return fail(PKV_ERR_INVALID_ARG, "%s: checked mode needs an error flag", n);
+    const size_t ws_bytes = ext_workspace(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim,
+                                          a.max_kv_len, a.window, a.num_sinks, a.fp8, a.flags);
+    if (ws_bytes > 0 && (!a.workspace || a.workspace_bytes < ws_bytes || !aligned(a.workspace, 256)))
+        return fail(PKV_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned", n, ws_bytes);
+
+    pkv::AttnParams p{};
+    p.q = a.q;
+    p.q_token_stride = a.q_token_stride;
+    p.q_head_stride = a.q_head_stride;
+    p.k_pool = a.k_pool;
+    p.v_pool = a.v_pool;
+    p.num_pages = a.num_pages;
+    p.page_stride = a.page_stride;
+    p.block_table = a.block_table;
+    p.block_table_stride = a.block_table_stride;
+    p.kv_lens = a.kv_lens;
+    p.q_indptr = a.q_indptr;
+    p.q_real = a.q_real;
+    p.batch = a.batch;
+    p.max_q_rows = a.max_q_rows;
+    p.max_kv_len = a.max_kv_len;
+    p.num_q_heads = a.num_q_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.head_dim = a.head_dim;
+    p.mask = static_cast<int>(a.mask);
+    p.causal_block = a.causal_block;
+    const float sc = a.scale > 0.f ? a.scale : 1.0f / std::sqrt(static_cast<float>(a.head_dim));
+    p.scale_log2 = sc * 1.4426950408889634f;
+    p.out = a.out;
+    p.out_f32 = a.out_dtype == PKV_F32;
+    p.lse = a.lse;
+    p.num_splits = 1;
+    p.split_keys = std::max(a.max_kv_len, 1);
+    p.checked = (a.flags & PKV_FLAG_CHECKED) != 0;
+    p.err = a.err;
+    p.kv_fp8 = a.fp8;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.scale_stride = a.scale_stride;
+    p.window = a.window;
+    p.num_sinks = a.num_sinks;
+    return from_cuda(pkv::launch_attn_simt_ext(p, a.stream), n);
+}
+
+}  // namespace
+
+size_t paged_attention_fp8_workspace_size(int batch, int max_q_rows, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int max_kv_len,
+                                          int window, int num_sinks, unsigned flags) {
+    return ext_workspace(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len, window, num_sinks,
+                         true, flags);
+}
+
+pkv_status paged_attention_fp8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* k_pool, const void* v_pool, const float* k_scale,
+                               const float* v_scale, int64_t scale_stride, int64_t num_pages,
+                               int page_size, int64_t page_stride, const int32_t* block_table,
+                               int64_t block_table_stride, const int32_t* kv_lens,
+                               const int32_t* q_indptr, const int32_t* q_real, int batch,
+                               int max_q_rows, int max_kv_len, int num_q_heads, int num_kv_heads,
+                               int head_dim, pkv_mask mask, int causal_block, int window,
+                               int num_sinks, float scale, void* out, pkv_dtype out_dtype,
+                               float* lse, void* workspace, size_t workspace_bytes, unsigned flags,
+                               int32_t* err, void* stream) {
+    return ext_attention({"fp8 attention", true, q, k_pool, v_pool, k_scale, v_scale, q_token_stride,
+                          q_head_stride, scale_stride, num_pages, page_stride, block_table_stride, page_size,
+                          block_table, kv_lens, q_indptr, q_real, batch, max_q_rows, max_kv_len, num_q_heads,
+                          num_kv_heads, head_dim, mask, causal_block, window, num_sinks, scale, out, out_dtype,
+                          lse, workspace, workspace_bytes, flags, err, static_cast<cudaStream_t>(stream)});
+}
+
+size_t paged_attention_window_workspace_size(int batch, int max_q_rows, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int max_kv_len,
+                                             int window, int num_sinks, unsigned flags) {
+    return ext_workspace(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len, window, num_sinks,
+                         false, flags);
+}
+
+pkv_status paged_attention_window(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const void* k_pool, const void* v_pool, int64_t num_pages,
+                                  int page_size, int64_t page_stride, const int32_t* block_table,
+                                  int64_t block_table_stride, const int32_t* kv_lens,
+                                  const int32_t* q_indptr, const int32_t* q_real, int batch,
+                                  int max_q_rows, int max_kv_len, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int window, int num_sinks,
+                                  float scale, void* out, pkv_dtype out_dtype, float* lse,
+                                  void* workspace, size_t workspace_bytes, unsigned flags,
+                                  int32_t* err, void* stream) {
+    if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window attention: window %d (at least 1)", window);
+    return ext_attention({"window attention", false, q, k_pool, v_pool, nullptr, nullptr, q_token_stride,
+                          q_head_stride, 0, num_pages, page_stride, block_table_stride, page_size, block_table,
+                          kv_lens, q_indptr, q_real, batch, max_q_rows, max_kv_len, num_q_heads, num_kv_heads,
+                          head_dim, PKV_MASK_CAUSAL, 0, window, num_sinks, scale, out, out_dtype, lse, workspace,
+                          workspace_bytes, flags, err, static_cast<cudaStream_t>(stream)});
+}
+
 pkv_status copy_kv_slots(void* k_pool, void* v_pool, int num_layers, int64_t layer_stride,
                          int64_t num_pages, int page_size, int64_t page_stride, int num_kv_heads,
                          int head_dim, pkv_dtype dtype, const int64_t* src_slots,

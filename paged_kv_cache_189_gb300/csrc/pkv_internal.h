@@ -56,6 +56,27 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t s);
 
+// ---------------------------- quantising append -------------------------------
+struct AppendArgs {
+    const void* src[2];                         // K, V rows
+    int64_t src_token_stride, src_head_stride;  // elements
+    pkv_dtype src_dtype;
+    const int32_t* block_table;
+    int64_t block_table_stride;
+    const int32_t* kv_lens;
+    const int32_t* q_indptr;
+    const int32_t* q_real;
+    int batch, max_q_rows, max_kv_len;
+    int num_kv_heads, head_dim;
+    uint8_t* pool[2];
+    int64_t num_pages, page_stride;  // page_stride in bytes
+    float* scale[2];
+    int64_t scale_stride;
+    bool checked;
+    int32_t* err;
+};
+cudaError_t launch_append_fp8(const AppendArgs& a, cudaStream_t s);
+
 // ---------------------------- pool-to-pool slot copy --------------------------
 struct PlanArgs {
     const int32_t* block_table;
@@ -185,6 +206,13 @@ struct AttnParams {
     const int32_t* grp_tail_lens;   // [rows] keys of the row's tail
     const int32_t* grp_num_groups;  // device scalar
     int grp_max_tokens;             // host bound on the query tokens of one group
+    // paged_attention_fp8 / paged_attention_window: the pools' element type, the
+    // sliding window (0: none) and the first keys that stay visible behind it
+    bool kv_fp8;
+    const float* k_scale;  // [num_pages][scale_stride], fp8 pools only
+    const float* v_scale;
+    int64_t scale_stride;
+    int window, num_sinks;
 };
 
 // Decode kernel (one query row per sequence), split-KV, SIMT; K/V pages
@@ -197,6 +225,9 @@ size_t decode_sched_bytes(int batch, int num_kv_heads, int splits);  // scheduli
 // Generic SIMT kernel: any rows, masks, group sizes; no splits.  A slow
 // cross-check of the fast kernels and the path for shapes they do not cover.
 cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t s);
+
+// The same over bf16 or fp8 pools with a window and sinks.
+cudaError_t launch_attn_simt_ext(const AttnParams& p, cudaStream_t s);
 
 // Grouped mode of the one-tile tensor-core kernel: one CTA per (group, tile of
 // the group's query tokens, K/V head); each row attends to its group's shared

@@ -31,7 +31,9 @@ EXPORTED = ("pkv_status_string", "pkv_last_error", "kv_scatter_slots",
             "paged_attention_workspace_size", "paged_attention", "merge_attn_states",
             "rotate_rows", "paged_attention_no_alloc", "rope_write_kv_paged", "copy_kv_slots",
             "causal_layout", "plan_shared_prefix", "shared_prefix_attention",
-            "shared_prefix_attention_workspace_size", "pkv_plan_attention")
+            "shared_prefix_attention_workspace_size", "pkv_plan_attention", "kv_append_fp8",
+            "paged_attention_fp8_workspace_size", "paged_attention_fp8",
+            "paged_attention_window_workspace_size", "paged_attention_window")
 NO_ALLOC_SCRATCH_BYTES = 32 << 20
 
 _vp, _i64, _i32, _u32, _f32, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
@@ -66,6 +68,16 @@ _SIGNATURES = {
     "shared_prefix_attention": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _vp,
                                        _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                        _i32, _f32, _vp, _i32, _vp, _vp, _sz, _i32, _u32, _vp, _vp]),
+    "kv_append_fp8": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                             _i32, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _i64, _u32, _vp, _vp]),
+    "paged_attention_fp8_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _u32]),
+    "paged_attention_fp8": (_i32, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i64, _vp, _i64,
+                                   _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                   _f32, _vp, _i32, _vp, _vp, _sz, _u32, _vp, _vp]),
+    "paged_attention_window_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _u32]),
+    "paged_attention_window": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _vp, _vp,
+                                      _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp,
+                                      _vp, _sz, _u32, _vp, _vp]),
 }
 
 _lib = None
@@ -363,3 +375,131 @@ def shared_prefix_attention(q, k_pool, v_pool, plan, q_indptr, out, *, max_q_len
         max_q_len, max_group_tokens, max_group_keys, q.shape[1], H, D, scale, _ptr(out), _dtype(out),
         _ptr(lse), _ptr(workspace), ws_bytes, num_splits, flags, _ptr(err), _stream(stream))
     _check("shared_prefix_attention", st)
+
+
+# ----------------------------------------------------------------------------
+def _fp8_geometry(k_pool, v_pool, k_scale, v_scale):
+    """Geometry of two e4m3 pools (float8_e4m3fn or uint8) and their f32 scales
+    ``[num_pages, Hkv]`` (unit head stride)."""
+    n, P, H, D, page_stride = _pool_geometry(k_pool)
+    if k_pool.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_pool.dtype != k_pool.dtype:
+        raise ValueError("8-bit pools must be float8_e4m3fn (or its bytes as uint8)")
+    if v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride():
+        raise ValueError("K and V pools must have the same shape and strides")
+    for sc in (k_scale, v_scale):
+        if sc.dtype != torch.float32 or tuple(sc.shape) != (n, H) or (H > 1 and sc.stride(1) != 1):
+            raise ValueError("scales must be float32 [num_pages, num_kv_heads] with unit head stride")
+    if k_scale.stride(0) != v_scale.stride(0):
+        raise ValueError("K and V scales must have the same page stride")
+    return n, P, H, D, page_stride, max(k_scale.stride(0), H)
+
+
+def _tables(block_table, kv_lens, q_indptr, q_real, batch):
+    """The batch size, after the index tensors' types and layout are checked."""
+    for t in (block_table, kv_lens, q_indptr, q_real):
+        if t is not None and (t.dtype != torch.int32 or (t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1)):
+            raise ValueError("block_table, kv_lens, q_indptr and q_real must be int32 with unit last stride")
+    if batch is None:
+        batch = kv_lens.numel()
+    if (block_table.dim() != 2 or block_table.shape[0] < batch or kv_lens.numel() < batch or
+            q_indptr.numel() < batch + 1 or (q_real is not None and q_real.numel() < batch)):
+        raise ValueError("block_table, kv_lens, q_indptr or q_real too short for the batch")
+    return batch
+
+
+def _on_device(*tensors):
+    """All on the current CUDA device: the launch goes there."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, the current CUDA device is {dev}")
+
+
+def _states(q, out, lse, D):
+    """Checks of packed query rows and the states they produce."""
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1:
+        raise ValueError("q must be bf16 [rows, num_q_heads, head_dim] with unit last stride")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be dense with the shape of q")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be dense float32 [rows, num_q_heads]")
+
+
+def _workspace(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def kv_append_fp8(k_src, v_src, block_table, kv_lens, q_indptr, k_pool, v_pool, k_scale, v_scale, *,
+                  q_real=None, batch=None, max_q_rows, max_kv_len, checked=False, err=None, stream=None):
+    """Quantise this step's rows ``k_src``/``v_src [rows, Hkv, D]`` (bf16, f16
+    or f32, any token/head stride of whole 16 bytes) into e4m3 pools and their
+    per-page, per-head scales, in place (see ``include/pkv.h``)."""
+    n, P, H, D, page_stride, scale_stride = _fp8_geometry(k_pool, v_pool, k_scale, v_scale)
+    if k_src.shape != v_src.shape or k_src.stride() != v_src.stride() or k_src.dtype != v_src.dtype:
+        raise ValueError("k_src and v_src must have the same shape, strides and dtype")
+    if k_src.dim() != 3 or tuple(k_src.shape[1:]) != (H, D) or k_src.stride(2) != 1:
+        raise ValueError("sources must be [rows, num_kv_heads, head_dim] with unit last stride")
+    if k_src.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise ValueError("sources must be bf16, f16 or f32")
+    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
+    _on_device(k_src, v_src, block_table, kv_lens, q_indptr, q_real, k_pool, v_pool, k_scale, v_scale, err)
+    st = lib().kv_append_fp8(
+        _ptr(k_src), _ptr(v_src), _dtype(k_src), k_src.stride(0), k_src.stride(1), _ptr(block_table),
+        block_table.stride(0), _ptr(kv_lens), _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len,
+        H, D, _ptr(k_pool), _ptr(v_pool), n, P, page_stride, _ptr(k_scale), _ptr(v_scale), scale_stride,
+        PKV_FLAG_CHECKED if checked else 0, _ptr(err), _stream(stream))
+    _check("kv_append_fp8", st)
+
+
+def paged_attention_fp8_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len,
+                                       window=0, num_sinks=0, flags=0) -> int:
+    return int(lib().paged_attention_fp8_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim,
+                                                        max_kv_len, window, num_sinks, flags))
+
+
+def paged_attention_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, out, *,
+                        q_real=None, lse=None, batch=None, max_q_rows, max_kv_len, mask="causal",
+                        causal_block=0, window=0, num_sinks=0, scale=0.0, workspace=None, flags=0, err=None,
+                        stream=None):
+    """``paged_attention`` over e4m3 pools with a scale per page and head (as
+    :func:`kv_append_fp8` writes them); ``window`` > 0 limits causal rows to
+    their last ``window`` keys and the first ``num_sinks``."""
+    n, P, H, D, page_stride, scale_stride = _fp8_geometry(k_pool, v_pool, k_scale, v_scale)
+    _states(q, out, lse, D)
+    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
+    _on_device(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err)
+    st = lib().paged_attention_fp8(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+        scale_stride, n, P, page_stride, _ptr(block_table), block_table.stride(0), _ptr(kv_lens),
+        _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len, q.shape[1], H, D, MASKS[mask],
+        causal_block, window, num_sinks, float(scale), _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace),
+        _workspace(workspace), flags, _ptr(err), _stream(stream))
+    _check("paged_attention_fp8", st)
+
+
+def paged_attention_window_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len,
+                                          window, num_sinks=0, flags=0) -> int:
+    return int(lib().paged_attention_window_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads,
+                                                           head_dim, max_kv_len, window, num_sinks, flags))
+
+
+def paged_attention_window(q, k_pool, v_pool, block_table, kv_lens, q_indptr, out, *, window, num_sinks=0,
+                           q_real=None, lse=None, batch=None, max_q_rows, max_kv_len, scale=0.0,
+                           workspace=None, flags=0, err=None, stream=None):
+    """Causal ``paged_attention`` of bf16 pools in which a row sees its last
+    ``window`` keys (its own among them) and the first ``num_sinks``; pages
+    that no row sees are not read."""
+    n, P, H, D, page_stride = _pool_geometry(k_pool)
+    if k_pool.dtype != torch.bfloat16 or v_pool.dtype != torch.bfloat16:
+        raise ValueError("pools must be bf16")
+    if v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride():
+        raise ValueError("K and V pools must have the same shape and strides")
+    _states(q, out, lse, D)
+    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
+    _on_device(q, k_pool, v_pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err)
+    st = lib().paged_attention_window(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pool), _ptr(v_pool), n, P, page_stride, _ptr(block_table),
+        block_table.stride(0), _ptr(kv_lens), _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len,
+        q.shape[1], H, D, window, num_sinks, float(scale), _ptr(out), _dtype(out), _ptr(lse),
+        _ptr(workspace), _workspace(workspace), flags, _ptr(err), _stream(stream))
+    _check("paged_attention_window", st)
