@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(128) attn_simt_ext_kernel(AttnParams p) {
     const int rows = p.q_indptr[b + 1] - r0, nrows = min(rows, p.max_q_rows);
     if (i >= nrows) return;
     const int row = r0 + i;
-    const int qreal = min(p.q_real ? p.q_real[b] : nrows, nrows);
+    const int qreal = max(min(p.q_real ? p.q_real[b] : nrows, nrows), 0);
     int kv_len = p.kv_lens[b];
     if (p.checked && lane == 0 && i == 0 && h == 0 &&
         (kv_len > p.max_kv_len || kv_len < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[b] > rows)))

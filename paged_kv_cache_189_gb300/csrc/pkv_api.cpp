@@ -708,7 +708,36 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
 namespace {
 
 // Workspace of paged_attention_fp8 / paged_attention_window for these bounds.
-size_t ext_workspace(int, int, int, int, int, int, int, int, bool, unsigned) { return 0; }
+size_t ext_workspace(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
+                     bool fp8, unsigned flags) {
+    if (batch <= 0 || max_q_rows <= 0 || Hkv <= 0 || Hq < Hkv || max_kv_len < 0 || window < 0 || num_sinks < 0)
+        return 0;
+    if (flags & PKV_FLAG_SIMT_ONLY) return 0;
+    return pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8,
+                               current_device_sms())
+        .ws_bytes;
+}
+
+// One pool for the few-row kernel: boxes of one head's slots of a page, a whole
+// page of 64- or 128-byte rows (fp8), or 16 slots x 64 columns (bf16).
+pkv_status make_rows_map(CUtensorMap* m, const void* base, bool fp8, int D, int Hkv, int64_t num_pages,
+                         int64_t page_stride) {
+    auto fn = encode_fn();
+    if (!fn) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t esz = fp8 ? 1 : 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), 32,
+                          static_cast<cuuint64_t>(std::max<int64_t>(num_pages, 1))};
+    cuuint64_t strides[3] = {D * esz, static_cast<cuuint64_t>(Hkv) * D * esz,
+                             static_cast<cuuint64_t>(page_stride) * esz};
+    cuuint32_t box[4] = {fp8 ? static_cast<cuuint32_t>(D) : 64u, 1, fp8 ? 32u : 16u, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled(pool) failed: %d", (int)r);
+    return PKV_OK;
+}
 
 // The arguments paged_attention_fp8 and paged_attention_window share.
 struct ExtArgs {
@@ -823,7 +852,16 @@ pkv_status ext_attention(const ExtArgs& a) {
     p.scale_stride = a.scale_stride;
     p.window = a.window;
     p.num_sinks = a.num_sinks;
-    return from_cuda(pkv::launch_attn_simt_ext(p, a.stream), n);
+    if (a.flags & PKV_FLAG_SIMT_ONLY) return from_cuda(pkv::launch_attn_simt_ext(p, a.stream), n);
+
+    const pkv::RowsPlan rp = pkv::plan_attn_rows(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim,
+                                                 a.max_kv_len, a.window, a.num_sinks, a.fp8, current_device_sms());
+    CUtensorMap tk, tv;
+    pkv_status st = make_rows_map(&tk, a.k_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+    if (st != PKV_OK) return st;
+    st = make_rows_map(&tv, a.v_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+    if (st != PKV_OK) return st;
+    return from_cuda(pkv::launch_attn_rows(p, rp, a.workspace, &tk, &tv, a.stream), n);
 }
 
 }  // namespace

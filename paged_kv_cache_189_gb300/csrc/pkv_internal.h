@@ -229,6 +229,21 @@ cudaError_t launch_attn_simt(const AttnParams& p, cudaStream_t s);
 // The same over bf16 or fp8 pools with a window and sinks.
 cudaError_t launch_attn_simt_ext(const AttnParams& p, cudaStream_t s);
 
+// Few query rows per sequence over bf16 or fp8 pools with a window and sinks
+// (mma.sync, TMA-fed rings per warp).  The plan's row tile is 8 * row_tiles
+// (query row, grouped head) pairs; ctas = 0 runs one CTA per unit, else the
+// units' keys are cut into that many shares and a second launch joins them.
+struct RowsPlan {
+    int row_tiles;
+    int64_t tiles;  // row tiles of a sequence at the host bound
+    int ctas;
+    size_t ws_bytes;
+};
+RowsPlan plan_attn_rows(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window,
+                        int num_sinks, bool fp8, int sms);
+cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* workspace, const void* tmap_k,
+                             const void* tmap_v, cudaStream_t s);
+
 // Grouped mode of the one-tile tensor-core kernel: one CTA per (group, tile of
 // the group's query tokens, K/V head); each row attends to its group's shared
 // run and its own tail in one online softmax.
