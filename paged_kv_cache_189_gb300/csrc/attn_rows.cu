@@ -26,15 +26,25 @@
 //  * Weights are rounded once: to bf16 for bf16 pools, and w = 2^(a - M) vs to
 //    f16 for 8-bit ones, M following a + log2(vs), so w stays at or below 2^9
 //    whatever the scales.  Sums, maxima and outputs are f32.
-//  * A warp owns whole chunks of keys (32 in 8 bits, 16 in bf16) with its own
-//    ring of TMA copies and its own softmax state: no barrier between warps
-//    until a unit's end.  8 warps an SM keep 192 KB in flight.
+//  * Per CTA one warp looks up pages and scales ahead, 32 chunks at a time, and
+//    one fills a ring of chunks (32 keys in 8 bits, 16 in bf16) by TMA, so the
+//    chain length -> table -> scale stays off the copies' path; each consumer
+//    warp owns every kWarps-th stage and keeps its own softmax state: no
+//    barrier joins the consumers until a unit's end.  2 CTAs an SM keep 192 KB
+//    in flight.
 //  * Work: a unit is (sequence, K/V head, tile of 8 or 16 rows); its chunks are
-//    the pages its rows see.  All units' chunks form one line that is cut into
-//    equal shares, one per resident CTA; a unit cut between CTAs leaves partial
-//    states that a second launch joins in a fixed order.  The cut follows the
-//    lengths on the device (each CTA sums them itself), so a captured call
-//    replays with other lengths.  Small calls skip the cut: one CTA a unit.
+//    the pages its rows see.  All units' chunks form one line, laid out on the
+//    device (a captured call replays with other lengths), and the line is cut
+//    into pieces: a first, fixed one per CTA, then smaller ones taken by
+//    ticket.  SMs differ in the bandwidth they get (equal shares ended between
+//    84 and 120 us), which the tickets absorb.  A planner clears the ticket and
+//    writes where the pieces start while the CTAs, launched behind it with
+//    programmatic serialisation, find their first piece themselves.
+//  * A unit cut between pieces leaves one partial state per piece; a last launch
+//    joins them in the line's order, so results do not depend on who took which
+//    ticket.  (Joined by the CTA that completes a unit instead, the last CTAs
+//    ended up to 75 us after the others on three sequences of 10^5 keys.)
+//    Small calls skip all this: one CTA a unit.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -46,40 +56,96 @@ namespace pkv {
 namespace {
 
 constexpr int kPage = 32;
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kRingBytes = 24 * 1024;  // per warp
-constexpr int kMinShare = 2 * kWarps;  // chunks a CTA takes at least
-constexpr float kLazy = 8.0f;          // move the reference only past 2^8 growth
-constexpr float kLowScale = -90.0f;    // log2 of the smallest V scale M follows
+constexpr int kRingBytes = 96 * 1024;
+constexpr float kLazy = 8.0f;         // move the reference only past 2^8 growth
+constexpr float kLowScale = -90.0f;   // log2 of the smallest V scale M follows
+constexpr int kDescs = 8;             // segments the look-up may be ahead
+constexpr int kSelfBatch = 256;       // sequences up to which a CTA finds its first piece itself
+constexpr int kBatches = 1;           // batches of 32 chunks it may be ahead
 
 template <int D, bool FP8, int NT>
 struct Cfg {
+    static constexpr int kWarps = NT == 1 ? 6 : 4;       // consumers (their registers set the count)
+    static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kKeys = FP8 ? 32 : 16;          // keys of a chunk
     static constexpr int kTile = kKeys * D * (FP8 ? 1 : 2);
     static constexpr int kStage = 2 * kTile;             // K, V
-    static constexpr int kStages = kRingBytes / kStage;  // 3 (head dim 128), 6 (64)
+    static constexpr int kStages = kRingBytes / kStage;  // 12 (head dim 128), 24 (64)
+    static constexpr int kOwn = kStages / kWarps;        // stages of one consumer
     static constexpr int kRows = 8 * NT;
     static constexpr int kRedStride = D + 4;
-    static constexpr int kRedOff = kWarps * kStages * kStage;          // [warps][4][kRedStride] f32
+    static constexpr int kRedOff = kRingBytes;                              // [warps][4][kRedStride] f32
     static constexpr int kStatOff = kRedOff + kWarps * 4 * kRedStride * 4;  // m, l, l_b: [warps][kRows]
-    static constexpr int kMetaOff = kStatOff + 3 * kWarps * kRows * 4;  // [warps][stages] (ks, vs, key0)
-    static constexpr int kBarOff = kMetaOff + kWarps * kStages * 16;
-    static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
-    static_assert((kBytes + 2048) * kCtasPerSm <= 228 * 1024, "CTAs per SM must fit in shared memory");
-    static_assert(kMetaOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
+    static constexpr int kMetaOff = kStatOff + 3 * kWarps * kRows * 4;      // [stages] (ks, vs, key0)
+    static constexpr int kDescOff = kMetaOff + kStages * 16;
+    static constexpr int kQueueOff = kDescOff + kDescs * 64;          // [batches][32] look-ups
+    static constexpr int kHeadOff = kQueueOff + kBatches * 32 * 16;   // [batches] (chunks, K/V head)
+    static constexpr int kFlagOff = kHeadOff + kBatches * 8;  // set when a consumer's wait gave up
+    // full, empty [stages], dfull, dempty [descs], bfull, bempty [batches]
+    static constexpr int kBarOff = (kFlagOff + 4 + 7) & ~7;
+    static constexpr int kBytes = kBarOff + (2 * kStages + 2 * kDescs + 2 * kBatches) * 8;
+    static_assert(kStages % kWarps == 0, "each consumer owns whole stages");
+    static_assert((kBytes + 1024) * kCtasPerSm <= 228 * 1024, "CTAs per SM must fit in shared memory");
+    static_assert(kMetaOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
 };
 
 struct RowsArgs {
     AttnParams p;
-    int ctas;       // shares of the line (0: one CTA a unit)
+    int ctas;       // CTAs that share the line (0: one CTA a unit)
     int tiles_max;  // row tiles of a sequence at the host bound
-    float* frag_o;    // [ctas][2][rows][D] normalised partial outputs
-    float* frag_lse;  // [ctas][2][rows] (natural log)
-    int4* frag_dir;   // [ctas][2] (sequence, K/V head, row tile, flags)
+    // written by the planner
+    int* ticket;
+    int2* cuts;         // [units] first slot and number of its partial states; 0: none
+    int* seq_at;        // [batch + 1] the line's place of each sequence's first unit, and its length
+    int4* starts;       // [pieces] (sequence, K/V head, place in the head's units) each starts with
+    // partial states: piece i of unit u in slot i + u (both grow along the line)
+    float* frag_o;      // [pieces + units][rows][D] normalised outputs
+    float* frag_lse;    // [pieces + units][rows] log2 of the sums
 };
-constexpr int kFragValid = 1, kFragStarts = 2, kFragEnds = 4;
+
+// The cut of a line of T places: `first` pieces of together A1, then pieces of
+// q1 up to A2 and of q2 up to T.
+struct Line {
+    int T, A1, A2, first, size, longer, n1, n2, q1, q2;
+    __device__ __forceinline__ Line(int total, int ctas) {
+        // 70 % fixed, 20 % in tenths and 10 % in twentieths of a CTA's average
+        // share; pieces of at least 12 and 6 chunks, fixed ones of at least 8
+        T = total;
+        A1 = T / 10 * 7;
+        A2 = T / 10 * 9;
+        first = min(max(A1 / 8, 1), ctas);
+        size = A1 / first;
+        longer = A1 - size * first;  // the first so many pieces have one more
+        q1 = max((T / 10 + ctas - 1) / ctas, 12);
+        q2 = max((T / 20 + ctas - 1) / ctas, 6);
+        n1 = (A2 - A1 + q1 - 1) / q1;
+        n2 = (T - A2 + q2 - 1) / q2;
+    }
+    __device__ __forceinline__ int pieces() const { return first + n1 + n2; }
+    // places [from, to) of piece i
+    __device__ __forceinline__ void piece(int i, int& from, int& to) const {
+        if (i < first) {
+            from = i * size + min(i, longer);
+            to = from + size + (i < longer ? 1 : 0);
+        } else if (i < first + n1) {
+            from = A1 + (i - first) * q1;
+            to = min(from + q1, A2);
+        } else {
+            from = min(A2 + (i - first - n1) * q2, T);
+            to = min(from + q2, T);
+        }
+    }
+    __device__ __forceinline__ int piece_of(int at) const {
+        if (at < A1) {
+            const int x = longer * (size + 1);
+            return at < x ? at / (size + 1) : longer + (at - x) / size;
+        }
+        if (at < A2) return first + (at - A1) / q1;
+        return first + n1 + (at - A2) / q2;
+    }
+    static int most(int ctas) { return 6 * ctas + 8; }  // pieces, whatever T
+};
 
 // ---------------------------------------------------------------------------
 // Geometry
@@ -130,7 +196,7 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& s, int m
 template <int ROWS, int KEYS>
 struct Walk {
     int b, kvh, mt, at;  // next unit, and the place in it
-    int64_t left;        // places of the share still to come
+    int left;            // places of the piece still to come
     // the current segment
     Seq s;
     Span u;
@@ -141,7 +207,6 @@ struct Walk {
         while (left > 0 && b < p.batch) {
             s = sequence<ROWS>(p, b, G);
             if (mt >= s.tiles) {
-                at = 0;
                 mt = 0;
                 if (s.tiles == 0 || ++kvh == p.num_kv_heads) {
                     kvh = 0;
@@ -151,11 +216,16 @@ struct Walk {
             }
             u = span_of<ROWS, KEYS>(p, s, mt, G);
             const int places = max(u.n, 1);
+            if (at >= places) {  // a start counted from the head's first tile
+                at -= places;
+                ++mt;
+                continue;
+            }
             sb = b;
             skvh = kvh;
             smt = mt;
             ps = at;
-            pe = static_cast<int>(min(static_cast<int64_t>(places), at + left));
+            pe = min(places, at + left);
             starts = ps == 0;
             ends = pe == places;
             left -= pe - ps;
@@ -207,6 +277,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -219,65 +290,75 @@ struct State {
     float o[NT][D / 16][4];
 };
 
-// What a chunk needs of its segment.
-template <int NT>
-struct RowInfo {
-    int lim[NT][2], lo[NT][2];  // of this lane's rows
-    int all_end, all_lo;        // keys [all_lo, all_end) are visible to every real row
-    int any_lo, any_end, sinks; // keys outside [any_lo, any_end) and [0, sinks) to none
-    float fq[NT][2];            // score factor of this lane's rows
+// A segment as the look-up hands it to the consumers.
+struct __align__(16) Desc {
+    int r0, nrows, qreal, kv_len, lo, hi;  // hi, lo: of the unit's rows together
+    int kvh, row0;                         // K/V head, first (row, head) of the tile
+    int n;                                 // chunks; -1: no more segments
+    int frag;                              // slot of the partial state; -1: the whole unit is here
+    int all_lo, all_end;                   // keys [all_lo, all_end) are visible to every real row
+    int pad[4];
 };
+static_assert(sizeof(Desc) == 64, "descriptor size");
+// The keys [lo, lim) that token tok of the segment's sequence sees (and the sinks below lo).
+__device__ __forceinline__ void row_range(const AttnParams& p, const Desc& s, int tok, int& lo, int& lim) {
+    lim = tok < s.qreal ? row_limit(p, tok, s.qreal, s.kv_len) : 0;
+    lo = p.window > 0 ? s.kv_len - s.qreal + tok - p.window + 1 : 0;
+}
 
 // One chunk: scores, weights and the output update.  MASKED: some key of it is
 // hidden from some row.
 template <int D, bool FP8, int NT, bool MASKED>
 __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf)[NT][D / 16][2],
-                                           const RowInfo<NT>& ri, uint32_t kb, uint32_t vb, float ks, float vs,
-                                           int key0, int lane) {
+                                           const float (&fq)[NT][2], const AttnParams& p, const Desc& ds, int G,
+                                           uint32_t kb, uint32_t vb, float ks, float vs, int key0, int lane) {
     using C = Cfg<D, FP8, NT>;
     constexpr int MI = C::kKeys / 16;
     const int g = lane >> 2, t = lane & 3;
-    // ---- S^T = K Q^T
-    float s[MI][NT][4];
+    // ---- S^T = K Q^T, the steps of two independent accumulators in turn
+    constexpr int SA = FP8 ? MI : 2;  // accumulators: 16 keys each (8 bits), every other step (bf16)
+    float s[SA][NT][4];
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
+    for (int x = 0; x < SA; ++x)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mi][j][e] = 0.f;
-        const int r0 = 16 * mi + g;  // this lane's keys r0 and r0 + 8
-        if constexpr (FP8) {
-            constexpr int kLoads = D / 64;
-            constexpr int kRowB = D;
-            const uint32_t x = D == 128 ? ((2 * t) ^ g) << 4 : (t ^ ((r0 >> 1) & 3)) << 4;
-            const uint32_t a0 = kb + r0 * kRowB + x;
+            for (int e = 0; e < 4; ++e) s[x][j][e] = 0.f;
+    if constexpr (FP8) {
+        // this lane's keys: g, g + 8, g + 16, g + 24
+        const uint32_t a0 = kb + g * D + (D == 128 ? ((2 * t) ^ g) << 4 : (t ^ ((g >> 1) & 3)) << 4);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const uint4 u = lds128(a0 ^ (i << 4)), v = lds128((a0 ^ (i << 4)) + 8 * kRowB);
-                const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < D / 64; ++i) {
+            uint4 w[2 * MI];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+            for (int r = 0; r < 2 * MI; ++r) w[r] = lds128((a0 ^ (i << 4)) + r * 8 * D);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
                     uint32_t a[4];
-                    widen4(uw[k], a[0], a[2]);
-                    widen4(vw[k], a[1], a[3]);
+                    widen4(word(w[2 * mi], k), a[0], a[2]);
+                    widen4(word(w[2 * mi + 1], k), a[1], a[3]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) mma<FP8>(s[mi][j], a, qf[j][4 * i + k][0], qf[j][4 * i + k][1]);
                 }
-            }
-        } else {
-            const uint32_t a0 = kb + r0 * 128 + (((2 * t) ^ g) << 4);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t ad = (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
-                const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
-                const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma<FP8>(s[mi][j], x0, qf[j][2 * i][0], qf[j][2 * i][1]);
-                    mma<FP8>(s[mi][j], x1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
-                }
-            }
         }
+    } else {
+        const uint32_t a0 = kb + g * 128 + (((2 * t) ^ g) << 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t ad = (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
+            const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
+            const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma<FP8>(s[0][j], x0, qf[j][2 * i][0], qf[j][2 * i][1]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma<FP8>(s[1][j], x1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
     }
     // ---- weights
     float lv = 0.f;  // log2 of the V scale, rounded down
@@ -291,7 +372,9 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
         float ref[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float f = FP8 ? ri.fq[j][e] * ks : ri.fq[j][e];
+            const float f = FP8 ? fq[j][e] * ks : fq[j][e];
+            int lim = 0, lo = 0;
+            if constexpr (MASKED) row_range(p, ds, (ds.row0 + 8 * j + 2 * t + e) / G, lo, lim);
             float mx = -INFINITY;
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi)
@@ -300,7 +383,7 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
                     float x = s[mi][j][2 * hh + e] * f;
                     if constexpr (MASKED) {
                         const int key = key0 + 16 * mi + 8 * hh + g;
-                        if (!(key < ri.lim[j][e] && (key >= ri.lo[j][e] || key < ri.sinks))) x = -INFINITY;
+                        if (!(key < lim && (key >= lo || key < p.num_sinks))) x = -INFINITY;
                     }
                     s[mi][j][2 * hh + e] = x;
                     mx = fmaxf(mx, x);
@@ -358,7 +441,7 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int key = key0 + 8 * k + 2 * t + e;
-                if (key < ri.any_end && (key >= ri.any_lo || key < ri.sinks)) keep |= 0xffffu << (16 * e);
+                if (key < ds.hi && (key >= ds.lo || key < p.num_sinks)) keep |= 0xffffu << (16 * e);
             }
             vm[k] = keep;
         }
@@ -368,22 +451,25 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
         const uint32_t x = D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4;
         const uint32_t a0 = vb + lane * kRowB + x;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            uint32_t r[4];
-            ldmatrix_x4_trans(r, a0 ^ (c << 4));
+        for (int c0 = 0; c0 < D / 16; c0 += 2) {
+            uint32_t r[2][4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t a[4];
+            for (int c = 0; c < 2; ++c) ldmatrix_x4_trans(r[c], a0 ^ ((c0 + c) << 4));
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t w = r[2 * k + q];
-                    if constexpr (MASKED) w &= vm[2 * k + q];
-                    // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
-                    widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w = r[c][2 * k + q];
+                        if constexpr (MASKED) w &= vm[2 * k + q];
+                        // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
+                        widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c0 + c], a, pb[j][k][0], pb[j][k][1]);
                 }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c], a, pb[j][k][0], pb[j][k][1]);
-            }
         }
     } else {
         const int row = (lane & 7) + ((lane >> 4) << 3);
@@ -404,40 +490,42 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
     }
 }
 
-// Query rows 8j + g of a tile into the score product's B operand, in the order
-// the K loads give the dimensions; returns the factor that undoes the row's
-// scaling (1 for bf16 pools).
+// A lane's part of a query row, in the order the K loads give the dimensions.
 template <int D, bool FP8>
-__device__ __forceinline__ float load_q(const AttnParams& p, const __nv_bfloat16* q, bool exists, int t,
-                                        uint32_t (&f)[D / 16][2]) {
-    uint4 v[D / 32];
+__device__ __forceinline__ void fetch_q_row(const __nv_bfloat16* q, bool exists, int t, uint4 (&v)[D / 32]) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
         // 8-bit: D / 4 elements from t D / 4 on; bf16: 16 of each 64 from 16 t on
         const int at = FP8 ? t * (D / 4) + 8 * i : (i >> 1) * 64 + t * 16 + (i & 1) * 8;
         v[i] = exists ? __ldg(reinterpret_cast<const uint4*>(q + at)) : make_uint4(0u, 0u, 0u, 0u);
     }
+}
+// The same as the score product's B operand; returns the factor that undoes
+// the row's scaling (1 for bf16 pools).
+template <int D, bool FP8>
+__device__ __forceinline__ float pack_q(const uint4 (&v)[D / 32], uint32_t (&f)[D / 16][2]) {
     float undo = 1.f;
     if constexpr (FP8) {
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max((w[k] >> 7) & 255u, (w[k] >> 23) & 255u));
-        }
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = word(v[i], k);
+                top = max(top, max((w >> 7) & 255u, (w >> 23) & 255u));
+            }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = max(top, 9u);
         const float up = __uint_as_float((262u - top) << 23);  // the largest exponent to 2^8
         undo = __uint_as_float((top - 8u) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                f[2 * i + (k >> 1)][k & 1] = pack_f16x2(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
-        }
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = word(v[i], k);
+                f[2 * i + (k >> 1)][k & 1] = pack_f16x2(bf16lo(w) * up, bf16hi(w) * up);
+            }
     } else {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -450,435 +538,649 @@ __device__ __forceinline__ float load_q(const AttnParams& p, const __nv_bfloat16
     return undo;
 }
 
+struct Look {
+    int page, key0;
+    float ks, vs;
+};
+
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ RowsArgs a) {
     using C = Cfg<D, FP8, NT>;
     using W = Walk<C::kRows, C::kKeys>;
-    constexpr int S = C::kStages;
+    constexpr int S = C::kStages, NW = C::kWarps;
     const AttnParams& p = a.p;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long scan[kWarps];
-    __shared__ int begin[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.num_q_heads / p.num_kv_heads, Hkv = p.num_kv_heads;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
 
     if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle needs 1024-byte aligned tiles
         if (threadIdx.x == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
         return;
     }
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * S;
-    float4* meta = reinterpret_cast<float4*>(smem + C::kMetaOff) + warp * S;
-    uint8_t* ring = smem + warp * S * C::kStage;
-    if (lane == 0) {
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-        for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+    uint64_t* empty = full + S;
+    uint64_t* dfull = empty + S;
+    uint64_t* dempty = dfull + kDescs;
+    uint64_t* bfull = dempty + kDescs;
+    uint64_t* bempty = bfull + kBatches;
+    float4* meta = reinterpret_cast<float4*>(smem + C::kMetaOff);
+    Desc* desc = reinterpret_cast<Desc*>(smem + C::kDescOff);
+    Look* queue = reinterpret_cast<Look*>(smem + C::kQueueOff);
+    int2* head = reinterpret_cast<int2*>(smem + C::kHeadOff);
+    if (threadIdx.x == 0) {
+        *reinterpret_cast<int*>(smem + C::kFlagOff) = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kDescs; ++s) {
+            mbar_init(&dfull[s], 1);
+            mbar_init(&dempty[s], NW);
+        }
+        for (int s = 0; s < kBatches; ++s) {
+            mbar_init(&bfull[s], 32);
+            mbar_init(&bempty[s], 32);
+        }
         fence_mbar_init();
     }
+    __syncthreads();
 
-    // ---- this CTA's share
-    W cw;
-    if (a.ctas == 0) {
-        const int x = blockIdx.x;
-        cw.mt = x % a.tiles_max;
-        cw.kvh = (x / a.tiles_max) % Hkv;
-        cw.b = x / a.tiles_max / Hkv;
-        cw.at = 0;
-        const Seq s = sequence<C::kRows>(p, cw.b, G);
-        if (cw.mt >= s.tiles) return;
-        cw.left = max(span_of<C::kRows, C::kKeys>(p, s, cw.mt, G).n, 1);
-    } else {
-        auto weight = [&](int b) {  // places of one K/V head
-            const Seq s = sequence<C::kRows>(p, b, G);
-            long long w = 0;
-            for (int mt = 0; mt < s.tiles; ++mt) w += max(span_of<C::kRows, C::kKeys>(p, s, mt, G).n, 1);
-            return w;
+    if (warp == NW) {
+        // ============================ look-up ===============================
+        // The first piece of a small batch is found here, from the lengths, while
+        // the planner (launched before this grid, with programmatic
+        // serialisation) still runs; what it wrote is read behind await_planner.
+        // (One small loop for both passes: at a launch's start, straight-line
+        // code costs its instruction fetches.)
+        if (a.ctas > 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join, behind this grid
+        bool planned = false;
+        auto await_planner = [&] {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            planned = true;
         };
-        const int per = (p.batch + kThreads - 1) / kThreads;
-        const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += weight(b) * Hkv;
-        long long incl = mine;
+        W w;
+        w.b = w.kvh = w.mt = w.at = w.left = 0;
+        int T = 0, piece = blockIdx.x;
+        const bool self = p.batch <= kSelfBatch;
+        if (a.ctas > 0 && !self) {
+            await_planner();
+            T = __ldcg(a.seq_at + p.batch);
+        } else if (a.ctas > 0) {
+            int at = -1;  // pass 0: the line's length; pass 1: the sequence that holds its place `at`
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                int base = 0;
+#pragma unroll 1
+                for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                    int per_head = 0;
+                    if (b0 + lane < p.batch) {
+                        const Seq s = sequence<C::kRows>(p, b0 + lane, G);
+#pragma unroll 1
+                        for (int mt = 0; mt < s.tiles; ++mt)
+                            per_head += max(span_of<C::kRows, C::kKeys>(p, s, mt, G).n, 1);
+                    }
+                    int incl = per_head * Hkv;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        long long before = incl - mine, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-        const long long shares = min(static_cast<long long>(a.ctas), max(total / kMinShare, 1ll));
-        const long long c = blockIdx.x;
-        const long long from = c < shares ? total * c / shares : total;
-        const long long to = c < shares ? total * (c + 1) / shares : total;
-        if (from >= to) {
-            if (threadIdx.x < 2) a.frag_dir[c * 2 + threadIdx.x] = make_int4(0, 0, 0, 0);
-            return;
-        }
-        if (from >= before && from < before + mine) {
-            long long rem = from - before;
-            int b = b0;
-            for (; b < b1; ++b) {
-                const long long w = weight(b) * Hkv;
-                if (rem < w) break;
-                rem -= w;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += y;
+                    }
+                    const uint32_t ends = __ballot_sync(0xffffffffu, pass == 1 && base + incl > at);
+                    if (ends) {  // the first sequence to end behind it
+                        const int l = __ffs(ends) - 1;
+                        per_head = __shfl_sync(0xffffffffu, per_head, l);
+                        at -= base + __shfl_sync(0xffffffffu, incl, l) - per_head * Hkv;
+                        w.b = b0 + l;
+                        w.kvh = at / per_head;
+                        w.at = at - w.kvh * per_head;
+                        break;
+                    }
+                    base += __shfl_sync(0xffffffffu, incl, 31);
+                }
+                if (pass == 0) {
+                    T = base;
+                    const Line line(T, a.ctas);
+                    if (piece >= line.first) break;
+                    int to;
+                    line.piece(piece, at, to);
+                    w.left = to - at;
+                    if (w.left == 0) break;
+                }
             }
-            const long long w = weight(b);
-            begin[0] = b;
-            begin[1] = static_cast<int>(rem / w);
-            rem %= w;
-            const Seq s = sequence<C::kRows>(p, b, G);
-            int mt = 0;
-            for (;; ++mt) {
-                const int n = max(span_of<C::kRows, C::kKeys>(p, s, mt, G).n, 1);
-                if (rem < n) break;
-                rem -= n;
-            }
-            begin[2] = mt;
-            begin[3] = static_cast<int>(rem);
+        } else {
+            const int x = blockIdx.x;
+            w.mt = x % a.tiles_max;
+            w.kvh = (x / a.tiles_max) % Hkv;
+            w.b = x / a.tiles_max / Hkv;
+            w.left = w.mt < sequence<C::kRows>(p, w.b, G).tiles ? 0x7fffffff : 0;
         }
-        __syncthreads();
-        cw.b = begin[0];
-        cw.kvh = begin[1];
-        cw.mt = begin[2];
-        cw.at = begin[3];
-        cw.left = to - from;
+        const Line line(T, max(a.ctas, 1));
+        const int pieces = line.pieces();
+        int nseg = 0, nbatch = 0;
+        bool alive = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+        for (bool fixed = true; alive; fixed = false) {
+            // ---- the next piece, by ticket
+            if (a.ctas == 0 && !fixed) break;
+            if (a.ctas > 0 && !(fixed && self && piece < line.first)) {
+                if (!planned) await_planner();
+                if (!fixed || piece >= line.first) {
+                    int tk = 0;
+                    if (lane == 0) tk = atomicAdd(a.ticket, 1);
+                    piece = line.first + __shfl_sync(0xffffffffu, tk, 0);
+                }
+                if (piece >= pieces) break;
+                int from, to;
+                line.piece(piece, from, to);
+                const int4 at = __ldcg(a.starts + piece);
+                w.b = at.x;
+                w.kvh = at.y;
+                w.mt = 0;
+                w.at = at.z;
+                w.left = to - from;
+            }
+            // ---- its segments
+            while (alive && w.next(p, G)) {
+                const int ds = nseg % kDescs;
+                if (nseg >= kDescs && !wait(&dempty[ds], (nseg / kDescs - 1) & 1)) {
+                    alive = false;
+                    break;
+                }
+                if (lane == 0) {
+                    Desc d;
+                    d.r0 = w.s.r0;
+                    d.nrows = w.s.nrows;
+                    d.qreal = w.s.qreal;
+                    d.kv_len = w.s.kv_len;
+                    d.lo = w.u.lo;
+                    d.hi = w.u.hi;
+                    d.kvh = w.skvh;
+                    d.row0 = w.smt * C::kRows;
+                    d.n = max(w.pe - w.ps, 0);
+                    {
+                        const int tf = d.row0 / G, tl = min((d.row0 + C::kRows - 1) / G, d.qreal - 1);
+                        d.all_end = tf < d.qreal ? row_limit(p, tf, d.qreal, d.kv_len) : 0;
+                        d.all_lo = p.window > 0 ? max(0, d.kv_len - d.qreal + tl - p.window + 1) : 0;
+                    }
+                    d.frag = w.starts && w.ends ? -1 : piece + (w.sb * Hkv + w.skvh) * a.tiles_max + w.smt;
+                    desc[ds] = d;
+                    mbar_arrive(&dfull[ds]);
+                    if (p.checked && w.starts && w.skvh == 0 && w.smt == 0) {
+                        const int rows = p.q_indptr[w.sb + 1] - w.s.r0, kv = p.kv_lens[w.sb];
+                        if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[w.sb] > rows))
+                            set_err(p.err, PKV_ERRBIT_LEN);
+                    }
+                }
+                __syncwarp();
+                ++nseg;
+                if (a.ctas == 0) w.left = 0;  // its one unit
+                for (int c0 = w.ps; c0 < w.pe; c0 += 32) {
+                    // pages and scales of the next 32 chunks, one a lane
+                    const int bs = nbatch % kBatches;
+                    if (nbatch >= kBatches && !wait(&bempty[bs], (nbatch / kBatches - 1) & 1)) {
+                        alive = false;
+                        break;
+                    }
+                    const int i = c0 + lane;
+                    Look k;
+                    k.key0 = (i < w.u.nsc ? i : w.u.loc + i - w.u.nsc) * C::kKeys;
+                    k.page = static_cast<int>(p.num_pages);  // outside the tensor: the copy fills zeros
+                    k.ks = k.vs = 0.f;
+                    if (i < w.pe) {
+                        const int x = p.block_table[w.sb * p.block_table_stride + k.key0 / kPage];
+                        if (x >= 0 && x < p.num_pages) {
+                            k.page = x;
+                            if constexpr (FP8) {
+                                k.ks = __ldg(p.k_scale + x * p.scale_stride + w.skvh);
+                                k.vs = __ldg(p.v_scale + x * p.scale_stride + w.skvh);
+                            }
+                        } else if (p.checked) {
+                            set_err(p.err, PKV_ERRBIT_PAGE);
+                        }
+                    }
+                    queue[bs * 32 + lane] = k;
+                    if (lane == 0) head[bs] = make_int2(min(32, w.pe - c0), w.skvh);
+                    mbar_arrive(&bfull[bs]);
+                    ++nbatch;
+                }
+            }
+        }
+        if (!alive && lane == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        // the end marks (where a wait gave up, the readers' own waits run out too)
+        const int bs = nbatch % kBatches, ds = nseg % kDescs;
+        if (nbatch < kBatches || wait(&bempty[bs], (nbatch / kBatches - 1) & 1)) {
+            if (lane == 0) head[bs] = make_int2(-1, 0);
+            mbar_arrive(&bfull[bs]);
+        }
+        if (nseg < kDescs || wait(&dempty[ds], (nseg / kDescs - 1) & 1)) {
+            if (lane == 0) {
+                desc[ds].n = -1;
+                mbar_arrive(&dfull[ds]);
+            }
+        }
+        return;
+    }
+    if (warp == NW + 1) {
+        // ============================= copies ===============================
+        if (lane == 0) {
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+        }
+        int issued = 0;
+        bool alive = true;
+        for (int nb = 0; alive; ++nb) {
+            const int bs = nb % kBatches;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bfull[bs], (nb / kBatches) & 1))) {
+                alive = false;
+                break;
+            }
+            const int2 h = head[bs];
+            if (h.x < 0) break;
+            const Look k = queue[bs * 32 + lane];
+            mbar_arrive(&bempty[bs]);
+            for (int l = 0; l < h.x; ++l, ++issued) {
+                const int st = issued % S;
+                if (issued >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (issued / S - 1) & 1))) {
+                    alive = false;
+                    break;
+                }
+                if (lane == l) {
+                    uint8_t* kd = smem + st * C::kStage;
+                    uint8_t* vd = kd + C::kTile;
+                    meta[st] = make_float4(k.ks, k.vs, __int_as_float(k.key0), 0.f);
+                    mbar_arrive_expect_tx(&full[st], C::kStage);
+                    if constexpr (FP8) {
+                        tma_load_4d(kd, &tm_k, &full[st], 0, h.y, 0, k.page);
+                        tma_load_4d(vd, &tm_v, &full[st], 0, h.y, 0, k.page);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x) {
+                            tma_load_4d(kd + x * (C::kKeys * 128), &tm_k, &full[st], x * 64, h.y, k.key0 % kPage, k.page);
+                            tma_load_4d(vd + x * (C::kKeys * 128), &tm_v, &full[st], x * 64, h.y, k.key0 % kPage, k.page);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!alive && lane == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        // do not leave with copies into this CTA's shared memory in flight
+        for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&full[j % S], (j / S) & 1);
+        return;
     }
 
-    // ---- the warp's copies: every kWarps-th chunk of every segment, in order,
-    // S ahead of what it consumes
-    W iw = cw;
-    iw.ps = iw.pe = 0;
-    int ipos = 0, ibase = 0;  // next chunk to copy; chunk of lane 0's cached page
-    int my_page = 0;
-    float my_ks = 1.f, my_vs = 1.f;
-    int issued = 0;
-    bool more = true;
-    auto key_of = [](const W& w, int i) { return (i < w.u.nsc ? i : w.u.loc + i - w.u.nsc) * C::kKeys; };
-    auto look_up = [&] {  // pages and scales of this warp's next 32 chunks, one a lane
-        ibase = ipos;
-        const int i = ipos + kWarps * lane;
-        my_page = static_cast<int>(p.num_pages);  // outside the tensor: the copy fills zeros
-        my_ks = my_vs = 0.f;
-        if (i < iw.pe) {
-            const int page = p.block_table[iw.sb * p.block_table_stride + key_of(iw, i) / kPage];
-            if (page >= 0 && page < p.num_pages) {
-                my_page = page;
-                if constexpr (FP8) {
-                    my_ks = __ldg(p.k_scale + page * p.scale_stride + iw.skvh);
-                    my_vs = __ldg(p.v_scale + page * p.scale_stride + iw.skvh);
-                }
-            } else if (p.checked) {
-                set_err(p.err, PKV_ERRBIT_PAGE);
-            }
-        }
-    };
-    auto issue = [&] {
-        while (more && ipos >= iw.pe) {
-            more = iw.next(p, G);
-            if (more) {
-                ipos = iw.ps + warp;
-                if (ipos < iw.pe) look_up();
-            }
-        }
-        if (!more) return;
-        if (ipos - ibase >= 32 * kWarps) look_up();
-        const int l = (ipos - ibase) / kWarps;
-        const int page = __shfl_sync(0xffffffffu, my_page, l);
-        const float ks = __shfl_sync(0xffffffffu, my_ks, l), vs = __shfl_sync(0xffffffffu, my_vs, l);
-        if (lane == 0) {
-            const int st = issued % S, key0 = key_of(iw, ipos);
-            uint8_t* kd = ring + st * C::kStage;
-            uint8_t* vd = kd + C::kTile;
-            meta[st] = make_float4(ks, vs, __int_as_float(key0), 0.f);
-            mbar_arrive_expect_tx(&bars[st], C::kStage);
-            if constexpr (FP8) {
-                tma_load_4d(kd, &tm_k, &bars[st], 0, iw.skvh, 0, page);
-                tma_load_4d(vd, &tm_v, &bars[st], 0, iw.skvh, 0, page);
-            } else {
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    tma_load_4d(kd + h * (C::kKeys * 128), &tm_k, &bars[st], h * 64, iw.skvh, key0 % kPage, page);
-                    tma_load_4d(vd + h * (C::kKeys * 128), &tm_v, &bars[st], h * 64, iw.skvh, key0 % kPage, page);
-                }
-            }
-        }
-        ipos += kWarps;
-        ++issued;
-    };
-    __syncwarp();
-    for (int s = 0; s < S; ++s) issue();
-
-    // ---- segments
+    // ============================== consumers ===============================
     const int g = lane >> 2, t = lane & 3;
     float* red = reinterpret_cast<float*>(smem + C::kRedOff);
     float* red_m = reinterpret_cast<float*>(smem + C::kStatOff);
-    float* red_l = red_m + kWarps * C::kRows;
-    float* red_lb = red_l + kWarps * C::kRows;
-    const uint32_t ring_u = smem_u32(ring);
-    int consumed = 0;
-    bool dead = false;
-    int4 dir0 = make_int4(0, 0, 0, 0), dir1 = dir0;
-    int nseg = 0;
-    for (; cw.next(p, G); ++nseg) {
-        const int R0 = cw.smt * C::kRows;
-        const Seq& s = cw.s;
-        if (p.checked && threadIdx.x == 0 && cw.starts && cw.skvh == 0 && cw.smt == 0) {
-            const int rows = p.q_indptr[cw.sb + 1] - s.r0, kv = p.kv_lens[cw.sb];
-            if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[cw.sb] > rows))
-                set_err(p.err, PKV_ERRBIT_LEN);
-        }
-        RowInfo<NT> ri;
-        uint32_t qf[NT][D / 16][2];
+    float* red_l = red_m + NW * C::kRows;
+    float* red_lb = red_l + NW * C::kRows;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
+    const uint32_t ring_u = smem_u32(smem);
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"r"(NW * 32) : "memory"); };
+    int own = 0;      // stage of the warp's next chunk among its own, and its phase
+    uint32_t phase = 0;
+    int turn = 0;     // consumer whose turn the segment's first chunk is
+    uint4 raw[NT][D / 32];
+    bool have = false;  // the segment's query rows are in raw
+    auto fetch_q = [&](const Desc& s) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int R = R0 + 8 * j + g;
-            const int tok = R / G, h = cw.skvh * G + R % G;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                                     static_cast<int64_t>(s.r0 + tok) * p.q_token_stride +
-                                     static_cast<int64_t>(h) * p.q_head_stride;
-            const float undo = load_q<D, FP8>(p, q, tok < s.nrows, t, qf[j]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ri.fq[j][e] = p.scale_log2;
-                if constexpr (FP8) ri.fq[j][e] *= __shfl_sync(0xffffffffu, undo, (2 * t + e) * 4);
-                const int tk = (R0 + 8 * j + 2 * t + e) / G;
-                ri.lim[j][e] = tk < s.qreal ? row_limit(p, tk, s.qreal, s.kv_len) : 0;
-                ri.lo[j][e] = p.window > 0 ? s.kv_len - s.qreal + tk - p.window + 1 : 0;
-            }
+            const int R = s.row0 + 8 * j + g;
+            const int tok = R / G, h = s.kvh * G + R % G;
+            fetch_q_row<D, FP8>(static_cast<const __nv_bfloat16*>(p.q) +
+                                    static_cast<int64_t>(s.r0 + tok) * p.q_token_stride +
+                                    static_cast<int64_t>(h) * p.q_head_stride,
+                                tok < s.nrows, t, raw[j]);
         }
-        {
-            const int tf = R0 / G, tl = min((R0 + C::kRows - 1) / G, s.qreal - 1);
-            ri.all_end = tf < s.qreal ? row_limit(p, tf, s.qreal, s.kv_len) : 0;
-            ri.all_lo = p.window > 0 ? max(0, s.kv_len - s.qreal + tl - p.window + 1) : 0;
-            ri.any_lo = cw.u.lo;
-            ri.any_end = cw.u.hi;
-            ri.sinks = p.num_sinks;
-        }
+    };
+    for (int nseg = 0;; ++nseg) {
+        const int ds = nseg % kDescs;
+        bool dead = !__all_sync(0xffffffffu, mbar_wait(&dfull[ds], (nseg / kDescs) & 1));
+        const Desc& s = desc[ds];
+        const bool run = !dead && s.n >= 0;
+        const int R0 = s.row0;
         State<D, NT> st;
+        if (run) {
+            if (!have) fetch_q(s);
+            float fq[NT][2];  // score factors of this lane's rows
+            uint32_t qf[NT][D / 16][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+            for (int j = 0; j < NT; ++j) {
+                const float undo = pack_q<D, FP8>(raw[j], qf[j]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                st.m[j][e] = -INFINITY;
-                st.l[j][e] = st.lb[j][e] = 0.f;
-            }
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st.o[j][c][e] = 0.f;
-        }
-        for (int pos = cw.ps + warp; pos < cw.pe && !dead; pos += kWarps) {
-            const int sg = consumed % S;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[sg], (consumed / S) & 1))) {
-                if (lane == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
-                dead = true;
-                break;
-            }
-            const float4 me = meta[sg];
-            const int key0 = __float_as_int(me.z);
-            const uint32_t kb = ring_u + sg * C::kStage;
-            const bool whole = key0 + C::kKeys <= ri.all_end &&
-                               (key0 >= ri.all_lo || key0 + C::kKeys <= ri.sinks);
-            if (whole) chunk_step<D, FP8, NT, false>(st, qf, ri, kb, kb + C::kTile, me.x, me.y, key0, lane);
-            else chunk_step<D, FP8, NT, true>(st, qf, ri, kb, kb + C::kTile, me.x, me.y, key0, lane);
-            __syncwarp();
-            ++consumed;
-            issue();
-        }
-        // ---- join the warps' states, four rows at a time
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    st.l[j][e] += __shfl_xor_sync(0xffffffffu, st.l[j][e], o);
-                    if constexpr (!FP8) st.lb[j][e] += __shfl_xor_sync(0xffffffffu, st.lb[j][e], o);
-                }
-                if (g == 0) {
-                    const int r = warp * C::kRows + 8 * j + 2 * t + e;
-                    red_m[r] = st.m[j][e];
-                    red_l[r] = st.l[j][e];
-                    if constexpr (!FP8) red_lb[r] = st.lb[j][e];
+                for (int e = 0; e < 2; ++e) {
+                    fq[j][e] = p.scale_log2;
+                    if constexpr (FP8) fq[j][e] *= __shfl_sync(0xffffffffu, undo, (2 * t + e) * 4);
                 }
             }
-        const bool whole_unit = cw.starts && cw.ends;
-        const int slot = nseg == 0 ? 0 : 1;
-        if (!whole_unit) {
-            const int4 x = make_int4(cw.sb, cw.skvh, cw.smt,
-                                     kFragValid | (cw.starts ? kFragStarts : 0) | (cw.ends ? kFragEnds : 0));
-            if (slot == 0) dir0 = x;
-            else dir1 = x;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    st.m[j][e] = -INFINITY;
+                    st.l[j][e] = st.lb[j][e] = 0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st.o[j][c][e] = 0.f;
+            }
+            for (int i = warp >= turn ? warp - turn : warp - turn + NW; i < s.n; i += NW) {
+                const int sg = own * NW + warp;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) {
+                    dead = true;
+                    break;
+                }
+                const float4 me = meta[sg];
+                const int key0 = __float_as_int(me.z);
+                const uint32_t kb = ring_u + sg * C::kStage;
+                const bool whole = key0 + C::kKeys <= s.all_end &&
+                                   (key0 >= s.all_lo || key0 + C::kKeys <= p.num_sinks);
+                if (whole)
+                    chunk_step<D, FP8, NT, false>(st, qf, fq, p, s, G, kb, kb + C::kTile, me.x, me.y, key0, lane);
+                else
+                    chunk_step<D, FP8, NT, true>(st, qf, fq, p, s, G, kb, kb + C::kTile, me.x, me.y, key0, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[sg]);
+                if (++own == C::kOwn) {
+                    own = 0;
+                    phase ^= 1;
+                }
+            }
+            turn = (turn + s.n) % NW;
+            // ---- join the warps' states, four rows at a time
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        st.l[j][e] += __shfl_xor_sync(0xffffffffu, st.l[j][e], o);
+                        if constexpr (!FP8) st.lb[j][e] += __shfl_xor_sync(0xffffffffu, st.lb[j][e], o);
+                    }
+                    if (g == 0) {
+                        const int r = warp * C::kRows + 8 * j + 2 * t + e;
+                        red_m[r] = st.m[j][e];
+                        red_l[r] = st.l[j][e];
+                        if constexpr (!FP8) red_lb[r] = st.lb[j][e];
+                    }
+                }
         }
+        if (dead && lane == 0) {
+            set_err(p.err, PKV_ERRBIT_TIMEOUT);
+            *abort_flag = 1;
+        }
+        auto put_rows = [&](int rg) {
+            if ((t >> 1) == (rg & 1)) {
+                constexpr int RS = C::kRedStride;
+                float* r0 = red + (warp * 4 + 2 * (t & 1)) * RS;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const float(&o)[4] = st.o[rg >> 1][c];
+                    if constexpr (FP8) {
+                        *reinterpret_cast<float2*>(r0 + 16 * c + 2 * g) = make_float2(o[0], o[2]);
+                        *reinterpret_cast<float2*>(r0 + RS + 16 * c + 2 * g) = make_float2(o[1], o[3]);
+                    } else {
+                        r0[16 * c + g] = o[0];
+                        r0[16 * c + 8 + g] = o[2];
+                        r0[RS + 16 * c + g] = o[1];
+                        r0[RS + 16 * c + 8 + g] = o[3];
+                    }
+                }
+            }
+        };
+        if (run) put_rows(0);
+        // the next segment's query rows, on their way while this one is joined
+        have = false;
+        if (NT == 1 && run) {
+            const int dn = (nseg + 1) % kDescs;
+            have = __all_sync(0xffffffffu, mbar_test(&dfull[dn], ((nseg + 1) / kDescs) & 1)) && desc[dn].n >= 0;
+            if (have) fetch_q(desc[dn]);
+        }
+        // every consumer passes here once a segment, whether its waits held or not
+        sync();
+        if (*abort_flag || !run) break;
         const int rows_here = min(C::kRows, s.nrows * G - R0);
+        // rows 4 rg .. 4 rg + 3 of the warps' states in red / red_m / red_l: joined and written,
+        // as the result or as a partial state
+        auto join_rows = [&](int rg) {
+            for (int e = threadIdx.x; e < 4 * D / 2; e += NW * 32) {
+                const int rr = e / (D / 2), d = (e - rr * (D / 2)) * 2;
+                const int r = 4 * rg + rr;
+                if (r >= rows_here) continue;
+                const int tok = (R0 + r) / G, h = s.kvh * G + (R0 + r) % G;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * C::kRows + r]);
+                float L = 0.f, Lb = 0.f;
+                float2 O = make_float2(0.f, 0.f);
+                if (M != -INFINITY && tok < s.qreal) {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const float f = fast_exp2(red_m[w * C::kRows + r] - M);
+                        const float2 o = *reinterpret_cast<const float2*>(red + (w * 4 + rr) * C::kRedStride + d);
+                        L = fmaf(f, red_l[w * C::kRows + r], L);
+                        if constexpr (!FP8) Lb = fmaf(f, red_lb[w * C::kRows + r], Lb);
+                        O.x = fmaf(f, o.x, O.x);
+                        O.y = fmaf(f, o.y, O.y);
+                    }
+                }
+                // bf16 weights: normalised by the sum of the rounded ones
+                const float div = FP8 ? L : Lb;
+                const float inv = div > 0.f ? 1.0f / div : (div == div ? 0.f : div);
+                O.x *= inv;
+                O.y *= inv;
+                const float lse2 = L == 0.f ? -INFINITY : M + __log2f(L);
+                if (s.frag < 0) {
+                    const int64_t ot = static_cast<int64_t>(s.r0 + tok) * p.num_q_heads + h;
+                    if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + ot * D + d) = O;
+                    else
+                        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + ot * D + d) =
+                            pack_bf16x2(O.x, O.y);
+                    if (p.lse && d == 0) p.lse[ot] = lse2 * kLn2;
+                } else {
+                    const int64_t fr = static_cast<int64_t>(s.frag) * C::kRows + r;
+                    __stcg(reinterpret_cast<float2*>(a.frag_o + fr * D + d), O);
+                    if (d == 0) __stcg(a.frag_lse + fr, lse2);
+                }
+            }
+        };
 #pragma unroll
         for (int rg = 0; rg < C::kRows / 4; ++rg) {
             if (4 * rg < rows_here) {
-                if ((t >> 1) == (rg & 1)) {
-                    constexpr int RS = C::kRedStride;
-                    float* r0 = red + (warp * 4 + 2 * (t & 1)) * RS;
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const float(&o)[4] = st.o[rg >> 1][c];
-                        if constexpr (FP8) {
-                            *reinterpret_cast<float2*>(r0 + 16 * c + 2 * g) = make_float2(o[0], o[2]);
-                            *reinterpret_cast<float2*>(r0 + RS + 16 * c + 2 * g) = make_float2(o[1], o[3]);
-                        } else {
-                            r0[16 * c + g] = o[0];
-                            r0[16 * c + 8 + g] = o[2];
-                            r0[RS + 16 * c + g] = o[1];
-                            r0[RS + 16 * c + 8 + g] = o[3];
-                        }
-                    }
+                if (rg > 0) {
+                    put_rows(rg);
+                    sync();
                 }
-                __syncthreads();
-                for (int e = threadIdx.x; e < 4 * D / 2; e += kThreads) {
-                    const int rr = e / (D / 2), d = (e - rr * (D / 2)) * 2;
-                    const int r = 4 * rg + rr;
-                    if (r >= rows_here) continue;
-                    const int tok = (R0 + r) / G, h = cw.skvh * G + (R0 + r) % G;
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_m[w * C::kRows + r]);
-                    float L = 0.f, Lb = 0.f;
-                    float2 O = make_float2(0.f, 0.f);
-                    if (M != -INFINITY && tok < s.qreal) {
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w) {
-                            const float f = fast_exp2(red_m[w * C::kRows + r] - M);
-                            const float2 o = *reinterpret_cast<const float2*>(red + (w * 4 + rr) * C::kRedStride + d);
-                            L = fmaf(f, red_l[w * C::kRows + r], L);
-                            if constexpr (!FP8) Lb = fmaf(f, red_lb[w * C::kRows + r], Lb);
-                            O.x = fmaf(f, o.x, O.x);
-                            O.y = fmaf(f, o.y, O.y);
-                        }
-                    }
-                    // bf16 weights: normalised by the sum of the rounded ones
-                    const float div = FP8 ? L : Lb;
-                    const float inv = div > 0.f ? 1.0f / div : (div == div ? 0.f : div);
-                    O.x *= inv;
-                    O.y *= inv;
-                    const float lse = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
-                    if (whole_unit) {
-                        const int64_t ot = static_cast<int64_t>(s.r0 + tok) * p.num_q_heads + h;
-                        if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + ot * D + d) = O;
-                        else
-                            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + ot * D + d) =
-                                pack_bf16x2(O.x, O.y);
-                        if (p.lse && d == 0) p.lse[ot] = lse;
-                    } else {
-                        const int64_t fr = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kRows + r;
-                        *reinterpret_cast<float2*>(a.frag_o + fr * D + d) = O;
-                        if (d == 0) a.frag_lse[fr] = lse;
-                    }
-                }
-                __syncthreads();
+                join_rows(rg);
+                sync();
             }
         }
+        if (lane == 0) mbar_arrive(&dempty[ds]);
     }
-    if (a.ctas > 0 && threadIdx.x < 2)
-        a.frag_dir[static_cast<int64_t>(blockIdx.x) * 2 + threadIdx.x] = threadIdx.x == 0 ? dir0 : dir1;
-    // after a wait that gave up: leave with no copy in flight
-    for (int j = consumed; j < issued; ++j) mbar_wait(&bars[j % S], (j / S) & 1);
 }
 
-// Joins the partial states of the units cut between CTAs.  Block (c, r): the
-// unit that starts in CTA c and goes on behind it, row r; its pieces are CTA
-// c's last and the first of c + 1, c + 2, ... up to the one that ends it.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(const __grid_constant__ RowsArgs a) {
-    constexpr int DPL = D / 32;
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
+// The line: where each sequence's units start, one place per chunk (and one for
+// a unit without any), and what each piece starts with.  One CTA; also clears
+// the ticket and the counts.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 2048;  // sequences whose places stay in shared memory
+template <int ROWS, int KEYS>
+__global__ void __launch_bounds__(kPlanThreads) attn_rows_plan_kernel(const __grid_constant__ RowsArgs a) {
+    __shared__ int warp_sum[32];
+    __shared__ int places[kPlanSeqs + 1];
     const AttnParams& p = a.p;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, r = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int slot = -1;
-    int4 u = make_int4(0, 0, 0, 0);
-    for (int s = 0; s < 2; ++s) {
-        const int4 x = a.frag_dir[c * 2 + s];
-        if ((x.w & kFragValid) && (x.w & kFragStarts) && !(x.w & kFragEnds)) {
-            slot = s;
-            u = x;
-        }
-    }
-    if (slot < 0) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int G = p.num_q_heads / p.num_kv_heads;
-    const int R = u.z * ROWS + r;
-    const int r0 = p.q_indptr[u.x];
-    const int nrows = min(p.q_indptr[u.x + 1] - r0, p.max_q_rows);
-    const int tok = R / G, h = u.y * G + R % G;
-    if (tok >= nrows) return;
-    int n = 1;  // pieces: c's, then the first ones of the CTAs behind it
-    while (c + n < a.ctas) {
-        const int4 x = a.frag_dir[(c + n) * 2];
-        ++n;
-        if (!(x.w & kFragValid) || (x.w & kFragEnds)) break;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) *a.ticket = 0;
+    int* seq_at = p.batch <= kPlanSeqs ? places : a.seq_at;
+    int base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int mine = 0;
+        if (b < p.batch) {
+            const Seq s = sequence<ROWS>(p, b, G);
+            for (int mt = 0; mt < s.tiles; ++mt) mine += max(span_of<ROWS, KEYS>(p, s, mt, G).n, 1);
+            mine *= p.num_kv_heads;
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        int v = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        const int upto = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+        const int before = base + (warp > 0 ? upto : 0) + incl - mine;
+        if (b < p.batch) {
+            seq_at[b] = before;
+            a.seq_at[b] = before;
+        }
+        base += __shfl_sync(0xffffffffu, v, 31);
+        __syncthreads();
     }
+    if (threadIdx.x == 0) {
+        seq_at[p.batch] = base;
+        a.seq_at[p.batch] = base;
+    }
+    __syncthreads();
+    const Line line(base, a.ctas);
+    for (int i = threadIdx.x; i < line.pieces(); i += kPlanThreads) {
+        int from, to;
+        line.piece(i, from, to);
+        if (from >= to) continue;
+        int lo = 0, hi = p.batch - 1;  // the last sequence that starts at or before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (seq_at[mid] <= from) lo = mid;
+            else hi = mid - 1;
+        }
+        const int per_head = (seq_at[lo + 1] - seq_at[lo]) / p.num_kv_heads;
+        const int kvh = (from - seq_at[lo]) / per_head;
+        a.starts[i] = make_int4(lo, kvh, from - seq_at[lo] - kvh * per_head, 0);
+    }
+    // the units that pieces cut
+    const int units = a.tiles_max * p.num_kv_heads * p.batch;
+    for (int u = threadIdx.x; u < units; u += kPlanThreads) {
+        const int mt = u % a.tiles_max, kvh = u / a.tiles_max % p.num_kv_heads, b = u / a.tiles_max / p.num_kv_heads;
+        const int per_head = (seq_at[b + 1] - seq_at[b]) / p.num_kv_heads;
+        int at = seq_at[b] + kvh * per_head, n = per_head;
+        bool exists = n > 0;
+        if (a.tiles_max > 1) {
+            const Seq s = sequence<ROWS>(p, b, G);
+            exists = mt < s.tiles;
+            for (int m = 0; m < mt && exists; ++m) at += max(span_of<ROWS, KEYS>(p, s, m, G).n, 1);
+            if (exists) n = max(span_of<ROWS, KEYS>(p, s, mt, G).n, 1);
+        }
+        int2 cut = make_int2(0, 0);
+        if (exists) {
+            const int i0 = line.piece_of(at), i1 = line.piece_of(at + n - 1);
+            if (i1 > i0) cut = make_int2(i0 + u, i1 - i0 + 1);
+        }
+        a.cuts[u] = cut;
+    }
+}
+
+// Joins the partial states of the units that pieces cut: block (unit, four of
+// its rows), kJoinParts warps a row that take every kJoinParts-th state, a lane
+// D / 32 dimensions.
+constexpr int kJoinParts = 4;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinParts * 128) attn_rows_join_kernel(const __grid_constant__ RowsArgs a) {
+    constexpr int DPL = D / 32, kAhead = 32 / kJoinParts;
+    __shared__ float part_o[kJoinParts - 1][4][D];
+    const AttnParams& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x;
+    const int mt = unit % a.tiles_max, kvh = unit / a.tiles_max % p.num_kv_heads;
+    const int b = unit / a.tiles_max / p.num_kv_heads;
+    const int G = p.num_q_heads / p.num_kv_heads;
+    const int q0 = p.q_indptr[b];
+    const int nrows = min(p.q_indptr[b + 1] - q0, p.max_q_rows);
+    const int row = warp & 3, part = warp >> 2;
+    const int r = blockIdx.y * 4 + row, R = mt * ROWS + r;
+    const bool exists = R / G < nrows;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 cut = __ldcg(a.cuts + unit);
+    if (cut.y == 0 || mt * ROWS + static_cast<int>(blockIdx.y) * 4 >= nrows * G) return;  // uniform
     float M = -INFINITY, L = 0.f, O[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) O[i] = 0.f;
-    constexpr int kAhead = 4;
-    for (int k0 = warp; k0 < n; k0 += kWarps * kAhead) {
-        float lv[kAhead], ov[kAhead][DPL];
+    if (exists) {
+        const float* lse = a.frag_lse + static_cast<int64_t>(cut.x) * ROWS + r;
+        const float* o = a.frag_o + (static_cast<int64_t>(cut.x) * ROWS + r) * D + lane * DPL;
+        // 32 states at a time: their sums in the lanes, this warp's outputs in flight with them
+#pragma unroll 1
+        for (int k0 = 0; k0 < cut.y; k0 += 32) {
+            const int n = min(32, cut.y - k0);
+            const float e = lane < n ? __ldcg(lse + static_cast<int64_t>(k0 + lane) * ROWS) : -INFINITY;
+            float v[kAhead][DPL];
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const int k = k0 + x * kWarps;
-            lv[x] = -INFINITY;
-            if (k < n) {
-                const int64_t fr = (static_cast<int64_t>(c + k) * 2 + (k == 0 ? slot : 0)) * ROWS + r;
-                lv[x] = __ldcg(a.frag_lse + fr);
+            for (int x = 0; x < kAhead; ++x) {
+                const int k = kJoinParts * x + part;
+                const float* src = o + static_cast<int64_t>(k0 + k) * (ROWS * D);
+                if constexpr (DPL == 4) {
+                    const float4 u = k < n ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[x][0] = u.x;
+                    v[x][1] = u.y;
+                    v[x][2] = u.z;
+                    v[x][3] = u.w;
+                } else {
+                    const float2 u = k < n ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                    v[x][0] = u.x;
+                    v[x][1] = u.y;
+                }
+            }
+            const float Mn = fmaxf(M, warp_max(e));
+            const float ref = Mn == -INFINITY ? 0.f : Mn;
+            const float w = fast_exp2(e - ref), f = fast_exp2(M - ref);
+            M = Mn;
+            L = fmaf(L, f, warp_sum(w));
 #pragma unroll
-                for (int i = 0; i < DPL; ++i) ov[x][i] = __ldcg(a.frag_o + fr * D + lane * DPL + i);
+            for (int i = 0; i < DPL; ++i) O[i] *= f;
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const float wx = __shfl_sync(0xffffffffu, w, kJoinParts * x + part);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) O[i] = fmaf(wx, v[x][i], O[i]);
             }
         }
+        if (part > 0)
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            if (lv[x] == -INFINITY) continue;
-            const float Mn = fmaxf(M, lv[x]);
-            const float f = __expf(M - Mn), w = __expf(lv[x] - Mn);
-            L = fmaf(L, f, w);
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) O[i] = fmaf(w, ov[x][i], O[i] * f);
-            M = Mn;
-        }
+            for (int i = 0; i < DPL; ++i) part_o[part - 1][row][lane * DPL + i] = O[i];
     }
-    if (lane == 0) {
-        sm[warp] = M;
-        sl[warp] = L;
-    }
-#pragma unroll
-    for (int i = 0; i < DPL; ++i) so[warp][lane * DPL + i] = O[i];
     __syncthreads();
-    if (threadIdx.x >= D) return;
-    const int d = threadIdx.x;
-    M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float l = 0.f, o = 0.f;
-    if (M != -INFINITY) {
+    if (!exists || part > 0) return;
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = __expf(sm[w] - M);
-            l = fmaf(f, sl[w], l);
-            o = fmaf(f, so[w][d], o);
-        }
+    for (int i = 0; i < DPL; ++i) {
+#pragma unroll
+        for (int x = 0; x < kJoinParts - 1; ++x) O[i] += part_o[x][row][lane * DPL + i];
+        O[i] *= inv;
     }
-    o *= l == 0.f ? 0.f : 1.0f / l;
-    const int64_t ot = static_cast<int64_t>(r0 + tok) * p.num_q_heads + h;
-    if (p.out_f32) static_cast<float*>(p.out)[ot * D + d] = o;
-    else static_cast<__nv_bfloat16*>(p.out)[ot * D + d] = __float2bfloat16_rn(o);
-    if (p.lse && d == 0) p.lse[ot] = l == 0.f ? -INFINITY : M + __logf(l);
+    const int64_t ot = static_cast<int64_t>(q0 + R / G) * p.num_q_heads + kvh * G + R % G;
+#pragma unroll
+    for (int i = 0; i < DPL; i += 2) {
+        const int64_t at = ot * D + lane * DPL + i;
+        if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(O[i], O[i + 1]);
+        else *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at) = pack_bf16x2(O[i], O[i + 1]);
+    }
+    if (p.lse && lane == 0) p.lse[ot] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
 }
 
 template <int D, bool FP8, int NT>
-cudaError_t launch_rows(RowsArgs a, const RowsPlan& pl, const void* tk, const void* tv, cudaStream_t s) {
+cudaError_t launch_rows(const RowsArgs& a, const void* tk, const void* tv, cudaStream_t s) {
     using C = Cfg<D, FP8, NT>;
     auto kern = attn_rows_kernel<D, FP8, NT>;
     static DeviceOnce opted;
@@ -891,65 +1193,97 @@ cudaError_t launch_rows(RowsArgs a, const RowsPlan& pl, const void* tk, const vo
     });
     if (e != cudaSuccess) return e;
     const CUtensorMap &mk = *static_cast<const CUtensorMap*>(tk), &mv = *static_cast<const CUtensorMap*>(tv);
-    const unsigned grid = static_cast<unsigned>(a.ctas > 0 ? a.ctas : a.tiles_max * a.p.num_kv_heads * a.p.batch);
-    kern<<<grid, kThreads, C::kBytes, s>>>(mk, mv, a);
+    const unsigned units = static_cast<unsigned>(a.tiles_max * a.p.num_kv_heads * a.p.batch);
+    if (a.ctas == 0) {
+        kern<<<units, C::kThreads, C::kBytes, s>>>(mk, mv, a);
+        return cudaGetLastError();
+    }
+    attn_rows_plan_kernel<C::kRows, C::kKeys><<<1, kPlanThreads, 0, s>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.ctas == 0) return e;
+    if (e != cudaSuccess) return e;
+    // each behind the one before with programmatic serialisation: it starts beside it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), C::kRows);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(units, C::kRows / 4);
+    cfg.blockDim = dim3(kJoinParts * 128);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<D, C::kRows>, a);
 }
 
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+// The workspace of the cut line.
+struct RowsSpace {
+    size_t ticket, cuts, seq_at, starts, frag_lse, frag_o, bytes;
+    RowsSpace(int batch, int64_t units, int ctas, int rows, int D) {
+        auto take = [this](size_t n) {
+            const size_t at = bytes;
+            bytes += (n + 255) / 256 * 256;
+            return at;
+        };
+        const size_t pieces = Line::most(ctas), frags = pieces + static_cast<size_t>(units);
+        bytes = 0;
+        ticket = take(sizeof(int));
+        cuts = take(units * sizeof(int2));
+        seq_at = take((static_cast<size_t>(batch) + 1) * sizeof(int));
+        starts = take(pieces * sizeof(int4));
+        frag_lse = take(frags * rows * sizeof(float));
+        frag_o = take(frags * rows * D * sizeof(float));
+    }
+};
 
 }  // namespace
 
-// One CTA a unit while a unit is short (kDirectKeys keys at the host bound, a
-// few chunks a warp); beyond that the cut line.
+// One CTA a unit while a unit is short (kDirectBytes of K and V at the host
+// bound, what a CTA streams in about 6 us) or the rows alone make units enough (more than kCutTiles
+// tiles a sequence, whose places the planner would add up one by one); else
+// the cut line.
 RowsPlan plan_attn_rows(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window,
                         int num_sinks, bool fp8, int sms) {
-    constexpr int kDirectKeys = 512;
+    constexpr int64_t kDirectBytes = 384 * 1024;
+    constexpr int kCutTiles = 16;
     RowsPlan pl{};
     const int64_t rows = static_cast<int64_t>(max_q_rows) * (Hq / Hkv);
     pl.row_tiles = rows <= 8 ? 1 : 2;
     const int R = 8 * pl.row_tiles;
     pl.tiles = (rows + R - 1) / R;
+    pl.units = pl.tiles * Hkv * batch;
     int64_t keys = max_kv_len;
     if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + R + std::min(num_sinks, max_kv_len) + 62);
-    const int64_t units = pl.tiles * Hkv * batch;
-    (void)fp8;
-    if (keys <= kDirectKeys && units < (1ll << 31)) return pl;
+    const double places = static_cast<double>(pl.units) * (std::min<double>(keys, max_kv_len) / 16 + 3);
+    if (keys * 2 * D * (fp8 ? 1 : 2) <= kDirectBytes || pl.tiles > kCutTiles || places > 2e9) return pl;  // the line is counted in 32 bits
     pl.ctas = kCtasPerSm * sms;
-    pl.ws_bytes = align256(static_cast<size_t>(pl.ctas) * 2 * sizeof(int4)) +
-                  align256(static_cast<size_t>(pl.ctas) * 2 * R * sizeof(float)) +
-                  align256(static_cast<size_t>(pl.ctas) * 2 * R * D * sizeof(float));
+    pl.ws_bytes = RowsSpace(batch, pl.units, pl.ctas, R, D).bytes;
     return pl;
 }
 
 cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* workspace, const void* tk,
                              const void* tv, cudaStream_t s) {
+    if (pl.units > 0x7fffffff - Line::most(pl.ctas)) return cudaErrorInvalidConfiguration;
     RowsArgs a{};
     a.p = p;
     a.ctas = pl.ctas;
-    a.tiles_max = static_cast<int>(std::min<int64_t>(pl.tiles, 0x7fffffff));
+    a.tiles_max = static_cast<int>(pl.tiles);
     if (pl.ctas > 0) {
+        const RowsSpace x(p.batch, pl.units, pl.ctas, 8 * pl.row_tiles, p.head_dim);
         char* w = static_cast<char*>(workspace);
-        const size_t R = 8 * pl.row_tiles;
-        a.frag_dir = reinterpret_cast<int4*>(w);
-        w += align256(static_cast<size_t>(pl.ctas) * 2 * sizeof(int4));
-        a.frag_lse = reinterpret_cast<float*>(w);
-        w += align256(static_cast<size_t>(pl.ctas) * 2 * R * sizeof(float));
-        a.frag_o = reinterpret_cast<float*>(w);
+        a.ticket = reinterpret_cast<int*>(w + x.ticket);
+        a.cuts = reinterpret_cast<int2*>(w + x.cuts);
+            a.seq_at = reinterpret_cast<int*>(w + x.seq_at);
+        a.starts = reinterpret_cast<int4*>(w + x.starts);
+        a.frag_lse = reinterpret_cast<float*>(w + x.frag_lse);
+        a.frag_o = reinterpret_cast<float*>(w + x.frag_o);
     }
 #define PKV_ROWS(D_, F_, N_) \
-    if (p.head_dim == D_ && p.kv_fp8 == F_ && pl.row_tiles == N_) return launch_rows<D_, F_, N_>(a, pl, tk, tv, s);
+    if (p.head_dim == D_ && p.kv_fp8 == F_ && pl.row_tiles == N_) return launch_rows<D_, F_, N_>(a, tk, tv, s);
     PKV_ROWS(128, true, 1) PKV_ROWS(128, true, 2) PKV_ROWS(128, false, 1) PKV_ROWS(128, false, 2)
     PKV_ROWS(64, true, 1) PKV_ROWS(64, true, 2) PKV_ROWS(64, false, 1) PKV_ROWS(64, false, 2)
 #undef PKV_ROWS

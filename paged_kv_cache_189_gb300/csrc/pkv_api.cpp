@@ -713,8 +713,7 @@ size_t ext_workspace(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_
     if (batch <= 0 || max_q_rows <= 0 || Hkv <= 0 || Hq < Hkv || max_kv_len < 0 || window < 0 || num_sinks < 0)
         return 0;
     if (flags & PKV_FLAG_SIMT_ONLY) return 0;
-    return pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8,
-                               current_device_sms())
+    return pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, current_device_sms())
         .ws_bytes;
 }
 
@@ -856,6 +855,7 @@ pkv_status ext_attention(const ExtArgs& a) {
 
     const pkv::RowsPlan rp = pkv::plan_attn_rows(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim,
                                                  a.max_kv_len, a.window, a.num_sinks, a.fp8, current_device_sms());
+    if (rp.units > 0x7fffff00) return fail(PKV_ERR_UNSUPPORTED, "%s: too many row tiles", n);
     CUtensorMap tk, tv;
     pkv_status st = make_rows_map(&tk, a.k_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
     if (st != PKV_OK) return st;

@@ -231,11 +231,11 @@ cudaError_t launch_attn_simt_ext(const AttnParams& p, cudaStream_t s);
 
 // Few query rows per sequence over bf16 or fp8 pools with a window and sinks
 // (mma.sync, TMA-fed rings per warp).  The plan's row tile is 8 * row_tiles
-// (query row, grouped head) pairs; ctas = 0 runs one CTA per unit, else the
-// units' keys are cut into that many shares and a second launch joins them.
+// (query row, grouped head) pairs; ctas = 0 runs one CTA per unit, else that
+// many CTAs share the units' keys (a planner before and a join behind them).
 struct RowsPlan {
     int row_tiles;
-    int64_t tiles;  // row tiles of a sequence at the host bound
+    int64_t tiles, units;  // row tiles of a sequence, units of the call, at the host bounds
     int ctas;
     size_t ws_bytes;
 };
