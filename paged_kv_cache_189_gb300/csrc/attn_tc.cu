@@ -234,6 +234,11 @@ __device__ __forceinline__ int visible_keys(int i, int qreal, int kv_len, int ma
 
 struct TileGeom {
     int b, kvh, split, r0, nrows, qreal, kv_len, t0, kb, key_hi, nt;
+    // windowed calls: the pair's rows see keys inside [0, sinks) and [lo, key_hi),
+    // in the key tiles [0, nst) and from wt0 on; the split's first is the j0-th
+    int lo, sinks, nst, wt0, j0;
+    // expanded pools: page p of the sequence is page_base + p, less page_gap from page near on
+    int page_base, page_near, page_gap;
 };
 
 // The sequence at position `pos` when the batch is ordered by key count,
@@ -1269,6 +1274,54 @@ __device__ __forceinline__ TileGeom pair_geometry(const AttnParams& p, int TQ, i
     return g;
 }
 
+// The same for a call with a window and sinks (or none) over a bf16 pool or one
+// expanded from 8 bits.  Key tiles keep their absolute places; those between
+// the sinks and the window are left out.  The splits share the tiles evenly.
+__device__ __forceinline__ TileGeom ext_geometry(const AttnParams& p, int TQ, int b, int kvh, int x, int split) {
+    TileGeom g;
+    g.b = b;
+    g.kvh = kvh;
+    g.split = split;
+    g.r0 = p.q_indptr[b];
+    g.nrows = min(p.q_indptr[b + 1] - g.r0, p.max_q_rows);
+    g.t0 = x * 2 * TQ;
+    g.qreal = max(min(p.q_real ? p.q_real[b] : g.nrows, g.nrows), 0);
+    g.kv_len = min(max(p.kv_lens[b], 0), p.max_kv_len);
+    g.kb = 0;
+    g.key_hi = g.lo = g.nst = g.wt0 = g.j0 = g.nt = 0;
+    g.sinks = p.num_sinks;
+    const int first_new = g.kv_len - g.qreal;
+    const int seq_lo = p.window > 0 ? max(0, first_new - p.window + 1) : 0;
+    g.page_near = seq_lo / 32;
+    g.page_gap = g.page_near - min((min(p.num_sinks, g.kv_len) + 31) / 32, g.page_near);
+    g.page_base = b * p.expanded_pages;
+    if (g.t0 < g.qreal) {
+        const int last = min(g.t0 + 2 * TQ, g.qreal) - 1;
+        g.key_hi = min(visible_keys(last, g.qreal, g.kv_len, p.mask, max(p.causal_block, 1)), g.kv_len);
+        if (g.key_hi > 0) {
+            if (p.window > 0) g.lo = max(0, first_new + g.t0 - p.window + 1);
+            g.wt0 = g.lo / kTileN;
+            g.nst = min((min(p.num_sinks, g.key_hi) + kTileN - 1) / kTileN, g.wt0);
+            const int all = g.nst + (g.key_hi + kTileN - 1) / kTileN - g.wt0;
+            const int per = (all + p.num_splits - 1) / p.num_splits;
+            g.j0 = split * per;
+            g.nt = max(0, min(all, g.j0 + per) - g.j0);
+        }
+    }
+    return g;
+}
+
+// First key of the j-th key tile of this CTA.
+template <bool EXT>
+__device__ __forceinline__ int tile_key0(const TileGeom& g, int j) {
+    if constexpr (EXT) {
+        const int i = g.j0 + j;
+        return (i < g.nst ? i : i - g.nst + g.wt0) * kTileN;
+    } else {
+        return g.kb + j * kTileN;
+    }
+}
+
 // Stream-K unit u: tile pairs fastest, then K/V heads, then sequences, so the
 // units that read the same K/V run on neighbouring CTAs at about the same time.
 __device__ __forceinline__ TileGeom sk_unit(const AttnParams& p, int TQ, int u) {
@@ -1282,7 +1335,7 @@ __device__ __forceinline__ int sk_weight(const TileGeom& g, int TQ) {
 }
 
 // The segments of one CTA, in order.  Every role of the CTA walks them itself.
-template <bool SK>
+template <bool SK, bool EXT>
 struct SegIter {
     int u = 0, end_u = 0;  // stream-K: next shared unit (index among the shared ones)
     int a = 0, a1 = 0;     // this CTA's share [a, a1) of the shared units' weighted key tiles
@@ -1309,8 +1362,12 @@ struct SegIter {
         if constexpr (!SK) {
             if (done) return false;
             done = true;
-            s.g = pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
-                                blockIdx.z % p.num_splits);
+            if constexpr (EXT)
+                s.g = ext_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
+                                   blockIdx.z % p.num_splits);
+            else
+                s.g = pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
+                                    blockIdx.z % p.num_splits);
             s.u = -1;
             s.j0 = 0;
             s.j1 = s.g.nt;
@@ -1365,7 +1422,7 @@ __device__ __forceinline__ void zero_pair_rows(const AttnParams& p, const TileGe
     store_row_lse(p, g, i, g.kvh * G + r % G, -INFINITY);
 }
 
-template <int D, int GC, bool SK>
+template <int D, int GC, bool SK, bool EXT = false>
 __global__ void __maxnreg__(kRegs2)
     attn_tc2_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const AttnParams p) {
@@ -1377,7 +1434,7 @@ __global__ void __maxnreg__(kRegs2)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    SegIter<SK> it0;
+    SegIter<SK, EXT> it0;
     if constexpr (SK) {
         // launched behind the planner with programmatic serialisation: its unit
         // offsets are visible after this wait
@@ -1391,8 +1448,17 @@ __global__ void __maxnreg__(kRegs2)
         }
         it0.init(p);
     } else {
-        const TileGeom g = pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
-                                         blockIdx.z % p.num_splits);
+        const TileGeom g = EXT ? ext_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
+                                              blockIdx.z % p.num_splits)
+                               : pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
+                                               blockIdx.z % p.num_splits);
+        if constexpr (EXT) {
+            if (p.checked && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
+                const int rows = p.q_indptr[g.b + 1] - g.r0, kv = p.kv_lens[g.b];
+                if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[g.b] > rows))
+                    set_err(p.err, PKV_ERRBIT_LEN);
+            }
+        }
         if (g.t0 >= g.nrows) return;  // uniform
         if (g.nt == 0) {
             zero_pair_rows<D>(p, g, G, TQ);
@@ -1401,7 +1467,7 @@ __global__ void __maxnreg__(kRegs2)
     }
     {
         // a CTA without a segment leaves before any set-up (uniform)
-        SegIter<SK> probe = it0;
+        SegIter<SK, EXT> probe = it0;
         Seg s;
         if (!probe.next(p, TQ, s)) return;
     }
@@ -1478,7 +1544,7 @@ __global__ void __maxnreg__(kRegs2)
             uint8_t* ring = smem + (is_k ? SM::kKOff : SM::kVOff);
             uint64_t* full = is_k ? k_full : v_full;
             uint64_t* empty = is_k ? k_empty : v_empty;
-            SegIter<SK> it = it0;
+            SegIter<SK, EXT> it = it0;
             Seg sg;
             int n = 0;  // tiles issued
             bool alive = true;
@@ -1489,8 +1555,21 @@ __global__ void __maxnreg__(kRegs2)
                 auto fetch_pages = [&](int j, int (&ph)[4]) {
 #pragma unroll
                     for (int pg = 0; pg < 4; ++pg) {
-                        const int lp = (g.kb + j * kTileN) / 32 + pg;
-                        ph[pg] = lp < last_page ? bt[lp] : static_cast<int>(p.num_pages);
+                        const int lp = tile_key0<EXT>(g, j) / 32 + pg;
+                        if constexpr (EXT) {
+                            // pages that no row of the pair sees are not looked up: zeros
+                            const bool seen = lp * 32 < g.key_hi && (lp * 32 + 32 > g.lo || lp * 32 < g.sinks);
+                            ph[pg] = static_cast<int>(p.num_pages);
+                            if (seen && p.expanded_pages > 0) {
+                                ph[pg] = g.page_base + lp - (lp >= g.page_near ? g.page_gap : 0);
+                            } else if (seen) {
+                                const int phys = bt[lp];
+                                if (phys >= 0 && phys < p.num_pages) ph[pg] = phys;
+                                else if (p.checked) set_err(p.err, PKV_ERRBIT_PAGE);
+                            }
+                        } else {
+                            ph[pg] = lp < last_page ? bt[lp] : static_cast<int>(p.num_pages);
+                        }
                     }
                 };
                 int next[4] = {0, 0, 0, 0};
@@ -1508,7 +1587,7 @@ __global__ void __maxnreg__(kRegs2)
                     for (int pg = 0; pg < 4; ++pg) {
                         const int lp = (g.kb + j * kTileN) / 32 + pg;
                         int phys = cur[pg];
-                        if (p.checked && lp < last_page && (phys < 0 || phys >= p.num_pages)) {
+                        if (!EXT && p.checked && lp < last_page && (phys < 0 || phys >= p.num_pages)) {
                             set_err(p.err, PKV_ERRBIT_PAGE);
                             phys = static_cast<int>(p.num_pages);
                         }
@@ -1570,7 +1649,7 @@ __global__ void __maxnreg__(kRegs2)
                 tc_fence_after();
                 return true;
             };
-            SegIter<SK> it = it0;
+            SegIter<SK, EXT> it = it0;
             Seg sg;
             int gt = 0;          // K/V tiles consumed (ring position)
             int na = 0, nb = 0;  // P tiles of tile A / tile B consumed
@@ -1650,7 +1729,7 @@ __global__ void __maxnreg__(kRegs2)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 256;
         const uint32_t o_addr = lane_addr + 128;  // this row's O columns
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-        SegIter<SK> it = it0;
+        SegIter<SK, EXT> it = it0;
         Seg sg;
         int gt = 0;     // K/V ring position of the segment's first tile
         int nit = 0;    // key tiles of this tile's rows processed (S / P phases)
@@ -1665,6 +1744,8 @@ __global__ void __maxnreg__(kRegs2)
             const bool row_exists = t < TQ && i < g.nrows;
             const int limit = row_exists ? visible_keys(i, g.qreal, g.kv_len, p.mask, max(p.causal_block, 1))
                                          : 0;
+            // windowed: the row's first key (those below num_sinks stay visible)
+            const int row_lo = EXT && p.window > 0 ? g.kv_len - g.qreal + i - p.window + 1 : 0;
             {
                 // the row's query into the swizzled Q tile.  The previous segment's
                 // S MMAs have finished reading this Q tile (their S was consumed),
@@ -1704,7 +1785,7 @@ __global__ void __maxnreg__(kRegs2)
                     break;
                 }
                 tc_fence_after();
-                const int key0 = g.kb + j * kTileN;
+                const int key0 = tile_key0<EXT>(g, j);
                 if (warp_live) {
                     uint32_t sv[kTileN];  // this row's scores (f32 bits), then its packed P
                     tmem_load128(lane_addr, sv);
@@ -1712,6 +1793,15 @@ __global__ void __maxnreg__(kRegs2)
                     if (__any_sync(0xffffffffu, nvis < kTileN)) {
 #pragma unroll
                         for (int e = 0; e < kTileN; ++e) sv[e] = e < nvis ? sv[e] : __float_as_uint(-INFINITY);
+                    }
+                    if constexpr (EXT) {
+                        // keys between the sinks and the row's window (tiles at its lower edge)
+                        const int from = g.sinks - key0, to = row_lo - key0;
+                        if (__any_sync(0xffffffffu, to > max(from, 0))) {
+#pragma unroll
+                            for (int e = 0; e < kTileN; ++e)
+                                sv[e] = e >= from && e < to ? __float_as_uint(-INFINITY) : sv[e];
+                        }
                     }
                     float a[8];
 #pragma unroll
@@ -1771,8 +1861,25 @@ __global__ void __maxnreg__(kRegs2)
                     tmem_store64_nowait(lane_addr, zero);
                     tmem_store_wait();
                 }
-                // keys past the sequence's length inside its last page: zero their V rows
-                if (x == 0 && key0 + kTileN > g.kv_len && g.kv_len > key0) {
+                if constexpr (EXT) {
+                    // V rows of keys that no row of the pair sees may hold anything: zero them
+                    if (x == 0 && (key0 + kTileN > g.key_hi || (key0 < g.lo && key0 + kTileN > g.sinks))) {
+                        const int gj = gt + (j - sg.j0);
+                        const int vs = gj % kVStages;
+                        if (__all_sync(0xffffffffu, wait(&v_full[vs], (gj / kVStages) & 1))) {
+                            uint8_t* vt = smem + SM::kVOff + vs * TD::kTile;
+                            const int key = key0 + r;  // this thread's row of the tile
+                            if (!(key < g.key_hi && (key >= g.lo || key < g.sinks))) {
+#pragma unroll
+                                for (int c16 = 0; c16 < TD::kChunks; ++c16)
+                                    *reinterpret_cast<uint4*>(vt + (c16 >> 3) * kHalfBytes + sw128_offset(r, c16 & 7)) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                        }
+                    }
+                } else if (x == 0 && key0 + kTileN > g.kv_len && g.kv_len > key0) {
+                    // keys past the sequence's length inside its last page: zero their V rows
                     const int gj = gt + (j - sg.j0);
                     const int vs = gj % kVStages;
                     if (__all_sync(0xffffffffu, wait(&v_full[vs], (gj / kVStages) & 1))) {
@@ -2045,6 +2152,27 @@ cudaError_t launch_g2(const AttnParams& p, const void* tk, const void* tv, cudaS
     return cudaLaunchKernelEx(&rcfg, tc2_sk_reduce_kernel<D>, p);
 }
 
+// Windowed calls and calls over pools expanded from 8 bits: the two-tile kernel
+// for any number of rows (a pair whose rows fit one tile leaves the other idle).
+template <int D, int GC>
+cudaError_t launch_ext(const AttnParams& p, const void* tk, const void* tv, cudaStream_t s) {
+    auto kern = attn_tc2_kernel<D, GC, false, true>;
+    constexpr int kSmem = TwoTileSmem<D>::kBytes;
+    static DeviceOnce opted;
+    int dev = 0, done = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = opted.get(dev, &done, [&](int, int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const int TQ = kTileM / (p.num_q_heads / p.num_kv_heads);
+    dim3 grid((p.max_q_rows + 2 * TQ - 1) / (2 * TQ), p.num_kv_heads, p.batch * p.num_splits);
+    kern<<<grid, kThreads2, kSmem, s>>>(*static_cast<const CUtensorMap*>(tk), *static_cast<const CUtensorMap*>(tv), p);
+    return cudaGetLastError();
+}
+
 // One-tile launches: when a tile's rows (query rows x grouped heads) fit in
 // one 32-lane quadrant, they are held four times and each warp takes a
 // quarter of every key tile's columns.
@@ -2133,6 +2261,19 @@ size_t attn_tc_sk_bytes(int units, int ctas, int head_dim) {
            r256(2 * static_cast<size_t>(ctas) * 16) +
            r256(2 * static_cast<size_t>(ctas) * kSkFragRows * sizeof(float)) +
            r256(2 * static_cast<size_t>(ctas) * kSkFragRows * head_dim * sizeof(float));
+}
+
+cudaError_t launch_attn_tc_ext(const AttnParams& p, const void* tk, const void* tv, cudaStream_t s) {
+    if (p.head_dim == 128) {
+        switch (p.num_q_heads / p.num_kv_heads) {
+            case 1: return launch_ext<128, 1>(p, tk, tv, s);
+            case 4: return launch_ext<128, 4>(p, tk, tv, s);
+            case 8: return launch_ext<128, 8>(p, tk, tv, s);
+        }
+        return launch_ext<128, 0>(p, tk, tv, s);
+    }
+    if (p.head_dim == 64) return launch_ext<64, 0>(p, tk, tv, s);
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_attn_tc_grouped(const AttnParams& p, const void* tk, const void* tv, cudaStream_t s) {

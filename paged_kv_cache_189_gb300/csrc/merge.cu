@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
     if (row_in_seq >= nrows) return;
     const int row = r0 + row_in_seq;
     if (row >= static_cast<int64_t>(p.batch) * p.max_q_rows) return;  // workspace bound
-    int nsplit = p.num_splits;  // grouped mode: every split wrote a state for every token
-    if (!p.grp_perm) {
+    int nsplit = p.num_splits;  // grouped mode, windowed calls: every split wrote a state for every token
+    if (!p.grp_perm && !p.even_splits) {
         const int qreal = p.q_real ? p.q_real[b] : nrows;
         int kv_len = min(p.kv_lens[b], p.max_kv_len);
         if (row_in_seq >= qreal) kv_len = 0;

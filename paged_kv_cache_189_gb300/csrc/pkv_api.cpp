@@ -707,14 +707,59 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
 
 namespace {
 
+// The kernel of a paged_attention_fp8 / paged_attention_window call: the tile
+// kernel where the rows of a sequence and head are many, else the few-row one.
+struct ExtPlan {
+    bool tile = false;
+    pkv::RowsPlan rows{};
+    int splits = 1;
+    int pages = 0;  // pages a sequence has in the expanded pools
+    size_t expand_bytes = 0, states_o = 0, states_lse = 0, ws_bytes = 0;
+};
+// (query row, grouped head) pairs of a K/V head up to which the few-row kernel
+// reads the cache once per 16 of them
+constexpr int kFewRows = 64;
+
+ExtPlan plan_ext(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
+                 bool fp8, int sms) {
+    ExtPlan pl;
+    const int G = Hq / Hkv;
+    pl.tile = static_cast<int64_t>(max_q_rows) * G > kFewRows && pkv::attn_tc_supported(D, G);
+    if (!pl.tile) {
+        pl.rows = pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, sms);
+        pl.ws_bytes = pl.rows.ws_bytes;
+        return pl;
+    }
+    const int pair = 2 * pkv::attn_tc_rows_per_tile(G);
+    int64_t keys = max_kv_len, pages = (static_cast<int64_t>(max_kv_len) + 31) / 32;
+    if (window > 0) {
+        keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + pair + std::min(num_sinks, max_kv_len) + 254);
+        pages = std::min(pages, (std::min(num_sinks, max_kv_len) + 31) / 32 +
+                                    (static_cast<int64_t>(window) + max_q_rows + 29) / 32 + 1);
+    }
+    const int64_t ctas = static_cast<int64_t>((max_q_rows + pair - 1) / pair) * Hkv * batch;
+    pl.splits = tile_splits(ctas, static_cast<int>(keys), 0, sms);
+    if (fp8) {
+        pl.pages = static_cast<int>(pages);
+        pl.expand_bytes = round_up(static_cast<size_t>(batch) * pages * 32 * Hkv * D * 2, 256);
+    }
+    if (pl.splits > 1) {
+        const size_t states = static_cast<size_t>(batch) * max_q_rows * Hq * pl.splits;
+        pl.states_o = round_up(states * D * sizeof(float), 256);
+        pl.states_lse = round_up(states * sizeof(float), 256);
+    }
+    pl.ws_bytes = 2 * pl.expand_bytes + pl.states_o + pl.states_lse;
+    return pl;
+}
+
 // Workspace of paged_attention_fp8 / paged_attention_window for these bounds.
 size_t ext_workspace(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
                      bool fp8, unsigned flags) {
-    if (batch <= 0 || max_q_rows <= 0 || Hkv <= 0 || Hq < Hkv || max_kv_len < 0 || window < 0 || num_sinks < 0)
+    if (batch <= 0 || max_q_rows <= 0 || Hkv <= 0 || Hq < Hkv || max_kv_len < 0 || window < 0 || num_sinks < 0 ||
+        (D != 64 && D != 128))
         return 0;
     if (flags & PKV_FLAG_SIMT_ONLY) return 0;
-    return pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, current_device_sms())
-        .ws_bytes;
+    return plan_ext(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, current_device_sms()).ws_bytes;
 }
 
 // One pool for the few-row kernel: boxes of one head's slots of a page, a whole
@@ -810,10 +855,17 @@ pkv_status ext_attention(const ExtArgs& a) {
         return fail(PKV_ERR_UNSUPPORTED, "%s: flags 0x%x (only CHECKED and SIMT_ONLY)", n, a.flags);
     if ((a.flags & PKV_FLAG_CHECKED) && !a.err)
         return fail(PKV_ERR_INVALID_ARG, "%s: checked mode needs an error flag", n);
-    const size_t ws_bytes = ext_workspace(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim,
-                                          a.max_kv_len, a.window, a.num_sinks, a.fp8, a.flags);
-    if (ws_bytes > 0 && (!a.workspace || a.workspace_bytes < ws_bytes || !aligned(a.workspace, 256)))
-        return fail(PKV_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned", n, ws_bytes);
+    ExtPlan pl;
+    if (!(a.flags & PKV_FLAG_SIMT_ONLY))
+        pl = plan_ext(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim, a.max_kv_len, a.window,
+                      a.num_sinks, a.fp8, current_device_sms());
+    if (pl.ws_bytes > 0 && (!a.workspace || a.workspace_bytes < pl.ws_bytes || !aligned(a.workspace, 256)))
+        return fail(PKV_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned", n, pl.ws_bytes);
+    if (pl.tile && static_cast<int64_t>(a.batch) * pl.splits > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: batch x key splits above 65535", n);
+    if (pl.tile && a.fp8 && static_cast<int64_t>(a.batch) * pl.pages > 0x7fffffff)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: too many pages", n);
+    if (!pl.tile && pl.rows.units > 0x7fff0000) return fail(PKV_ERR_UNSUPPORTED, "%s: too many row tiles", n);
 
     pkv::AttnParams p{};
     p.q = a.q;
@@ -853,15 +905,40 @@ pkv_status ext_attention(const ExtArgs& a) {
     p.num_sinks = a.num_sinks;
     if (a.flags & PKV_FLAG_SIMT_ONLY) return from_cuda(pkv::launch_attn_simt_ext(p, a.stream), n);
 
-    const pkv::RowsPlan rp = pkv::plan_attn_rows(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim,
-                                                 a.max_kv_len, a.window, a.num_sinks, a.fp8, current_device_sms());
-    if (rp.units > 0x7fffff00) return fail(PKV_ERR_UNSUPPORTED, "%s: too many row tiles", n);
     CUtensorMap tk, tv;
-    pkv_status st = make_rows_map(&tk, a.k_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+    pkv_status st;
+    if (!pl.tile) {
+        st = make_rows_map(&tk, a.k_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+        if (st != PKV_OK) return st;
+        st = make_rows_map(&tv, a.v_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+        if (st != PKV_OK) return st;
+        return from_cuda(pkv::launch_attn_rows(p, pl.rows, a.workspace, &tk, &tv, a.stream), n);
+    }
+    char* w = static_cast<char*>(a.workspace);
+    if (a.fp8) {
+        const cudaError_t e = pkv::launch_expand_fp8(p, w, w + pl.expand_bytes, pl.pages, a.stream);
+        if (e != cudaSuccess) return from_cuda(e, n);
+        p.k_pool = w;
+        p.v_pool = w + pl.expand_bytes;
+        p.expanded_pages = pl.pages;
+        p.num_pages = static_cast<int64_t>(a.batch) * pl.pages;
+        p.page_stride = static_cast<int64_t>(32) * a.num_kv_heads * a.head_dim;
+        w += 2 * pl.expand_bytes;
+    }
+    p.num_splits = pl.splits;
+    p.even_splits = true;
+    if (pl.splits > 1) {
+        p.ws_o = reinterpret_cast<float*>(w);
+        p.ws_lse = reinterpret_cast<float*>(w + pl.states_o);
+    }
+    const int64_t map_pages = std::max<int64_t>(p.num_pages, 1);
+    st = make_pool_map(&tk, p.k_pool, a.head_dim, a.num_kv_heads, 32, map_pages, p.page_stride);
     if (st != PKV_OK) return st;
-    st = make_rows_map(&tv, a.v_pool, a.fp8, a.head_dim, a.num_kv_heads, a.num_pages, a.page_stride);
+    st = make_pool_map(&tv, p.v_pool, a.head_dim, a.num_kv_heads, 32, map_pages, p.page_stride);
     if (st != PKV_OK) return st;
-    return from_cuda(pkv::launch_attn_rows(p, rp, a.workspace, &tk, &tv, a.stream), n);
+    const cudaError_t e = pkv::launch_attn_tc_ext(p, &tk, &tv, a.stream);
+    if (e != cudaSuccess || pl.splits == 1) return from_cuda(e, n);
+    return from_cuda(pkv::launch_split_reduce(p, a.stream), n);
 }
 
 }  // namespace

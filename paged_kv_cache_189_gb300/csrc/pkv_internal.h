@@ -213,6 +213,9 @@ struct AttnParams {
     const float* v_scale;
     int64_t scale_stride;
     int window, num_sinks;
+    // tile kernel over a pool expanded from 8 bits: pages each sequence has there (0: paged pools)
+    int expanded_pages;
+    bool even_splits;  // every split wrote a state for every row
 };
 
 // Decode kernel (one query row per sequence), split-KV, SIMT; K/V pages
@@ -243,6 +246,15 @@ RowsPlan plan_attn_rows(int batch, int max_q_rows, int Hq, int Hkv, int D, int m
                         int num_sinks, bool fp8, int sms);
 cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* workspace, const void* tmap_k,
                              const void* tmap_v, cudaStream_t s);
+
+// The two-tile tensor-core kernel with a window and sinks, over bf16 pools or
+// pools expanded from 8 bits.
+cudaError_t launch_attn_tc_ext(const AttnParams& p, const void* tmap_k, const void* tmap_v, cudaStream_t s);
+
+// The pages of an 8-bit pool that some row of the call sees, as bf16 (code *
+// scale): page p of sequence b at [b][p] of k_out / v_out, [batch][pages][32]
+// [Hkv][D], without the pages between the sinks and the window.
+cudaError_t launch_expand_fp8(const AttnParams& p, void* k_out, void* v_out, int pages, cudaStream_t s);
 
 // Grouped mode of the one-tile tensor-core kernel: one CTA per (group, tile of
 // the group's query tokens, K/V head); each row attends to its group's shared
