@@ -12,12 +12,14 @@
 //
 // One warp per (sequence, touched page, K/V head, K or V): it owns the page's
 // 32 slots of that head, so nothing is shared between warps and the result does
-// not depend on their order.  The warp's rows (16-byte vectors, D * size / 16
-// lanes of them a row) are loaded together and stay in registers between the
-// maximum and the conversion, so every source byte is read once.
+// not depend on their order.  Rows of 2-byte elements (16-byte vectors, D / 8
+// lanes a row) are all loaded at once, before the page is looked up, and stay
+// in registers between the maximum (packed, two elements an instruction) and
+// the conversion: every source byte is read once.  4-byte rows would take 128
+// registers; they are read a second time, from cache.
 // Bound: HBM for chunks (2 bytes read and 1 written per bf16 element), launch
-// and one chain of dependent loads (lengths, page id, row, old scale) for one
-// token per sequence.
+// and one chain of dependent loads (lengths, page id, old scale) for one token
+// per sequence.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -39,29 +41,41 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t pair) {
     return __half22float2(__half2(h));
 }
 
-// The values of one 16-byte vector as f32, infinities brought to the type's
-// largest finite value.
+// One 16-byte vector of the source type: its values as f32, the largest
+// magnitude so far (NaN passed over), the type's largest finite value.
 template <typename T>
 struct Src;
 template <>
 struct Src<__nv_bfloat16> {
     static constexpr int kVec = 8;
+    static constexpr float kTop = 3.3895313892515355e38f;
+    __nv_bfloat162 peak = __floats2bfloat162_rn(0.f, 0.f);
+    __device__ void see(const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) peak = __hmax2(peak, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    }
+    __device__ float top() const { return fmaxf(__low2float(peak), __high2float(peak)); }
     __device__ static void widen(const uint4& v, float (&x)[kVec]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        constexpr float top = 3.3895313892515355e38f;  // 0x7f7f
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = bf16lo(w[i]);
             x[2 * i + 1] = bf16hi(w[i]);
         }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(top, x[i]);
     }
 };
 template <>
 struct Src<__half> {
     static constexpr int kVec = 8;
+    static constexpr float kTop = 65504.f;
+    __half2 peak = __floats2half2_rn(0.f, 0.f);
+    __device__ void see(const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) peak = __hmax2(peak, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    }
+    __device__ float top() const { return fmaxf(__low2float(peak), __high2float(peak)); }
     __device__ static void widen(const uint4& v, float (&x)[kVec]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -70,21 +84,25 @@ struct Src<__half> {
             x[2 * i] = f.x;
             x[2 * i + 1] = f.y;
         }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(65504.f, x[i]);
     }
 };
 template <>
 struct Src<float> {
     static constexpr int kVec = 4;
-    __device__ static void widen(const uint4& v, float (&x)[kVec]) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    static constexpr float kTop = 3.4028234663852886e38f;
+    float peak = 0.f;
+    __device__ void see(const uint4& v) {
+        float x[kVec];
+        widen(v, x);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            x[i] = __uint_as_float(w[i]);
-            if (fabsf(x[i]) == INFINITY) x[i] = copysignf(3.4028234663852886e38f, x[i]);
-        }
+        for (int i = 0; i < kVec; ++i) peak = fmaxf(peak, fabsf(x[i]));
+    }
+    __device__ float top() const { return peak; }
+    __device__ static void widen(const uint4& v, float (&x)[kVec]) {
+        x[0] = __uint_as_float(v.x);
+        x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z);
+        x[3] = __uint_as_float(v.w);
     }
 };
 
@@ -96,29 +114,32 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
 
-// x / scale: by the exact reciprocal where the scale is a power of two
-struct Divide {
-    float scale, inv;
-    bool exact;
-    __device__ explicit Divide(float s) : scale(s), inv(s > 0.f ? 1.0f / s : 0.f) {
-        exact = (__float_as_uint(s) & 0x7fffffu) == 0;
-    }
-    __device__ float operator()(float x) const { return exact ? x * inv : x / scale; }
-};
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&y)[N]) {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        w[i] = to_e4m3x2(y[4 * i], y[4 * i + 1]) | (to_e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+    if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) append_fp8_kernel(const AppendArgs a, int pages_bound) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 5 : 8)
+    append_fp8_kernel(const __grid_constant__ AppendArgs a, int pages_bound) {
     constexpr int kVec = Src<T>::kVec;          // elements of a lane's vector
     constexpr int kLanes = D / kVec;            // lanes a row takes
     constexpr int kRows = 32 / kLanes;          // rows of one warp-wide load
     constexpr int kSteps = kPage / kRows;
+    constexpr bool kKeep = sizeof(T) == 2;
     const int lane = threadIdx.x & 31;
     const int Hkv = a.num_kv_heads;
     const int b = blockIdx.y;
     const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (page, K or V, head), heads fastest
     const int t = item / (2 * Hkv);
     if (t >= pages_bound) return;
-    const int which = (item / Hkv) & 1, h = item % Hkv;
+    const int rest = item - t * 2 * Hkv;
+    const int which = rest >= Hkv ? 1 : 0, h = rest - which * Hkv;
 
     const int r0 = a.q_indptr[b];
     const int rows = a.q_indptr[b + 1] - r0, nrows = min(rows, a.max_q_rows);
@@ -132,78 +153,94 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp8_kernel(const AppendArg
     const int first = kv_len - qreal;                 // position of the first new row (may be below 0)
     const int pos0 = (max(first, 0) / kPage + t) * kPage;  // this page's first position
     if (pos0 >= kv_len) return;
+    const int begin = max(first - pos0, 0), end = min(kv_len - pos0, kPage);  // slots that receive rows
+
+    const int sub = lane / kLanes, col = (lane % kLanes) * kVec;
+    const T* src = static_cast<const T*>(a.src[which]) +
+                   (static_cast<int64_t>(r0) - first + pos0 + sub) * a.src_token_stride +
+                   static_cast<int64_t>(h) * a.src_head_stride + col;
+    const int64_t step = a.src_token_stride * kRows;
+    auto row = [&](int s) {
+        return s * kRows + sub >= begin && s * kRows + sub < end
+                   ? __ldg(reinterpret_cast<const uint4*>(src + s * step)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 v[kKeep ? kSteps : 1];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) v[s] = row(s);
+    }
     const int page = a.block_table[b * a.block_table_stride + pos0 / kPage];
     if (page < 0 || page >= a.num_pages) {
         if (a.checked && lane == 0) set_err(a.err, PKV_ERRBIT_PAGE);
         return;
     }
-    const int begin = max(first - pos0, 0), end = min(kv_len - pos0, kPage);  // slots that receive rows
     float* sp = a.scale[which] + page * a.scale_stride + h;
     const float had = begin > 0 ? *sp : 0.f;
 
-    const int sub = lane / kLanes, col = (lane % kLanes) * kVec;
-    const T* src = static_cast<const T*>(a.src[which]) + (static_cast<int64_t>(r0) - first + pos0) * a.src_token_stride +
-                   static_cast<int64_t>(h) * a.src_head_stride + col;
-    uint4 v[kSteps];
+    Src<T> peak;
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int slot = s * kRows + sub;
-        v[s] = slot >= begin && slot < end
-                   ? __ldg(reinterpret_cast<const uint4*>(src + slot * a.src_token_stride))
-                   : make_uint4(0u, 0u, 0u, 0u);
+        for (int s = 0; s < kSteps; ++s) peak.see(v[s]);
+    } else {
+#pragma unroll 8
+        for (int s = 0; s < kSteps; ++s) peak.see(row(s));
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        float x[kVec];
-        Src<T>::widen(v[s], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf passes NaN over
-    }
-    const float scale = fmaxf(had, scale_for(warp_max(amax)));
-    const Divide div(scale);
-    uint8_t* dst = a.pool[which] + page * a.page_stride + static_cast<int64_t>(h) * D + col;
+    const float amax = warp_max(peak.top());
+    const float scale = fmaxf(had, scale_for(fminf(amax, Src<T>::kTop)));
+    const float inv = scale > 0.f ? 1.0f / scale : 0.f;
+    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;  // a power of two: its reciprocal is exact
     const int64_t slot_stride = static_cast<int64_t>(Hkv) * D;
-    auto store = [&](int slot, const float (&y)[kVec]) {
-        uint32_t w[kVec / 4];
-#pragma unroll
-        for (int i = 0; i < kVec / 4; ++i)
-            w[i] = to_e4m3x2(y[4 * i], y[4 * i + 1]) | (to_e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
-        if constexpr (kVec == 8) *reinterpret_cast<uint2*>(dst + slot * slot_stride) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(dst + slot * slot_stride) = w[0];
-    };
+    uint8_t* dst = a.pool[which] + page * a.page_stride + sub * slot_stride + static_cast<int64_t>(h) * D + col;
     // the scale grew: the page's earlier codes, to the new one
     if (begin > 0 && scale != had) {
-        for (int slot = sub; slot < begin; slot += kRows) {
+#pragma unroll 1
+        for (int s = 0; s * kRows + sub < begin; ++s) {
+            uint8_t* at = dst + s * kRows * slot_stride;
             uint32_t w[kVec / 4];
             if constexpr (kVec == 8) {
-                const uint2 c = *reinterpret_cast<const uint2*>(dst + slot * slot_stride);
+                const uint2 c = *reinterpret_cast<const uint2*>(at);
                 w[0] = c.x;
                 w[1] = c.y;
             } else {
-                w[0] = *reinterpret_cast<const uint32_t*>(dst + slot * slot_stride);
+                w[0] = *reinterpret_cast<const uint32_t*>(at);
             }
             float y[kVec];
 #pragma unroll
             for (int i = 0; i < kVec / 4; ++i) {
                 const float2 lo = from_e4m3x2(w[i] & 0xffffu), hi = from_e4m3x2(w[i] >> 16);
-                y[4 * i] = div(lo.x * had);
-                y[4 * i + 1] = div(lo.y * had);
-                y[4 * i + 2] = div(hi.x * had);
-                y[4 * i + 3] = div(hi.y * had);
+                const float o[4] = {lo.x * had, lo.y * had, hi.x * had, hi.y * had};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[4 * i + e] = exact ? o[e] * inv : o[e] / scale;
             }
-            store(slot, y);
+            store_codes<kVec>(at, y);
         }
     }
+    if (exact && amax != INFINITY) {
+#pragma unroll(kKeep ? kSteps : 4)
+        for (int s = 0; s < kSteps; ++s) {
+            if (s * kRows + sub >= begin && s * kRows + sub < end) {
+                float x[kVec];
+                if constexpr (kKeep) Src<T>::widen(v[s], x);
+                else Src<T>::widen(row(s), x);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int slot = s * kRows + sub;
-        if (slot >= begin && slot < end) {
-            float x[kVec];
-            Src<T>::widen(v[s], x);
+                for (int i = 0; i < kVec; ++i) x[i] *= inv;
+                store_codes<kVec>(dst + s * kRows * slot_stride, x);
+            }
+        }
+    } else {
+        // infinities among the rows, or an old scale that is no power of two
+#pragma unroll 1
+        for (int s = 0; s < kSteps; ++s) {
+            if (s * kRows + sub >= begin && s * kRows + sub < end) {
+                float x[kVec];
+                Src<T>::widen(row(s), x);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) x[i] = div(x[i]);
-            store(slot, x);
+                for (int i = 0; i < kVec; ++i) {
+                    if (fabsf(x[i]) == INFINITY) x[i] = copysignf(Src<T>::kTop, x[i]);
+                    x[i] = exact ? x[i] * inv : x[i] / scale;
+                }
+                store_codes<kVec>(dst + s * kRows * slot_stride, x);
+            }
         }
     }
     if (lane == 0) *sp = scale;
