@@ -48,6 +48,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
@@ -57,7 +58,7 @@ namespace {
 
 constexpr int kPage = 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kRingBytes = 96 * 1024;
+constexpr int kRingBytes = 64 * 1024;
 constexpr float kLazy = 8.0f;         // move the reference only past 2^8 growth
 constexpr float kLowScale = -90.0f;   // log2 of the smallest V scale M follows
 constexpr int kDescs = 8;             // segments the look-up may be ahead
@@ -66,7 +67,9 @@ constexpr int kBatches = 1;           // batches of 32 chunks it may be ahead
 
 template <int D, bool FP8, int NT>
 struct Cfg {
-    static constexpr int kWarps = NT == 1 ? 6 : 4;       // consumers (their registers set the count)
+    static constexpr int kWarps = 4;                     // consumers
+    static constexpr int kChunks = 1;                    // chunks a consumer takes at once
+    static constexpr int kRedRows = 4;                   // rows joined at a time
     static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kKeys = FP8 ? 32 : 16;          // keys of a chunk
     static constexpr int kTile = kKeys * D * (FP8 ? 1 : 2);
@@ -75,15 +78,17 @@ struct Cfg {
     static constexpr int kOwn = kStages / kWarps;        // stages of one consumer
     static constexpr int kRows = 8 * NT;
     static constexpr int kRedStride = D + 4;
-    static constexpr int kRedOff = kRingBytes;                              // [warps][4][kRedStride] f32
-    static constexpr int kStatOff = kRedOff + kWarps * 4 * kRedStride * 4;  // m, l, l_b: [warps][kRows]
-    static constexpr int kMetaOff = kStatOff + 3 * kWarps * kRows * 4;      // [stages] (ks, vs, key0)
+    static constexpr int kRedOff = kRingBytes;                              // [warps][kRedRows][kRedStride] f32
+    static constexpr int kStatOff = kRedOff + kWarps * kRedRows * kRedStride * 4;  // m, l, l_b: [warps][kRows]
+    static constexpr int kQOff = (kStatOff + 3 * kWarps * kRows * 4 + 15) & ~15;   // [NT][D / 32][lanes] 16 bytes
+    static constexpr int kFacOff = kQOff + NT * (D / 32) * 512;                    // [kRows] score factors
+    static constexpr int kMetaOff = kFacOff + kRows * 4;                    // [stages] (ks, vs, key0)
     static constexpr int kDescOff = kMetaOff + kStages * 16;
     static constexpr int kQueueOff = kDescOff + kDescs * 64;          // [batches][32] look-ups
     static constexpr int kHeadOff = kQueueOff + kBatches * 32 * 16;   // [batches] (chunks, K/V head)
-    static constexpr int kFlagOff = kHeadOff + kBatches * 8;  // set when a consumer's wait gave up
+    static constexpr int kFlagOff = kHeadOff + kBatches * 8;  // a consumer's wait gave up; segments staged
     // full, empty [stages], dfull, dempty [descs], bfull, bempty [batches]
-    static constexpr int kBarOff = (kFlagOff + 4 + 7) & ~7;
+    static constexpr int kBarOff = kFlagOff + 8;
     static constexpr int kBytes = kBarOff + (2 * kStages + 2 * kDescs + 2 * kBatches) * 8;
     static_assert(kStages % kWarps == 0, "each consumer owns whole stages");
     static_assert((kBytes + 1024) * kCtasPerSm <= 228 * 1024, "CTAs per SM must fit in shared memory");
@@ -94,6 +99,7 @@ struct RowsArgs {
     AttnParams p;
     int ctas;       // CTAs that share the line (0: one CTA a unit)
     int tiles_max;  // row tiles of a sequence at the host bound
+    bool even;      // all pieces fixed
     // written by the planner
     int* ticket;
     int2* cuts;         // [units] first slot and number of its partial states; 0: none
@@ -108,12 +114,15 @@ struct RowsArgs {
 // q1 up to A2 and of q2 up to T.
 struct Line {
     int T, A1, A2, first, size, longer, n1, n2, q1, q2;
-    __device__ __forceinline__ Line(int total, int ctas) {
-        // 70 % fixed, 20 % in tenths and 10 % in twentieths of a CTA's average
-        // share; pieces of at least 12 and 6 chunks, fixed ones of at least 8
+    __device__ __forceinline__ Line(int total, int ctas, bool even) {
+        // 85 % fixed, 10 % in tenths and 5 % in twentieths of a CTA's average
+        // share; pieces of at least 12 and 6 chunks, fixed ones of at least 8.
+        // Few long units: all fixed, else the last ones fall into a hundred
+        // states each (three sequences of 10^5 keys: 88 us against 94; 64
+        // ragged sequences: 114 against 108 the other way round).
         T = total;
-        A1 = T / 10 * 7;
-        A2 = T / 10 * 9;
+        A1 = even ? T : T / 20 * 17;
+        A2 = even ? T : T / 20 * 19;
         first = min(max(A1 / 8, 1), ctas);
         size = A1 / first;
         longer = A1 - size * first;  // the first so many pieces have one more
@@ -306,17 +315,29 @@ __device__ __forceinline__ void row_range(const AttnParams& p, const Desc& s, in
     lo = p.window > 0 ? s.kv_len - s.qreal + tok - p.window + 1 : 0;
 }
 
-// One chunk: scores, weights and the output update.  MASKED: some key of it is
+// The chunks of one step: shared-memory addresses of K (V follows), scales and
+// first keys.
+template <int NC>
+struct Chunks {
+    uint32_t kb[NC];
+    float ks[NC], vs[NC];
+    int key0[NC];
+};
+
+// NC chunks: scores, weights and the output update.  Two at once where there
+// are two: their chains of matrix steps, maxima and exponentials run beside
+// each other, and the row statistics move once.  MASKED: some key of them is
 // hidden from some row.
-template <int D, bool FP8, int NT, bool MASKED>
-__device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf)[NT][D / 16][2],
-                                           const float (&fq)[NT][2], const AttnParams& p, const Desc& ds, int G,
-                                           uint32_t kb, uint32_t vb, float ks, float vs, int key0, int lane) {
+template <int D, bool FP8, int NT, int NC, bool MASKED>
+__device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const float (&fq)[NT][2],
+                                           const AttnParams& p, const Desc& ds, int G, const Chunks<NC>& ch,
+                                           int lane) {
     using C = Cfg<D, FP8, NT>;
-    constexpr int MI = C::kKeys / 16;
+    constexpr int MI = C::kKeys / 16;  // 16-key tiles of a chunk
+    constexpr int MT = NC * MI;
     const int g = lane >> 2, t = lane & 3;
-    // ---- S^T = K Q^T, the steps of two independent accumulators in turn
-    constexpr int SA = FP8 ? MI : 2;  // accumulators: 16 keys each (8 bits), every other step (bf16)
+    // ---- S^T = K Q^T, the steps of independent accumulators in turn
+    constexpr int SA = FP8 || MT > 1 ? MT : 2;  // one tile: every other step to a second accumulator
     float s[SA][NT][4];
 #pragma unroll
     for (int x = 0; x < SA; ++x)
@@ -325,46 +346,67 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[x][j][e] = 0.f;
     if constexpr (FP8) {
-        // this lane's keys: g, g + 8, g + 16, g + 24
-        const uint32_t a0 = kb + g * D + (D == 128 ? ((2 * t) ^ g) << 4 : (t ^ ((g >> 1) & 3)) << 4);
+        // this lane's keys of a chunk: g, g + 8, g + 16, g + 24
+        const uint32_t a0 = g * D + (D == 128 ? ((2 * t) ^ g) << 4 : (t ^ ((g >> 1) & 3)) << 4);
+        constexpr int MG = NT == 1 ? 2 : 1;  // tiles in turn (two row tiles make two chains already)
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            uint4 w[2 * MI];
+        for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-            for (int r = 0; r < 2 * MI; ++r) w[r] = lds128((a0 ^ (i << 4)) + r * 8 * D);
+            for (int m0 = 0; m0 < MT; m0 += MG) {
+                uint4 w[2 * MG];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+                for (int r = 0; r < 2 * MG; ++r)
+                    w[r] = lds128(ch.kb[m0 / MI] + (a0 ^ (i << 4)) + ((m0 % MI) * 2 + r) * 8 * D);
 #pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    uint32_t a[4];
-                    widen4(word(w[2 * mi], k), a[0], a[2]);
-                    widen4(word(w[2 * mi + 1], k), a[1], a[3]);
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    uint4 q[NT];  // steps 2 k2 and 2 k2 + 1
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) mma<FP8>(s[mi][j], a, qf[j][4 * i + k][0], qf[j][4 * i + k][1]);
+                    for (int j = 0; j < NT; ++j) q[j] = lds128(qb + (j * (D / 32) + 2 * i + k2) * 512);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int mi = 0; mi < MG; ++mi) {
+                            uint32_t a[4];
+                            widen4(word(w[2 * mi], 2 * k2 + k), a[0], a[2]);
+                            widen4(word(w[2 * mi + 1], 2 * k2 + k), a[1], a[3]);
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma<FP8>(s[m0 + mi][j], a, word(q[j], 2 * k), word(q[j], 2 * k + 1));
+                        }
                 }
-        }
+            }
     } else {
-        const uint32_t a0 = kb + g * 128 + (((2 * t) ^ g) << 4);
+        const uint32_t a0 = g * 128 + (((2 * t) ^ g) << 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            const uint32_t ad = (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
-            const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
-            const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
+            uint4 q[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma<FP8>(s[0][j], x0, qf[j][2 * i][0], qf[j][2 * i][1]);
+            for (int j = 0; j < NT; ++j) q[j] = lds128(qb + (j * (D / 32) + i) * 512);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma<FP8>(s[1][j], x1, qf[j][2 * i + 1][0], qf[j][2 * i + 1][1]);
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t ad = ch.kb[m] + (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
+                const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
+                const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma<FP8>(s[m][j], x0, q[j].x, q[j].y);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma<FP8>(s[MT > 1 ? m : 1][j], x1, q[j].z, q[j].w);
+            }
         }
+        if constexpr (MT == 1)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
+                for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
     }
     // ---- weights
-    float lv = 0.f;  // log2 of the V scale, rounded down
-    if constexpr (FP8)
-        lv = fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(vs) >> 23) & 255u) - 127), kLowScale);
-    uint32_t pb[NT][MI][2];
+    float lv[NC];  // log2 of the V scales, rounded down
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        lv[c] = FP8 ? fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(ch.vs[c]) >> 23) & 255u) - 127),
+                            kLowScale)
+                    : 0.f;
+    uint32_t pb[NT][MT][2];
     bool moved = false;
     float alpha[NT][2];
 #pragma unroll
@@ -372,26 +414,30 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
         float ref[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float f = FP8 ? fq[j][e] * ks : fq[j][e];
             int lim = 0, lo = 0;
             if constexpr (MASKED) row_range(p, ds, (ds.row0 + 8 * j + 2 * t + e) / G, lo, lim);
             float mx = -INFINITY;
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
+            for (int c = 0; c < NC; ++c) {
+                const float f = FP8 ? fq[j][e] * ch.ks[c] : fq[j][e];
+                float mc = -INFINITY;
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    float x = s[mi][j][2 * hh + e] * f;
-                    if constexpr (MASKED) {
-                        const int key = key0 + 16 * mi + 8 * hh + g;
-                        if (!(key < lim && (key >= lo || key < p.num_sinks))) x = -INFINITY;
+                for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float x = s[c * MI + mi][j][2 * hh + e] * f;
+                        if constexpr (MASKED) {
+                            const int key = ch.key0[c] + 16 * mi + 8 * hh + g;
+                            if (!(key < lim && (key >= lo || key < p.num_sinks))) x = -INFINITY;
+                        }
+                        s[c * MI + mi][j][2 * hh + e] = x;
+                        mc = fmaxf(mc, x);
                     }
-                    s[mi][j][2 * hh + e] = x;
-                    mx = fmaxf(mx, x);
-                }
+                mx = fmaxf(mx, FP8 ? mc + lv[c] : mc);
+            }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if constexpr (FP8) mx += lv;
             alpha[j][e] = 1.f;
             if (mx > st.m[j][e] + kLazy) {  // also the first visible key
                 alpha[j][e] = fast_exp2(st.m[j][e] - mx);
@@ -402,21 +448,21 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
         }
         float sum[2] = {0.f, 0.f}, sumb[2] = {0.f, 0.f};
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                const float p0 = fast_exp2(s[mi][j][2 * hh] - ref[0]), p1 = fast_exp2(s[mi][j][2 * hh + 1] - ref[1]);
+                const float p0 = fast_exp2(s[m][j][2 * hh] - ref[0]), p1 = fast_exp2(s[m][j][2 * hh + 1] - ref[1]);
                 sum[0] += p0;
                 sum[1] += p1;
                 uint32_t w;
                 if constexpr (FP8) {
-                    w = pack_f16x2(p0 * vs, p1 * vs);
+                    w = pack_f16x2(p0 * ch.vs[m / MI], p1 * ch.vs[m / MI]);
                 } else {
                     w = pack_bf16x2(p0, p1);
                     sumb[0] += bf16lo(w);
                     sumb[1] += bf16hi(w);
                 }
-                pb[j][mi][hh] = movmatrix(w);  // (key g; rows 2t, 2t + 1) -> (row g; keys 2t, 2t + 1)
+                pb[j][m][hh] = movmatrix(w);  // (key g; rows 2t, 2t + 1) -> (row g; keys 2t, 2t + 1)
             }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -433,59 +479,62 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
                 for (int e = 0; e < 4; ++e) st.o[j][c][e] *= alpha[j][e & 1];
     }
     // ---- O^T += V^T P^T; the V of keys that no row sees may hold anything
-    uint32_t vm[2 * MI];
-    if constexpr (MASKED) {
 #pragma unroll
-        for (int k = 0; k < 2 * MI; ++k) {
-            uint32_t keep = 0;
+    for (int n = 0; n < NC; ++n) {
+        const uint32_t vb = ch.kb[n] + C::kTile;
+        uint32_t vm[2 * MI];
+        if constexpr (MASKED) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = key0 + 8 * k + 2 * t + e;
-                if (key < ds.hi && (key >= ds.lo || key < p.num_sinks)) keep |= 0xffffu << (16 * e);
-            }
-            vm[k] = keep;
-        }
-    }
-    if constexpr (FP8) {
-        constexpr int kRowB = D;
-        const uint32_t x = D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4;
-        const uint32_t a0 = vb + lane * kRowB + x;
+            for (int k = 0; k < 2 * MI; ++k) {
+                uint32_t keep = 0;
 #pragma unroll
-        for (int c0 = 0; c0 < D / 16; c0 += 2) {
-            uint32_t r[2][4];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) ldmatrix_x4_trans(r[c], a0 ^ ((c0 + c) << 4));
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t a[4];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w = r[c][2 * k + q];
-                        if constexpr (MASKED) w &= vm[2 * k + q];
-                        // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
-                        widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c0 + c], a, pb[j][k][0], pb[j][k][1]);
+                for (int e = 0; e < 2; ++e) {
+                    const int key = ch.key0[n] + 8 * k + 2 * t + e;
+                    if (key < ds.hi && (key >= ds.lo || key < p.num_sinks)) keep |= 0xffffu << (16 * e);
                 }
-        }
-    } else {
-        const int row = (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t a0 = vb + row * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            uint32_t r[4];
-            ldmatrix_x4_trans(r, (a0 ^ ((2 * c & 7) << 4)) + (c >> 2) * (C::kKeys * 128));
-            if constexpr (MASKED) {
-                r[0] &= vm[0];
-                r[1] &= vm[0];
-                r[2] &= vm[1];
-                r[3] &= vm[1];
+                vm[k] = keep;
             }
+        }
+        if constexpr (FP8) {
+            const uint32_t a0 = vb + lane * D + (D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c], r, pb[j][0][0], pb[j][0][1]);
+            for (int c0 = 0; c0 < D / 16; c0 += 2) {
+                uint32_t r[2][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) ldmatrix_x4_trans(r[c], a0 ^ ((c0 + c) << 4));
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t a[4];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w = r[c][2 * k + q];
+                            if constexpr (MASKED) w &= vm[2 * k + q];
+                            // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
+                            widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            mma<FP8>(st.o[j][c0 + c], a, pb[j][n * MI + k][0], pb[j][n * MI + k][1]);
+                    }
+            }
+        } else {
+            const int row = (lane & 7) + ((lane >> 4) << 3);
+            const uint32_t a0 = vb + row * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t r[4];
+                ldmatrix_x4_trans(r, (a0 ^ ((2 * c & 7) << 4)) + (c >> 2) * (C::kKeys * 128));
+                if constexpr (MASKED) {
+                    r[0] &= vm[0];
+                    r[1] &= vm[0];
+                    r[2] &= vm[1];
+                    r[3] &= vm[1];
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c], r, pb[j][n][0], pb[j][n][1]);
+            }
         }
     }
 }
@@ -500,42 +549,30 @@ __device__ __forceinline__ void fetch_q_row(const __nv_bfloat16* q, bool exists,
         v[i] = exists ? __ldg(reinterpret_cast<const uint4*>(q + at)) : make_uint4(0u, 0u, 0u, 0u);
     }
 }
-// The same as the score product's B operand; returns the factor that undoes
-// the row's scaling (1 for bf16 pools).
+// The same as the score product's B operand, two steps a vector; returns the
+// factor that undoes the row's scaling (1 for bf16 pools).
 template <int D, bool FP8>
-__device__ __forceinline__ float pack_q(const uint4 (&v)[D / 32], uint32_t (&f)[D / 16][2]) {
-    float undo = 1.f;
-    if constexpr (FP8) {
-        uint32_t top = 0;
+__device__ __forceinline__ float pack_q(uint4 (&v)[D / 32]) {
+    if constexpr (!FP8) return 1.f;
+    uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w = word(v[i], k);
-                top = max(top, max((w >> 7) & 255u, (w >> 23) & 255u));
-            }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = max(top, 9u);
-        const float up = __uint_as_float((262u - top) << 23);  // the largest exponent to 2^8
-        undo = __uint_as_float((top - 8u) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w = word(v[i], k);
-                f[2 * i + (k >> 1)][k & 1] = pack_f16x2(bf16lo(w) * up, bf16hi(w) * up);
-            }
-    } else {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            f[2 * i][0] = v[i].x;
-            f[2 * i][1] = v[i].y;
-            f[2 * i + 1][0] = v[i].z;
-            f[2 * i + 1][1] = v[i].w;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w = word(v[i], k);
+            top = max(top, max((w >> 7) & 255u, (w >> 23) & 255u));
         }
-    }
-    return undo;
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top, 9u);
+    const float up = __uint_as_float((262u - top) << 23);  // the largest exponent to 2^8
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        v[i] = make_uint4(pack_f16x2(bf16lo(v[i].x) * up, bf16hi(v[i].x) * up),
+                          pack_f16x2(bf16lo(v[i].y) * up, bf16hi(v[i].y) * up),
+                          pack_f16x2(bf16lo(v[i].z) * up, bf16hi(v[i].z) * up),
+                          pack_f16x2(bf16lo(v[i].w) * up, bf16hi(v[i].w) * up));
+    return __uint_as_float((top - 8u) << 23);
 }
 
 struct Look {
@@ -570,7 +607,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
     Look* queue = reinterpret_cast<Look*>(smem + C::kQueueOff);
     int2* head = reinterpret_cast<int2*>(smem + C::kHeadOff);
     if (threadIdx.x == 0) {
-        *reinterpret_cast<int*>(smem + C::kFlagOff) = 0;
+        *reinterpret_cast<int2*>(smem + C::kFlagOff) = make_int2(0, 0);
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -641,7 +678,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
                 }
                 if (pass == 0) {
                     T = base;
-                    const Line line(T, a.ctas);
+                    const Line line(T, a.ctas, a.even);
                     if (piece >= line.first) break;
                     int to;
                     line.piece(piece, at, to);
@@ -656,7 +693,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
             w.b = x / a.tiles_max / Hkv;
             w.left = w.mt < sequence<C::kRows>(p, w.b, G).tiles ? 0x7fffffff : 0;
         }
-        const Line line(T, max(a.ctas, 1));
+        const Line line(T, max(a.ctas, 1), a.even);
         const int pieces = line.pieces();
         int nseg = 0, nbatch = 0;
         bool alive = true;
@@ -768,7 +805,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
-        int issued = 0;
+        int issued = 0, gave_up = -1;
         bool alive = true;
         for (int nb = 0; alive; ++nb) {
             const int bs = nb % kBatches;
@@ -780,34 +817,61 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
             if (h.x < 0) break;
             const Look k = queue[bs * 32 + lane];
             mbar_arrive(&bempty[bs]);
-            for (int l = 0; l < h.x; ++l, ++issued) {
-                const int st = issued % S;
-                if (issued >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (issued / S - 1) & 1))) {
-                    alive = false;
-                    break;
-                }
-                if (lane == l) {
-                    uint8_t* kd = smem + st * C::kStage;
-                    uint8_t* vd = kd + C::kTile;
-                    meta[st] = make_float4(k.ks, k.vs, __int_as_float(k.key0), 0.f);
-                    mbar_arrive_expect_tx(&full[st], C::kStage);
-                    if constexpr (FP8) {
-                        tma_load_4d(kd, &tm_k, &full[st], 0, h.y, 0, k.page);
-                        tma_load_4d(vd, &tm_v, &full[st], 0, h.y, 0, k.page);
-                    } else {
+            // as many chunks at once as there are stages: each lane copies one, as
+            // soon as its stage is free (one after the other, a chunk took ~500
+            // cycles of this warp, the limit at head dim 64)
+            constexpr int kAtOnce = S < 32 ? S : 32;
+            for (int l0 = 0; alive && l0 < h.x; l0 += kAtOnce) {
+                const int n = min(kAtOnce, h.x - l0);
+                const int src = l0 + lane;
+                Look c;
+                c.page = __shfl_sync(0xffffffffu, k.page, src & 31);
+                c.key0 = __shfl_sync(0xffffffffu, k.key0, src & 31);
+                c.ks = __shfl_sync(0xffffffffu, k.ks, src & 31);
+                c.vs = __shfl_sync(0xffffffffu, k.vs, src & 31);
+                const int at = issued + lane, st = at % S;
+                bool todo = lane < n;
+                uint64_t t0 = 0;
+                for (uint32_t it = 0; __any_sync(0xffffffffu, todo); ++it) {
+                    if (todo && (at < S || mbar_try_wait(&empty[st], (at / S - 1) & 1))) {
+                        uint8_t* kd = smem + st * C::kStage;
+                        uint8_t* vd = kd + C::kTile;
+                        meta[st] = make_float4(c.ks, c.vs, __int_as_float(c.key0), 0.f);
+                        mbar_arrive_expect_tx(&full[st], C::kStage);
+                        if constexpr (FP8) {
+                            tma_load_4d(kd, &tm_k, &full[st], 0, h.y, 0, c.page);
+                            tma_load_4d(vd, &tm_v, &full[st], 0, h.y, 0, c.page);
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < D / 64; ++x) {
-                            tma_load_4d(kd + x * (C::kKeys * 128), &tm_k, &full[st], x * 64, h.y, k.key0 % kPage, k.page);
-                            tma_load_4d(vd + x * (C::kKeys * 128), &tm_v, &full[st], x * 64, h.y, k.key0 % kPage, k.page);
+                            for (int x = 0; x < D / 64; ++x) {
+                                tma_load_4d(kd + x * (C::kKeys * 128), &tm_k, &full[st], x * 64, h.y, c.key0 % kPage, c.page);
+                                tma_load_4d(vd + x * (C::kKeys * 128), &tm_v, &full[st], x * 64, h.y, c.key0 % kPage, c.page);
+                            }
+                        }
+                        todo = false;
+                    }
+                    if ((it & 63u) == 63u) {
+                        const uint64_t now = global_timer_ns();
+                        if (t0 == 0) t0 = now;
+                        if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {
+                            alive = false;
+                            break;
                         }
                     }
                 }
-                __syncwarp();
+                // (after a wait that gave up: the lanes that did issue are not one
+                // run of stages; every one is waited for below)
+                if (!alive) {
+                    gave_up = todo || lane >= n ? -1 : at;
+                    break;
+                }
+                issued += n;
             }
         }
         if (!alive && lane == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
         // do not leave with copies into this CTA's shared memory in flight
         for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&full[j % S], (j / S) & 1);
+        if (gave_up >= 0) mbar_wait(&full[gave_up % S], (gave_up / S) & 1);
         return;
     }
 
@@ -823,18 +887,26 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
     int own = 0;      // stage of the warp's next chunk among its own, and its phase
     uint32_t phase = 0;
     int turn = 0;     // consumer whose turn the segment's first chunk is
-    uint4 raw[NT][D / 32];
-    bool have = false;  // the segment's query rows are in raw
+    // A segment's query rows, in fragment order in shared memory: tile j is
+    // brought in by warp j, while the segment before it is joined if its
+    // descriptor is there by then.
+    uint4* qs = reinterpret_cast<uint4*>(smem + C::kQOff);
+    float* facs = reinterpret_cast<float*>(smem + C::kFacOff);
+    const uint32_t qb = smem_u32(qs + lane);
+    volatile int* staged = reinterpret_cast<volatile int*>(smem + C::kFlagOff) + 1;  // segments staged
+    uint4 raw[D / 32];
     auto fetch_q = [&](const Desc& s) {
+        const int R = s.row0 + 8 * warp + g;
+        const int tok = R / G, h = s.kvh * G + R % G;
+        fetch_q_row<D, FP8>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(s.r0 + tok) * p.q_token_stride +
+                                static_cast<int64_t>(h) * p.q_head_stride,
+                            tok < s.nrows, t, raw);
+    };
+    auto stage_q = [&] {
+        const float undo = pack_q<D, FP8>(raw);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int R = s.row0 + 8 * j + g;
-            const int tok = R / G, h = s.kvh * G + R % G;
-            fetch_q_row<D, FP8>(static_cast<const __nv_bfloat16*>(p.q) +
-                                    static_cast<int64_t>(s.r0 + tok) * p.q_token_stride +
-                                    static_cast<int64_t>(h) * p.q_head_stride,
-                                tok < s.nrows, t, raw[j]);
-        }
+        for (int i = 0; i < D / 32; ++i) qs[(warp * (D / 32) + i) * 32 + lane] = raw[i];
+        if (t == 0) facs[8 * warp + g] = p.scale_log2 * undo;
     };
     for (int nseg = 0;; ++nseg) {
         const int ds = nseg % kDescs;
@@ -843,19 +915,19 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
         const bool run = !dead && s.n >= 0;
         const int R0 = s.row0;
         State<D, NT> st;
-        if (run) {
-            if (!have) fetch_q(s);
-            float fq[NT][2];  // score factors of this lane's rows
-            uint32_t qf[NT][D / 16][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float undo = pack_q<D, FP8>(raw[j], qf[j]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    fq[j][e] = p.scale_log2;
-                    if constexpr (FP8) fq[j][e] *= __shfl_sync(0xffffffffu, undo, (2 * t + e) * 4);
-                }
+        if (*staged <= nseg) {  // the same for all: written before the last barrier
+            if (run && warp < NT) {
+                fetch_q(s);
+                stage_q();
             }
+            sync();
+        }
+        if (run) {
+            float fq[NT][2];  // score factors of this lane's rows
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) fq[j][e] = facs[8 * j + 2 * t + e];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -868,30 +940,50 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st.o[j][c][e] = 0.f;
             }
-            for (int i = warp >= turn ? warp - turn : warp - turn + NW; i < s.n; i += NW) {
-                const int sg = own * NW + warp;
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) {
-                    dead = true;
-                    break;
+            int i = warp >= turn ? warp - turn : warp - turn + NW;
+            // NC of this warp's chunks; false: a wait gave up
+            auto step = [&](auto nc) -> bool {
+                constexpr int NC = decltype(nc)::value;
+                Chunks<NC> ch;
+                int stage[NC];
+                bool all = true;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int sg = own * NW + warp;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) return false;
+                    const float4 me = meta[sg];
+                    stage[c] = sg;
+                    ch.kb[c] = ring_u + sg * C::kStage;
+                    ch.ks[c] = me.x;
+                    ch.vs[c] = me.y;
+                    ch.key0[c] = __float_as_int(me.z);
+                    all = all && ch.key0[c] + C::kKeys <= s.all_end &&
+                          (ch.key0[c] >= s.all_lo || ch.key0[c] + C::kKeys <= p.num_sinks);
+                    if (++own == C::kOwn) {
+                        own = 0;
+                        phase ^= 1;
+                    }
                 }
-                const float4 me = meta[sg];
-                const int key0 = __float_as_int(me.z);
-                const uint32_t kb = ring_u + sg * C::kStage;
-                const bool whole = key0 + C::kKeys <= s.all_end &&
-                                   (key0 >= s.all_lo || key0 + C::kKeys <= p.num_sinks);
-                if (whole)
-                    chunk_step<D, FP8, NT, false>(st, qf, fq, p, s, G, kb, kb + C::kTile, me.x, me.y, key0, lane);
-                else
-                    chunk_step<D, FP8, NT, true>(st, qf, fq, p, s, G, kb, kb + C::kTile, me.x, me.y, key0, lane);
+                if (all) chunk_step<D, FP8, NT, NC, false>(st, qb, fq, p, s, G, ch, lane);
+                else if constexpr (NC == 1) chunk_step<D, FP8, NT, NC, true>(st, qb, fq, p, s, G, ch, lane);
+                else {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        chunk_step<D, FP8, NT, 1, true>(
+                            st, qb, fq, p, s, G, Chunks<1>{{ch.kb[c]}, {ch.ks[c]}, {ch.vs[c]}, {ch.key0[c]}}, lane);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[sg]);
-                if (++own == C::kOwn) {
-                    own = 0;
-                    phase ^= 1;
+                if (lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) mbar_arrive(&empty[stage[c]]);
                 }
-            }
+                return true;
+            };
+            for (; i + NW * (C::kChunks - 1) < s.n && !dead; i += NW * C::kChunks)
+                dead = !step(std::integral_constant<int, C::kChunks>{});
+            for (; i < s.n && !dead; i += NW) dead = !step(std::integral_constant<int, 1>{});
             turn = (turn + s.n) % NW;
-            // ---- join the warps' states, four rows at a time
+            // ---- join the warps' states, kRedRows rows at a time
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -913,13 +1005,13 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
             set_err(p.err, PKV_ERRBIT_TIMEOUT);
             *abort_flag = 1;
         }
-        auto put_rows = [&](int rg) {
-            if ((t >> 1) == (rg & 1)) {
-                constexpr int RS = C::kRedStride;
-                float* r0 = red + (warp * 4 + 2 * (t & 1)) * RS;
+        constexpr int RR = C::kRedRows, RS = C::kRedStride;
+        auto put_rows = [&](int rg) {  // rows RR rg .. RR rg + RR - 1
+            if (t / (RR / 2) == rg % (8 / RR)) {
+                float* r0 = red + (warp * RR + 2 * (t % (RR / 2))) * RS;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                    const float(&o)[4] = st.o[rg >> 1][c];
+                    const float(&o)[4] = st.o[rg / (8 / RR)][c];
                     if constexpr (FP8) {
                         *reinterpret_cast<float2*>(r0 + 16 * c + 2 * g) = make_float2(o[0], o[2]);
                         *reinterpret_cast<float2*>(r0 + RS + 16 * c + 2 * g) = make_float2(o[1], o[3]);
@@ -934,22 +1026,26 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
         };
         if (run) put_rows(0);
         // the next segment's query rows, on their way while this one is joined
-        have = false;
-        if (NT == 1 && run) {
+        bool ahead = false;
+        if (NT == 1 && run && warp == 0) {
             const int dn = (nseg + 1) % kDescs;
-            have = __all_sync(0xffffffffu, mbar_test(&dfull[dn], ((nseg + 1) / kDescs) & 1)) && desc[dn].n >= 0;
-            if (have) fetch_q(desc[dn]);
+            ahead = __all_sync(0xffffffffu, mbar_test(&dfull[dn], ((nseg + 1) / kDescs) & 1)) && desc[dn].n >= 0;
+            if (ahead) fetch_q(desc[dn]);
         }
         // every consumer passes here once a segment, whether its waits held or not
         sync();
         if (*abort_flag || !run) break;
+        if (NT == 1 && ahead) {  // nobody reads this segment's rows any more
+            stage_q();
+            if (lane == 0) *staged = nseg + 2;
+        }
         const int rows_here = min(C::kRows, s.nrows * G - R0);
-        // rows 4 rg .. 4 rg + 3 of the warps' states in red / red_m / red_l: joined and written,
+        // rows RR rg .. RR rg + RR - 1 of the warps' states in red / red_m / red_l: joined and written,
         // as the result or as a partial state
         auto join_rows = [&](int rg) {
-            for (int e = threadIdx.x; e < 4 * D / 2; e += NW * 32) {
+            for (int e = threadIdx.x; e < RR * D / 2; e += NW * 32) {
                 const int rr = e / (D / 2), d = (e - rr * (D / 2)) * 2;
-                const int r = 4 * rg + rr;
+                const int r = RR * rg + rr;
                 if (r >= rows_here) continue;
                 const int tok = (R0 + r) / G, h = s.kvh * G + (R0 + r) % G;
                 float M = -INFINITY;
@@ -961,7 +1057,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
                         const float f = fast_exp2(red_m[w * C::kRows + r] - M);
-                        const float2 o = *reinterpret_cast<const float2*>(red + (w * 4 + rr) * C::kRedStride + d);
+                        const float2 o = *reinterpret_cast<const float2*>(red + (w * RR + rr) * RS + d);
                         L = fmaf(f, red_l[w * C::kRows + r], L);
                         if constexpr (!FP8) Lb = fmaf(f, red_lb[w * C::kRows + r], Lb);
                         O.x = fmaf(f, o.x, O.x);
@@ -989,8 +1085,8 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
             }
         };
 #pragma unroll
-        for (int rg = 0; rg < C::kRows / 4; ++rg) {
-            if (4 * rg < rows_here) {
+        for (int rg = 0; rg < C::kRows / RR; ++rg) {
+            if (RR * rg < rows_here) {
                 if (rg > 0) {
                     put_rows(rg);
                     sync();
@@ -1055,7 +1151,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_rows_plan_kernel(const __gr
         a.seq_at[p.batch] = base;
     }
     __syncthreads();
-    const Line line(base, a.ctas);
+    const Line line(base, a.ctas, a.even);
     for (int i = threadIdx.x; i < line.pieces(); i += kPlanThreads) {
         int from, to;
         line.piece(i, from, to);
@@ -1272,6 +1368,7 @@ cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* work
     a.p = p;
     a.ctas = pl.ctas;
     a.tiles_max = static_cast<int>(pl.tiles);
+    a.even = pl.units < pl.ctas;
     if (pl.ctas > 0) {
         const RowsSpace x(p.batch, pl.units, pl.ctas, 8 * pl.row_tiles, p.head_dim);
         char* w = static_cast<char*>(workspace);

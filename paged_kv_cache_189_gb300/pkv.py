@@ -133,8 +133,11 @@ def _stream(stream):
     return ctypes.c_void_p(stream)
 
 
+_DTYPES = {torch.bfloat16: PKV_BF16, torch.float16: PKV_F16, torch.float32: PKV_F32}
+
+
 def _dtype(t):
-    return {torch.bfloat16: PKV_BF16, torch.float16: PKV_F16, torch.float32: PKV_F32}[t.dtype]
+    return _DTYPES[t.dtype]
 
 
 def _pool_geometry(pool):
@@ -378,54 +381,91 @@ def shared_prefix_attention(q, k_pool, v_pool, plan, q_indptr, out, *, max_q_len
 
 
 # ----------------------------------------------------------------------------
-def _fp8_geometry(k_pool, v_pool, k_scale, v_scale):
-    """Geometry of two e4m3 pools (float8_e4m3fn or uint8) and their f32 scales
-    ``[num_pages, Hkv]`` (unit head stride)."""
-    n, P, H, D, page_stride = _pool_geometry(k_pool)
-    if k_pool.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_pool.dtype != k_pool.dtype:
-        raise ValueError("8-bit pools must be float8_e4m3fn (or its bytes as uint8)")
-    if v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride():
-        raise ValueError("K and V pools must have the same shape and strides")
-    for sc in (k_scale, v_scale):
-        if sc.dtype != torch.float32 or tuple(sc.shape) != (n, H) or (H > 1 and sc.stride(1) != 1):
-            raise ValueError("scales must be float32 [num_pages, num_kv_heads] with unit head stride")
-    if k_scale.stride(0) != v_scale.stride(0):
-        raise ValueError("K and V scales must have the same page stride")
-    return n, P, H, D, page_stride, max(k_scale.stride(0), H)
+# The entry points below check their tensors here: a wrong type, shape, stride
+# or device raises ValueError before a pointer is handed out.  The checks are
+# written flat, since a small call's cost is its host time.
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _tables(block_table, kv_lens, q_indptr, q_real, batch):
-    """The batch size, after the index tensors' types and layout are checked."""
-    for t in (block_table, kv_lens, q_indptr, q_real):
-        if t is not None and (t.dtype != torch.int32 or (t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1)):
-            raise ValueError("block_table, kv_lens, q_indptr and q_real must be int32 with unit last stride")
+def _pools(k_pool, v_pool):
+    """Shape and page stride of two like pools with dense slots."""
+    shape, st = k_pool.shape, k_pool.stride()
+    if len(shape) != 4:
+        raise ValueError("pools must be [num_pages, page_size, num_kv_heads, head_dim]")
+    n, P, H, D = shape
+    if st[3] != 1 or st[2] != D or st[1] != H * D:
+        raise ValueError("pool slots must be dense [num_kv_heads, head_dim] rows")
+    if v_pool.shape != shape or v_pool.stride() != st or v_pool.dtype != k_pool.dtype:
+        raise ValueError("K and V pools must have the same shape, strides and type")
+    return n, P, H, D, st[0]
+
+
+def _scales(k_scale, v_scale, n, H):
+    """Page stride of the f32 scales ``[num_pages, Hkv]`` (unit head stride)."""
+    st = k_scale.stride()
+    if (k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.shape != (n, H) or
+            v_scale.shape != (n, H) or v_scale.stride() != st or (H > 1 and st[1] != 1)):
+        raise ValueError("scales must be float32 [num_pages, num_kv_heads] with unit head stride, K's and V's alike")
+    return max(st[0], H)
+
+
+def _index(t, count, what):
+    """A dense int32 vector of at least ``count`` entries."""
+    if t.dtype is not _I32 or t.numel() < count or (t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{what} must be a dense int32 vector of at least {count} entries")
+
+
+def _tables(block_table, kv_lens, q_indptr, q_real, batch, keys):
+    """The batch size and the table's row stride, for up to ``keys`` keys a row."""
     if batch is None:
         batch = kv_lens.numel()
-    if (block_table.dim() != 2 or block_table.shape[0] < batch or kv_lens.numel() < batch or
-            q_indptr.numel() < batch + 1 or (q_real is not None and q_real.numel() < batch)):
-        raise ValueError("block_table, kv_lens, q_indptr or q_real too short for the batch")
-    return batch
-
-
-def _on_device(*tensors):
-    """All on the current CUDA device: the launch goes there."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, the current CUDA device is {dev}")
+    _index(kv_lens, batch, "kv_lens")
+    _index(q_indptr, batch + 1, "q_indptr")
+    if q_real is not None:
+        _index(q_real, batch, "q_real")
+    if block_table.dtype is not _I32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, pages]")
+    st, shape = block_table.stride(), block_table.shape
+    if shape[0] < batch or (st[1] != 1 and shape[1] > 1) or shape[1] * 32 < keys:
+        raise ValueError("block_table must have a row of max_kv_len / 32 pages per sequence and unit last stride")
+    return batch, shape[1] if shape[0] == 1 else st[0]
 
 
 def _states(q, out, lse, D):
-    """Checks of packed query rows and the states they produce."""
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1:
+    """Token and head stride of packed query rows, after the outputs are checked."""
+    shape, st = q.shape, q.stride()
+    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != D or st[2] != 1:
         raise ValueError("q must be bf16 [rows, num_q_heads, head_dim] with unit last stride")
-    if out.shape != q.shape or not out.is_contiguous():
+    if out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be dense with the shape of q")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse must be dense float32 [rows, num_q_heads]")
+    return st
 
 
-def _workspace(workspace):
+def _on_device(tensors):
+    """All on the current CUDA device: the launch goes there."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("tensors must be on one CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _launch_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(workspace):
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
@@ -434,21 +474,26 @@ def kv_append_fp8(k_src, v_src, block_table, kv_lens, q_indptr, k_pool, v_pool, 
     """Quantise this step's rows ``k_src``/``v_src [rows, Hkv, D]`` (bf16, f16
     or f32, any token/head stride of whole 16 bytes) into e4m3 pools and their
     per-page, per-head scales, in place (see ``include/pkv.h``)."""
-    n, P, H, D, page_stride, scale_stride = _fp8_geometry(k_pool, v_pool, k_scale, v_scale)
-    if k_src.shape != v_src.shape or k_src.stride() != v_src.stride() or k_src.dtype != v_src.dtype:
+    n, P, H, D, page_stride = _pools(k_pool, v_pool)
+    if k_pool.dtype not in _FP8_TYPES:
+        raise ValueError("8-bit pools must be float8_e4m3fn (or its bytes as uint8)")
+    scale_stride = _scales(k_scale, v_scale, n, H)
+    shape, st = k_src.shape, k_src.stride()
+    if v_src.shape != shape or v_src.stride() != st or v_src.dtype != k_src.dtype:
         raise ValueError("k_src and v_src must have the same shape, strides and dtype")
-    if k_src.dim() != 3 or tuple(k_src.shape[1:]) != (H, D) or k_src.stride(2) != 1:
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or st[2] != 1:
         raise ValueError("sources must be [rows, num_kv_heads, head_dim] with unit last stride")
-    if k_src.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+    if k_src.dtype not in (_BF16, torch.float16, _F32):
         raise ValueError("sources must be bf16, f16 or f32")
-    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
-    _on_device(k_src, v_src, block_table, kv_lens, q_indptr, q_real, k_pool, v_pool, k_scale, v_scale, err)
-    st = lib().kv_append_fp8(
-        _ptr(k_src), _ptr(v_src), _dtype(k_src), k_src.stride(0), k_src.stride(1), _ptr(block_table),
-        block_table.stride(0), _ptr(kv_lens), _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len,
-        H, D, _ptr(k_pool), _ptr(v_pool), n, P, page_stride, _ptr(k_scale), _ptr(v_scale), scale_stride,
-        PKV_FLAG_CHECKED if checked else 0, _ptr(err), _stream(stream))
-    _check("kv_append_fp8", st)
+    batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    dev = _on_device((k_src, v_src, block_table, kv_lens, q_indptr, q_real, k_pool, v_pool, k_scale, v_scale, err))
+    status = lib().kv_append_fp8(
+        k_src.data_ptr(), v_src.data_ptr(), _dtype(k_src), st[0], st[1], block_table.data_ptr(), table_stride,
+        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, H, D,
+        k_pool.data_ptr(), v_pool.data_ptr(), n, P, page_stride, k_scale.data_ptr(), v_scale.data_ptr(),
+        scale_stride, PKV_FLAG_CHECKED if checked else 0, _address(err), _launch_stream(stream, dev))
+    if status:
+        _check("kv_append_fp8", status)
 
 
 def paged_attention_fp8_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len,
@@ -464,17 +509,22 @@ def paged_attention_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_len
     """``paged_attention`` over e4m3 pools with a scale per page and head (as
     :func:`kv_append_fp8` writes them); ``window`` > 0 limits causal rows to
     their last ``window`` keys and the first ``num_sinks``."""
-    n, P, H, D, page_stride, scale_stride = _fp8_geometry(k_pool, v_pool, k_scale, v_scale)
-    _states(q, out, lse, D)
-    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
-    _on_device(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err)
-    st = lib().paged_attention_fp8(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-        scale_stride, n, P, page_stride, _ptr(block_table), block_table.stride(0), _ptr(kv_lens),
-        _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len, q.shape[1], H, D, MASKS[mask],
-        causal_block, window, num_sinks, float(scale), _ptr(out), _dtype(out), _ptr(lse), _ptr(workspace),
-        _workspace(workspace), flags, _ptr(err), _stream(stream))
-    _check("paged_attention_fp8", st)
+    n, P, H, D, page_stride = _pools(k_pool, v_pool)
+    if k_pool.dtype not in _FP8_TYPES:
+        raise ValueError("8-bit pools must be float8_e4m3fn (or its bytes as uint8)")
+    scale_stride = _scales(k_scale, v_scale, n, H)
+    st = _states(q, out, lse, D)
+    batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    dev = _on_device((q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, q_real, out, lse,
+                      workspace, err))
+    status = lib().paged_attention_fp8(
+        q.data_ptr(), st[0], st[1], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        scale_stride, n, P, page_stride, block_table.data_ptr(), table_stride, kv_lens.data_ptr(),
+        q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, q.shape[1], H, D, MASKS[mask],
+        causal_block, window, num_sinks, scale, out.data_ptr(), _dtype(out), _address(lse), _address(workspace),
+        _bytes(workspace), flags, _address(err), _launch_stream(stream, dev))
+    if status:
+        _check("paged_attention_fp8", status)
 
 
 def paged_attention_window_workspace_size(batch, max_q_rows, num_q_heads, num_kv_heads, head_dim, max_kv_len,
@@ -489,17 +539,17 @@ def paged_attention_window(q, k_pool, v_pool, block_table, kv_lens, q_indptr, ou
     """Causal ``paged_attention`` of bf16 pools in which a row sees its last
     ``window`` keys (its own among them) and the first ``num_sinks``; pages
     that no row sees are not read."""
-    n, P, H, D, page_stride = _pool_geometry(k_pool)
-    if k_pool.dtype != torch.bfloat16 or v_pool.dtype != torch.bfloat16:
+    n, P, H, D, page_stride = _pools(k_pool, v_pool)
+    if k_pool.dtype is not _BF16:
         raise ValueError("pools must be bf16")
-    if v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride():
-        raise ValueError("K and V pools must have the same shape and strides")
-    _states(q, out, lse, D)
-    batch = _tables(block_table, kv_lens, q_indptr, q_real, batch)
-    _on_device(q, k_pool, v_pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err)
-    st = lib().paged_attention_window(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pool), _ptr(v_pool), n, P, page_stride, _ptr(block_table),
-        block_table.stride(0), _ptr(kv_lens), _ptr(q_indptr), _ptr(q_real), batch, max_q_rows, max_kv_len,
-        q.shape[1], H, D, window, num_sinks, float(scale), _ptr(out), _dtype(out), _ptr(lse),
-        _ptr(workspace), _workspace(workspace), flags, _ptr(err), _stream(stream))
-    _check("paged_attention_window", st)
+    st = _states(q, out, lse, D)
+    batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    dev = _on_device((q, k_pool, v_pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err))
+    status = lib().paged_attention_window(
+        q.data_ptr(), st[0], st[1], k_pool.data_ptr(), v_pool.data_ptr(), n, P, page_stride,
+        block_table.data_ptr(), table_stride, kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch,
+        max_q_rows, max_kv_len, q.shape[1], H, D, window, num_sinks, scale, out.data_ptr(), _dtype(out),
+        _address(lse), _address(workspace), _bytes(workspace), flags, _address(err),
+        _launch_stream(stream, dev))
+    if status:
+        _check("paged_attention_window", status)
