@@ -57,8 +57,6 @@ namespace pkv {
 namespace {
 
 constexpr int kPage = 32;
-constexpr int kCtasPerSm = 2;
-constexpr int kRingBytes = 64 * 1024;
 constexpr float kLazy = 8.0f;         // move the reference only past 2^8 growth
 constexpr float kLowScale = -90.0f;   // log2 of the smallest V scale M follows
 constexpr int kDescs = 8;             // segments the look-up may be ahead
@@ -68,6 +66,9 @@ constexpr int kBatches = 1;           // batches of 32 chunks it may be ahead
 template <int D, bool FP8, int NT>
 struct Cfg {
     static constexpr int kWarps = 4;                     // consumers
+    // 64-wide heads leave registers and ring space for a third CTA
+    static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 3 : 2;
+    static constexpr int kRingBytes = (kCtasPerSm == 3 ? 48 : 64) * 1024;
     static constexpr int kChunks = 1;                    // chunks a consumer takes at once
     static constexpr int kRedRows = 4;                   // rows joined at a time
     static constexpr int kThreads = (kWarps + 2) * 32;
@@ -581,7 +582,7 @@ struct Look {
 };
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), kCtasPerSm)
+__global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>::kCtasPerSm))
     attn_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ RowsArgs a) {
     using C = Cfg<D, FP8, NT>;
@@ -1356,7 +1357,7 @@ RowsPlan plan_attn_rows(int batch, int max_q_rows, int Hq, int Hkv, int D, int m
     if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + R + std::min(num_sinks, max_kv_len) + 62);
     const double places = static_cast<double>(pl.units) * (std::min<double>(keys, max_kv_len) / 16 + 3);
     if (keys * 2 * D * (fp8 ? 1 : 2) <= kDirectBytes || pl.tiles > kCutTiles || places > 2e9) return pl;  // the line is counted in 32 bits
-    pl.ctas = kCtasPerSm * sms;
+    pl.ctas = (D == 64 && pl.row_tiles == 1 ? Cfg<64, true, 1>::kCtasPerSm : Cfg<128, true, 1>::kCtasPerSm) * sms;
     pl.ws_bytes = RowsSpace(batch, pl.units, pl.ctas, R, D).bytes;
     return pl;
 }
