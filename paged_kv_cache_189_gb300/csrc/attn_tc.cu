@@ -236,7 +236,7 @@ struct TileGeom {
     int b, kvh, split, r0, nrows, qreal, kv_len, t0, kb, key_hi, nt;
     // windowed calls: the pair's rows see keys inside [0, sinks) and [lo, key_hi),
     // in the key tiles [0, nst) and from wt0 on; the split's first is the j0-th
-    int lo, sinks, nst, wt0, j0;
+    int lo, lo_last, sinks, nst, wt0, j0;  // lo_last: where the last row's window starts
     // expanded pools: page p of the sequence is page_base + p, less page_gap from page near on
     int page_base, page_near, page_gap;
 };
@@ -1288,7 +1288,7 @@ __device__ __forceinline__ TileGeom ext_geometry(const AttnParams& p, int TQ, in
     g.qreal = max(min(p.q_real ? p.q_real[b] : g.nrows, g.nrows), 0);
     g.kv_len = min(max(p.kv_lens[b], 0), p.max_kv_len);
     g.kb = 0;
-    g.key_hi = g.lo = g.nst = g.wt0 = g.j0 = g.nt = 0;
+    g.key_hi = g.lo = g.lo_last = g.nst = g.wt0 = g.j0 = g.nt = 0;
     g.sinks = p.num_sinks;
     const int first_new = g.kv_len - g.qreal;
     const int seq_lo = p.window > 0 ? max(0, first_new - p.window + 1) : 0;
@@ -1299,7 +1299,10 @@ __device__ __forceinline__ TileGeom ext_geometry(const AttnParams& p, int TQ, in
         const int last = min(g.t0 + 2 * TQ, g.qreal) - 1;
         g.key_hi = min(visible_keys(last, g.qreal, g.kv_len, p.mask, max(p.causal_block, 1)), g.kv_len);
         if (g.key_hi > 0) {
-            if (p.window > 0) g.lo = max(0, first_new + g.t0 - p.window + 1);
+            if (p.window > 0) {
+                g.lo = max(0, first_new + g.t0 - p.window + 1);
+                g.lo_last = max(0, first_new + last - p.window + 1);
+            }
             g.wt0 = g.lo / kTileN;
             g.nst = min((min(p.num_sinks, g.key_hi) + kTileN - 1) / kTileN, g.wt0);
             const int all = g.nst + (g.key_hi + kTileN - 1) / kTileN - g.wt0;
@@ -1363,8 +1366,7 @@ struct SegIter {
             if (done) return false;
             done = true;
             if constexpr (EXT)
-                s.g = ext_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
-                                   blockIdx.z % p.num_splits);
+                s.g = ext_geometry(p, TQ, u, blockIdx.y, a, blockIdx.z % p.num_splits);
             else
                 s.g = pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
                                     blockIdx.z % p.num_splits);
@@ -1422,7 +1424,7 @@ __device__ __forceinline__ void zero_pair_rows(const AttnParams& p, const TileGe
     store_row_lse(p, g, i, g.kvh * G + r % G, -INFINITY);
 }
 
-template <int D, int GC, bool SK, bool EXT = false>
+template <int D, int GC, bool SK, bool EXT = false, bool WIN = false>
 __global__ void __maxnreg__(kRegs2)
     attn_tc2_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const AttnParams p) {
@@ -1448,8 +1450,14 @@ __global__ void __maxnreg__(kRegs2)
         }
         it0.init(p);
     } else {
-        const TileGeom g = EXT ? ext_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
-                                              blockIdx.z % p.num_splits)
+        if constexpr (EXT) {
+            // the heaviest pairs first: sequences by key count, the last rows
+            // (which see most keys) before the first
+            it0.u = blockIdx.z / p.num_splits;
+            if (p.order_by_keys) it0.u = longest_first(p, it0.u, reinterpret_cast<int*>(smem));
+            it0.a = gridDim.x - 1 - blockIdx.x;
+        }
+        const TileGeom g = EXT ? ext_geometry(p, TQ, it0.u, blockIdx.y, it0.a, blockIdx.z % p.num_splits)
                                : pair_geometry(p, TQ, blockIdx.z / p.num_splits, blockIdx.y, blockIdx.x,
                                                blockIdx.z % p.num_splits);
         if constexpr (EXT) {
@@ -1745,7 +1753,7 @@ __global__ void __maxnreg__(kRegs2)
             const int limit = row_exists ? visible_keys(i, g.qreal, g.kv_len, p.mask, max(p.causal_block, 1))
                                          : 0;
             // windowed: the row's first key (those below num_sinks stay visible)
-            const int row_lo = EXT && p.window > 0 ? g.kv_len - g.qreal + i - p.window + 1 : 0;
+            const int row_lo = WIN ? g.kv_len - g.qreal + i - p.window + 1 : 0;
             {
                 // the row's query into the swizzled Q tile.  The previous segment's
                 // S MMAs have finished reading this Q tile (their S was consumed),
@@ -1794,10 +1802,11 @@ __global__ void __maxnreg__(kRegs2)
 #pragma unroll
                         for (int e = 0; e < kTileN; ++e) sv[e] = e < nvis ? sv[e] : __float_as_uint(-INFINITY);
                     }
-                    if constexpr (EXT) {
-                        // keys between the sinks and the row's window (tiles at its lower edge)
-                        const int from = g.sinks - key0, to = row_lo - key0;
-                        if (__any_sync(0xffffffffu, to > max(from, 0))) {
+                    if constexpr (WIN) {
+                        // keys between the sinks and the row's window: tiles that start
+                        // before the window of the pair's last row (uniform)
+                        if (key0 < g.lo_last) {
+                            const int from = g.sinks - key0, to = row_lo - key0;
 #pragma unroll
                             for (int e = 0; e < kTileN; ++e)
                                 sv[e] = e >= from && e < to ? __float_as_uint(-INFINITY) : sv[e];
@@ -2153,23 +2162,26 @@ cudaError_t launch_g2(const AttnParams& p, const void* tk, const void* tv, cudaS
 }
 
 // Windowed calls and calls over pools expanded from 8 bits: the two-tile kernel
-// for any number of rows (a pair whose rows fit one tile leaves the other idle).
+// for any number of rows (a pair whose rows fit one tile leaves the other idle),
+// the heaviest tile pairs dispatched first.
 template <int D, int GC>
 cudaError_t launch_ext(const AttnParams& p, const void* tk, const void* tv, cudaStream_t s) {
-    auto kern = attn_tc2_kernel<D, GC, false, true>;
+    auto kern = p.window > 0 ? attn_tc2_kernel<D, GC, false, true, true> : attn_tc2_kernel<D, GC, false, true, false>;
     constexpr int kSmem = TwoTileSmem<D>::kBytes;
-    static DeviceOnce opted;
+    static DeviceOnce opted[2];
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = opted.get(dev, &done, [&](int, int* v) {
+    e = opted[p.window > 0 ? 1 : 0].get(dev, &done, [&](int, int* v) {
         *v = 1;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e != cudaSuccess) return e;
     const int TQ = kTileM / (p.num_q_heads / p.num_kv_heads);
     dim3 grid((p.max_q_rows + 2 * TQ - 1) / (2 * TQ), p.num_kv_heads, p.batch * p.num_splits);
-    kern<<<grid, kThreads2, kSmem, s>>>(*static_cast<const CUtensorMap*>(tk), *static_cast<const CUtensorMap*>(tv), p);
+    AttnParams q = p;
+    q.order_by_keys = p.window == 0 && p.batch >= 2 && p.batch <= kOrderMaxBatch;
+    kern<<<grid, kThreads2, kSmem, s>>>(*static_cast<const CUtensorMap*>(tk), *static_cast<const CUtensorMap*>(tv), q);
     return cudaGetLastError();
 }
 
