@@ -410,25 +410,20 @@ def _scales(k_scale, v_scale, n, H):
     return max(st[0], H)
 
 
-def _index(t, count, what):
-    """A dense int32 vector of at least ``count`` entries."""
-    if t.dtype is not _I32 or t.numel() < count or (t.dim() > 0 and t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{what} must be a dense int32 vector of at least {count} entries")
-
-
 def _tables(block_table, kv_lens, q_indptr, q_real, batch, keys):
     """The batch size and the table's row stride, for up to ``keys`` keys a row."""
+    count = kv_lens.numel()
     if batch is None:
-        batch = kv_lens.numel()
-    _index(kv_lens, batch, "kv_lens")
-    _index(q_indptr, batch + 1, "q_indptr")
-    if q_real is not None:
-        _index(q_real, batch, "q_real")
-    if block_table.dtype is not _I32 or block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [batch, pages]")
+        batch = count
+    if (kv_lens.dtype is not _I32 or q_indptr.dtype is not _I32 or count < batch or q_indptr.numel() <= batch or
+            not kv_lens.is_contiguous() or not q_indptr.is_contiguous()):
+        raise ValueError("kv_lens [batch] and q_indptr [batch + 1] must be dense int32")
+    if q_real is not None and (q_real.dtype is not _I32 or q_real.numel() < batch or not q_real.is_contiguous()):
+        raise ValueError("q_real must be dense int32 [batch]")
     st, shape = block_table.stride(), block_table.shape
-    if shape[0] < batch or (st[1] != 1 and shape[1] > 1) or shape[1] * 32 < keys:
-        raise ValueError("block_table must have a row of max_kv_len / 32 pages per sequence and unit last stride")
+    if (block_table.dtype is not _I32 or len(shape) != 2 or shape[0] < batch or (st[1] != 1 and shape[1] > 1) or
+            shape[1] * 32 < keys):
+        raise ValueError("block_table must be int32 [batch, pages] with unit last stride and room for max_kv_len keys")
     return batch, shape[1] if shape[0] == 1 else st[0]
 
 
@@ -446,10 +441,10 @@ def _states(q, out, lse, D):
 
 def _on_device(tensors):
     """All on the current CUDA device: the launch goes there."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError("tensors must be on one CUDA device")
+    devs = {t.get_device() for t in tensors if t is not None}
+    dev = devs.pop()
+    if devs or dev < 0:
+        raise ValueError("tensors must be on one CUDA device")
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
@@ -466,7 +461,7 @@ def _address(t):
 
 
 def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return 0 if workspace is None else workspace.nbytes
 
 
 def kv_append_fp8(k_src, v_src, block_table, kv_lens, q_indptr, k_pool, v_pool, k_scale, v_scale, *,
