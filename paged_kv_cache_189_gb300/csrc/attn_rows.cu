@@ -48,7 +48,6 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
-#include <type_traits>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
@@ -69,7 +68,6 @@ struct Cfg {
     // 64-wide heads leave registers and ring space for a third CTA
     static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 3 : 2;
     static constexpr int kRingBytes = (kCtasPerSm == 3 ? 48 : 64) * 1024;
-    static constexpr int kChunks = 1;                    // chunks a consumer takes at once
     static constexpr int kRedRows = 4;                   // rows joined at a time
     static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kKeys = FP8 ? 32 : 16;          // keys of a chunk
@@ -316,29 +314,23 @@ __device__ __forceinline__ void row_range(const AttnParams& p, const Desc& s, in
     lo = p.window > 0 ? s.kv_len - s.qreal + tok - p.window + 1 : 0;
 }
 
-// The chunks of one step: shared-memory addresses of K (V follows), scales and
-// first keys.
-template <int NC>
-struct Chunks {
-    uint32_t kb[NC];
-    float ks[NC], vs[NC];
-    int key0[NC];
+// A chunk: shared-memory address of its K (V follows), scales, first key.
+struct Chunk {
+    uint32_t kb;
+    float ks, vs;
+    int key0;
 };
 
-// NC chunks: scores, weights and the output update.  Two at once where there
-// are two: their chains of matrix steps, maxima and exponentials run beside
-// each other, and the row statistics move once.  MASKED: some key of them is
+// One chunk: scores, weights and the output update.  MASKED: some key of it is
 // hidden from some row.
-template <int D, bool FP8, int NT, int NC, bool MASKED>
+template <int D, bool FP8, int NT, bool MASKED>
 __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const float (&fq)[NT][2],
-                                           const AttnParams& p, const Desc& ds, int G, const Chunks<NC>& ch,
-                                           int lane) {
+                                           const AttnParams& p, const Desc& ds, int G, const Chunk& ch, int lane) {
     using C = Cfg<D, FP8, NT>;
     constexpr int MI = C::kKeys / 16;  // 16-key tiles of a chunk
-    constexpr int MT = NC * MI;
     const int g = lane >> 2, t = lane & 3;
     // ---- S^T = K Q^T, the steps of independent accumulators in turn
-    constexpr int SA = FP8 || MT > 1 ? MT : 2;  // one tile: every other step to a second accumulator
+    constexpr int SA = 2;  // the two tiles of 32 keys; one tile: every other step to the second
     float s[SA][NT][4];
 #pragma unroll
     for (int x = 0; x < SA; ++x)
@@ -353,11 +345,11 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-            for (int m0 = 0; m0 < MT; m0 += MG) {
+            for (int m0 = 0; m0 < MI; m0 += MG) {
                 uint4 w[2 * MG];
 #pragma unroll
                 for (int r = 0; r < 2 * MG; ++r)
-                    w[r] = lds128(ch.kb[m0 / MI] + (a0 ^ (i << 4)) + ((m0 % MI) * 2 + r) * 8 * D);
+                    w[r] = lds128(ch.kb + (a0 ^ (i << 4)) + (2 * m0 + r) * 8 * D);
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
                     uint4 q[NT];  // steps 2 k2 and 2 k2 + 1
@@ -383,31 +375,24 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
             uint4 q[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) q[j] = lds128(qb + (j * (D / 32) + i) * 512);
+            const uint32_t ad = ch.kb + (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
+            const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
+            const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const uint32_t ad = ch.kb[m] + (a0 ^ ((i & 1) << 4)) + (i >> 1) * (C::kKeys * 128);
-                const uint4 u = lds128(ad), v = lds128(ad + 8 * 128);
-                const uint32_t x0[4] = {u.x, v.x, u.y, v.y}, x1[4] = {u.z, v.z, u.w, v.w};
+            for (int j = 0; j < NT; ++j) mma<FP8>(s[0][j], x0, q[j].x, q[j].y);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma<FP8>(s[m][j], x0, q[j].x, q[j].y);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) mma<FP8>(s[MT > 1 ? m : 1][j], x1, q[j].z, q[j].w);
-            }
+            for (int j = 0; j < NT; ++j) mma<FP8>(s[1][j], x1, q[j].z, q[j].w);
         }
-        if constexpr (MT == 1)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
+            for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
     }
     // ---- weights
-    float lv[NC];  // log2 of the V scales, rounded down
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-        lv[c] = FP8 ? fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(ch.vs[c]) >> 23) & 255u) - 127),
-                            kLowScale)
-                    : 0.f;
-    uint32_t pb[NT][MT][2];
+    float lv = 0.f;  // log2 of the V scale, rounded down
+    if constexpr (FP8)
+        lv = fmaxf(static_cast<float>(static_cast<int>((__float_as_uint(ch.vs) >> 23) & 255u) - 127), kLowScale);
+    uint32_t pb[NT][MI][2];
     bool moved = false;
     float alpha[NT][2];
 #pragma unroll
@@ -417,28 +402,24 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
         for (int e = 0; e < 2; ++e) {
             int lim = 0, lo = 0;
             if constexpr (MASKED) row_range(p, ds, (ds.row0 + 8 * j + 2 * t + e) / G, lo, lim);
+            const float f = FP8 ? fq[j][e] * ch.ks : fq[j][e];
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const float f = FP8 ? fq[j][e] * ch.ks[c] : fq[j][e];
-                float mc = -INFINITY;
+            for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-                for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        float x = s[c * MI + mi][j][2 * hh + e] * f;
-                        if constexpr (MASKED) {
-                            const int key = ch.key0[c] + 16 * mi + 8 * hh + g;
-                            if (!(key < lim && (key >= lo || key < p.num_sinks))) x = -INFINITY;
-                        }
-                        s[c * MI + mi][j][2 * hh + e] = x;
-                        mc = fmaxf(mc, x);
+                for (int hh = 0; hh < 2; ++hh) {
+                    float x = s[mi][j][2 * hh + e] * f;
+                    if constexpr (MASKED) {
+                        const int key = ch.key0 + 16 * mi + 8 * hh + g;
+                        if (!(key < lim && (key >= lo || key < p.num_sinks))) x = -INFINITY;
                     }
-                mx = fmaxf(mx, FP8 ? mc + lv[c] : mc);
-            }
+                    s[mi][j][2 * hh + e] = x;
+                    mx = fmaxf(mx, x);
+                }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if constexpr (FP8) mx += lv;
             alpha[j][e] = 1.f;
             if (mx > st.m[j][e] + kLazy) {  // also the first visible key
                 alpha[j][e] = fast_exp2(st.m[j][e] - mx);
@@ -449,7 +430,7 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
         }
         float sum[2] = {0.f, 0.f}, sumb[2] = {0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MI; ++m)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const float p0 = fast_exp2(s[m][j][2 * hh] - ref[0]), p1 = fast_exp2(s[m][j][2 * hh + 1] - ref[1]);
@@ -457,7 +438,7 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
                 sum[1] += p1;
                 uint32_t w;
                 if constexpr (FP8) {
-                    w = pack_f16x2(p0 * ch.vs[m / MI], p1 * ch.vs[m / MI]);
+                    w = pack_f16x2(p0 * ch.vs, p1 * ch.vs);
                 } else {
                     w = pack_bf16x2(p0, p1);
                     sumb[0] += bf16lo(w);
@@ -480,62 +461,59 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
                 for (int e = 0; e < 4; ++e) st.o[j][c][e] *= alpha[j][e & 1];
     }
     // ---- O^T += V^T P^T; the V of keys that no row sees may hold anything
+    const uint32_t vb = ch.kb + C::kTile;
+    uint32_t vm[2 * MI];
+    if constexpr (MASKED) {
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const uint32_t vb = ch.kb[n] + C::kTile;
-        uint32_t vm[2 * MI];
-        if constexpr (MASKED) {
+        for (int k = 0; k < 2 * MI; ++k) {
+            uint32_t keep = 0;
 #pragma unroll
-            for (int k = 0; k < 2 * MI; ++k) {
-                uint32_t keep = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = ch.key0[n] + 8 * k + 2 * t + e;
-                    if (key < ds.hi && (key >= ds.lo || key < p.num_sinks)) keep |= 0xffffu << (16 * e);
-                }
-                vm[k] = keep;
+            for (int e = 0; e < 2; ++e) {
+                const int key = ch.key0 + 8 * k + 2 * t + e;
+                if (key < ds.hi && (key >= ds.lo || key < p.num_sinks)) keep |= 0xffffu << (16 * e);
             }
+            vm[k] = keep;
         }
-        if constexpr (FP8) {
-            const uint32_t a0 = vb + lane * D + (D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4);
+    }
+    if constexpr (FP8) {
+        const uint32_t a0 = vb + lane * D + (D == 128 ? (lane & 7) << 4 : ((lane >> 1) & 3) << 4);
 #pragma unroll
-            for (int c0 = 0; c0 < D / 16; c0 += 2) {
-                uint32_t r[2][4];
+        for (int c0 = 0; c0 < D / 16; c0 += 2) {
+            uint32_t r[2][4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) ldmatrix_x4_trans(r[c], a0 ^ ((c0 + c) << 4));
+            for (int c = 0; c < 2; ++c) ldmatrix_x4_trans(r[c], a0 ^ ((c0 + c) << 4));
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t a[4];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t a[4];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t w = r[c][2 * k + q];
-                            if constexpr (MASKED) w &= vm[2 * k + q];
-                            // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
-                            widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            mma<FP8>(st.o[j][c0 + c], a, pb[j][n * MI + k][0], pb[j][n * MI + k][1]);
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w = r[c][2 * k + q];
+                        if constexpr (MASKED) w &= vm[2 * k + q];
+                        // (key 2t: dims d, d + 1; key 2t + 1: dims d, d + 1) -> d of both keys, d + 1 of both
+                        widen4(__byte_perm(w, w, 0x3120), a[2 * q], a[2 * q + 1]);
                     }
-            }
-        } else {
-            const int row = (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t a0 = vb + row * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t r[4];
-                ldmatrix_x4_trans(r, (a0 ^ ((2 * c & 7) << 4)) + (c >> 2) * (C::kKeys * 128));
-                if constexpr (MASKED) {
-                    r[0] &= vm[0];
-                    r[1] &= vm[0];
-                    r[2] &= vm[1];
-                    r[3] &= vm[1];
+                    for (int j = 0; j < NT; ++j)
+                        mma<FP8>(st.o[j][c0 + c], a, pb[j][k][0], pb[j][k][1]);
                 }
+        }
+    } else {
+        const int row = (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t a0 = vb + row * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c], r, pb[j][n][0], pb[j][n][1]);
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[4];
+            ldmatrix_x4_trans(r, (a0 ^ ((2 * c & 7) << 4)) + (c >> 2) * (C::kKeys * 128));
+            if constexpr (MASKED) {
+                r[0] &= vm[0];
+                r[1] &= vm[0];
+                r[2] &= vm[1];
+                r[3] &= vm[1];
             }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma<FP8>(st.o[j][c], r, pb[j][0][0], pb[j][0][1]);
         }
     }
 }
@@ -941,48 +919,25 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st.o[j][c][e] = 0.f;
             }
-            int i = warp >= turn ? warp - turn : warp - turn + NW;
-            // NC of this warp's chunks; false: a wait gave up
-            auto step = [&](auto nc) -> bool {
-                constexpr int NC = decltype(nc)::value;
-                Chunks<NC> ch;
-                int stage[NC];
-                bool all = true;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int sg = own * NW + warp;
-                    if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) return false;
-                    const float4 me = meta[sg];
-                    stage[c] = sg;
-                    ch.kb[c] = ring_u + sg * C::kStage;
-                    ch.ks[c] = me.x;
-                    ch.vs[c] = me.y;
-                    ch.key0[c] = __float_as_int(me.z);
-                    all = all && ch.key0[c] + C::kKeys <= s.all_end &&
-                          (ch.key0[c] >= s.all_lo || ch.key0[c] + C::kKeys <= p.num_sinks);
-                    if (++own == C::kOwn) {
-                        own = 0;
-                        phase ^= 1;
-                    }
+            for (int i = warp >= turn ? warp - turn : warp - turn + NW; i < s.n; i += NW) {
+                const int sg = own * NW + warp;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) {
+                    dead = true;
+                    break;
                 }
-                if (all) chunk_step<D, FP8, NT, NC, false>(st, qb, fq, p, s, G, ch, lane);
-                else if constexpr (NC == 1) chunk_step<D, FP8, NT, NC, true>(st, qb, fq, p, s, G, ch, lane);
-                else {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        chunk_step<D, FP8, NT, 1, true>(
-                            st, qb, fq, p, s, G, Chunks<1>{{ch.kb[c]}, {ch.ks[c]}, {ch.vs[c]}, {ch.key0[c]}}, lane);
-                }
+                const float4 me = meta[sg];
+                const Chunk ch{ring_u + sg * C::kStage, me.x, me.y, __float_as_int(me.z)};
+                const bool whole = ch.key0 + C::kKeys <= s.all_end &&
+                                   (ch.key0 >= s.all_lo || ch.key0 + C::kKeys <= p.num_sinks);
+                if (whole) chunk_step<D, FP8, NT, false>(st, qb, fq, p, s, G, ch, lane);
+                else chunk_step<D, FP8, NT, true>(st, qb, fq, p, s, G, ch, lane);
                 __syncwarp();
-                if (lane == 0) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) mbar_arrive(&empty[stage[c]]);
+                if (lane == 0) mbar_arrive(&empty[sg]);
+                if (++own == C::kOwn) {
+                    own = 0;
+                    phase ^= 1;
                 }
-                return true;
-            };
-            for (; i + NW * (C::kChunks - 1) < s.n && !dead; i += NW * C::kChunks)
-                dead = !step(std::integral_constant<int, C::kChunks>{});
-            for (; i < s.n && !dead; i += NW) dead = !step(std::integral_constant<int, 1>{});
+            }
             turn = (turn + s.n) % NW;
             // ---- join the warps' states, kRedRows rows at a time
 #pragma unroll
