@@ -283,7 +283,8 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  * paged_attention_fp8 -- paged_attention over the 8-bit cache of kv_append_fp8,
  * optionally with a sliding window and sinks.
  *
- * Same rows, masks, outputs and conventions as paged_attention, with
+ * Same rows, masks, outputs and conventions as paged_attention (q and out must
+ * not overlap), with
  *   k_j = k_scale[page(j), head] * code,  v_j = v_scale[page(j), head] * code
  * (any finite f32 scales >= 0).  window = 0 attends as `mask` says.  window > 0
  * (mask PKV_MASK_CAUSAL only): the row at position p = kv_len - q_real + i sees
@@ -306,7 +307,8 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  *
  *  workspace      paged_attention_fp8_workspace_size(...) bytes, 256-byte
  *                 aligned; one workspace must not serve two calls in flight
- *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY
+ *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY (a generic kernel without
+ *                 a workspace), PKV_FLAG_TEST_WAIT_TIMEOUT (few-row calls)
  */
 size_t paged_attention_fp8_workspace_size(int batch, int max_q_rows, int num_q_heads,
                                           int num_kv_heads, int head_dim, int max_kv_len,

@@ -58,6 +58,9 @@ namespace {
 constexpr int kPage = 32;
 constexpr float kLazy = 8.0f;         // move the reference only past 2^8 growth
 constexpr float kLowScale = -90.0f;   // log2 of the smallest V scale M follows
+// PKV_FLAG_TEST_WAIT_TIMEOUT: the limit of the waits that are meant to run out
+// (consumers on a barrier nothing completes, the other warps' as they follow)
+constexpr uint64_t kTestWaitNs = 20000, kWaitNs = 2000000000ull;
 constexpr int kDescs = 8;             // segments the look-up may be ahead
 constexpr int kSelfBatch = 256;       // sequences up to which a CTA finds its first piece itself
 constexpr int kBatches = 1;           // batches of 32 chunks it may be ahead
@@ -86,9 +89,9 @@ struct Cfg {
     static constexpr int kQueueOff = kDescOff + kDescs * 64;          // [batches][32] look-ups
     static constexpr int kHeadOff = kQueueOff + kBatches * 32 * 16;   // [batches] (chunks, K/V head)
     static constexpr int kFlagOff = kHeadOff + kBatches * 8;  // a consumer's wait gave up; segments staged
-    // full, empty [stages], dfull, dempty [descs], bfull, bempty [batches]
+    // full, empty [stages], dfull, dempty [descs], bfull, bempty [batches], never
     static constexpr int kBarOff = kFlagOff + 8;
-    static constexpr int kBytes = kBarOff + (2 * kStages + 2 * kDescs + 2 * kBatches) * 8;
+    static constexpr int kBytes = kBarOff + (2 * kStages + 2 * kDescs + 2 * kBatches + 1) * 8;
     static_assert(kStages % kWarps == 0, "each consumer owns whole stages");
     static_assert((kBytes + 1024) * kCtasPerSm <= 228 * 1024, "CTAs per SM must fit in shared memory");
     static_assert(kMetaOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
@@ -581,6 +584,8 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
     uint64_t* dempty = dfull + kDescs;
     uint64_t* bfull = dempty + kDescs;
     uint64_t* bempty = bfull + kBatches;
+    uint64_t* never = bempty + kBatches;  // nothing completes it
+    const uint64_t limit = p.test_wait_timeout ? kTestWaitNs : kWaitNs;
     float4* meta = reinterpret_cast<float4*>(smem + C::kMetaOff);
     Desc* desc = reinterpret_cast<Desc*>(smem + C::kDescOff);
     Look* queue = reinterpret_cast<Look*>(smem + C::kQueueOff);
@@ -599,6 +604,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
             mbar_init(&bfull[s], 32);
             mbar_init(&bempty[s], 32);
         }
+        mbar_init(never, 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -676,7 +682,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
         const int pieces = line.pieces();
         int nseg = 0, nbatch = 0;
         bool alive = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)); };
         for (bool fixed = true; alive; fixed = false) {
             // ---- the next piece, by ticket
             if (a.ctas == 0 && !fixed) break;
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                     if ((it & 63u) == 63u) {
                         const uint64_t now = global_timer_ns();
                         if (t0 == 0) t0 = now;
-                        if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {
+                        if (__any_sync(0xffffffffu, now - t0 > limit)) {
                             alive = false;
                             break;
                         }
@@ -919,7 +925,9 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st.o[j][c][e] = 0.f;
             }
-            for (int i = warp >= turn ? warp - turn : warp - turn + NW; i < s.n; i += NW) {
+            // the test hook: a wait that runs out before the first chunk
+            if (p.test_wait_timeout && !__all_sync(0xffffffffu, mbar_wait(never, 0, kTestWaitNs))) dead = true;
+            for (int i = warp >= turn ? warp - turn : warp - turn + NW; i < s.n && !dead; i += NW) {
                 const int sg = own * NW + warp;
                 if (!__all_sync(0xffffffffu, mbar_wait(&full[sg], phase))) {
                     dead = true;
@@ -938,7 +946,6 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                     phase ^= 1;
                 }
             }
-            turn = (turn + s.n) % NW;
             // ---- join the warps' states, kRedRows rows at a time
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -1009,10 +1016,15 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                 for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * C::kRows + r]);
                 float L = 0.f, Lb = 0.f;
                 float2 O = make_float2(0.f, 0.f);
-                if (M != -INFINITY && tok < s.qreal) {
+                if (tok < s.qreal) {
+                    // (no visible key: every l and o is 0, or NaN where a score was)
+                    const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        const float f = fast_exp2(red_m[w * C::kRows + r] - M);
+                    for (int k = 0; k < NW; ++k) {
+                        // by the place of the warps' chunks in the segment, not by the warp's
+                        // number: which warp had the first depends on what came before
+                        const int w = (turn + k) % NW;
+                        const float f = fast_exp2(red_m[w * C::kRows + r] - ref);
                         const float2 o = *reinterpret_cast<const float2*>(red + (w * RR + rr) * RS + d);
                         L = fmaf(f, red_l[w * C::kRows + r], L);
                         if constexpr (!FP8) Lb = fmaf(f, red_lb[w * C::kRows + r], Lb);
@@ -1051,6 +1063,8 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                 sync();
             }
         }
+        turn = (turn + s.n) % NW;
+        __syncwarp();
         if (lane == 0) mbar_arrive(&dempty[ds]);
     }
 }

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(128) attn_simt_ext_kernel(AttnParams p) {
         for (int j = 0; j < DPL; ++j) dot = fmaf(q[j], kx[j], dot);
         const float s = warp_sum(dot);
         const float m_new = fmaxf(m, s);
-        if (m_new == -INFINITY) continue;  // a score of -inf before any other: weight 0
+        if (s == -INFINITY && m_new == -INFINITY) continue;  // -inf before any other score: weight 0
         const float alpha = fast_exp2(m - m_new);
         const float pk = fast_exp2(s - m_new);
         l = l * alpha + pk;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(128) attn_simt_ext_kernel(AttnParams p) {
         for (int j = 0; j < DPL; ++j) o[j] = fmaf(pk, vx[j], o[j] * alpha);
         m = m_new;
     }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int64_t st = static_cast<int64_t>(row) * p.num_q_heads + h;
 #pragma unroll
     for (int j = 0; j < DPL; ++j) {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(128) attn_simt_ext_kernel(AttnParams p) {
         if (p.out_f32) static_cast<float*>(p.out)[st * D + lane * DPL + j] = v;
         else static_cast<__nv_bfloat16*>(p.out)[st * D + lane * DPL + j] = __float2bfloat16_rn(v);
     }
-    if (p.lse && lane == 0) p.lse[st] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[st] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 }  // namespace

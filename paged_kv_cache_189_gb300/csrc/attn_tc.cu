@@ -1915,7 +1915,8 @@ __global__ void __maxnreg__(kRegs2)
             // state in this CTA's fragment slot (the first or the last segment)
             const bool whole = sg.j0 == 0 && sg.j1 == g.nt;
             const int fslot = blockIdx.x * 2 + (slot == 0 ? 0 : 1);
-            const bool any = l > 0.f && l_b > 0.f;
+            // (windowed and expanded calls: a row whose scores are NaN keeps NaN)
+            const bool any = EXT ? l != 0.f : l > 0.f && l_b > 0.f;
             const float inv_l = any ? 1.0f / l_b : 0.f;
             if (ok_o && row_exists) {
                 const float lse = any ? (m_used + __log2f(l)) * kLn2 : -INFINITY;

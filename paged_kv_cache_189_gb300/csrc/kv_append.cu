@@ -142,18 +142,18 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 5 : 8)
     const int which = rest >= Hkv ? 1 : 0, h = rest - which * Hkv;
 
     const int r0 = a.q_indptr[b];
-    const int rows = a.q_indptr[b + 1] - r0, nrows = min(rows, a.max_q_rows);
-    const int qreal = min(a.q_real ? a.q_real[b] : nrows, nrows);
-    int kv_len = a.kv_lens[b];
+    const int rows = a.q_indptr[b + 1] - r0;
+    const int real = a.q_real ? a.q_real[b] : rows, kv_len = a.kv_lens[b];
     if (a.checked && item == 0 && lane == 0 &&
-        (kv_len > a.max_kv_len || kv_len < 0 || rows > a.max_q_rows || (a.q_real && a.q_real[b] > rows)))
+        (kv_len > a.max_kv_len || kv_len < 0 || rows > a.max_q_rows || real > rows))
         set_err(a.err, PKV_ERRBIT_LEN);
-    kv_len = min(max(kv_len, 0), a.max_kv_len);
-    if (qreal <= 0) return;
-    const int first = kv_len - qreal;                 // position of the first new row (may be below 0)
+    const int first = max(kv_len, 0) - max(real, 0);  // position of the first new row (may be below 0)
+    // new rows end here: as many as there are, below the host bounds
+    const int last = min(first + min(min(real, rows), a.max_q_rows), a.max_kv_len);
+    if (real <= 0 || first >= last) return;
     const int pos0 = (max(first, 0) / kPage + t) * kPage;  // this page's first position
-    if (pos0 >= kv_len) return;
-    const int begin = max(first - pos0, 0), end = min(kv_len - pos0, kPage);  // slots that receive rows
+    if (pos0 >= last) return;
+    const int begin = max(first - pos0, 0), end = min(last - pos0, kPage);  // slots that receive rows
 
     const int sub = lane / kLanes, col = (lane % kLanes) * kVec;
     const T* src = static_cast<const T*>(a.src[which]) +

@@ -717,14 +717,19 @@ struct ExtPlan {
     size_t expand_bytes = 0, states_o = 0, states_lse = 0, ws_bytes = 0;
 };
 // (query row, grouped head) pairs of a K/V head up to which the few-row kernel
-// reads the cache once per 16 of them
-constexpr int kFewRows = 64;
+// runs.  It reads the cache once per 16 of them (through L2), the tile kernel
+// once, but an 8-bit one only after its expansion to bf16.  Measured (us,
+// few-row / tile): 64 sequences of 2000-4000 keys, 32 / 8 heads of 128: 8 bits
+// 331 / 382 at 64 pairs, 379 / 382 at 80, 467 / 380 at 96; bf16 through a
+// 1024-key window 91 / 109 at 16, 141 / 98 at 32.  One sequence of 30000 keys,
+// 8 bits: 58 / 124 at 80.
+constexpr int kFewRowsFp8 = 80, kFewRowsBf16 = 16;
 
 ExtPlan plan_ext(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
                  bool fp8, int sms) {
     ExtPlan pl;
     const int G = Hq / Hkv;
-    pl.tile = static_cast<int64_t>(max_q_rows) * G > kFewRows && pkv::attn_tc_supported(D, G);
+    pl.tile = max_kv_len > 0 && static_cast<int64_t>(max_q_rows) * G > (fp8 ? kFewRowsFp8 : kFewRowsBf16) && pkv::attn_tc_supported(D, G);
     if (!pl.tile) {
         pl.rows = pkv::plan_attn_rows(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, sms);
         pl.ws_bytes = pl.rows.ws_bytes;
@@ -851,14 +856,16 @@ pkv_status ext_attention(const ExtArgs& a) {
     if (a.block_table_stride < pages_needed)
         return fail(PKV_ERR_INVALID_ARG, "%s: block_table_stride %lld < %lld pages for max_kv_len", n,
                     (long long)a.block_table_stride, (long long)pages_needed);
-    if (a.flags & ~(PKV_FLAG_CHECKED | PKV_FLAG_SIMT_ONLY))
-        return fail(PKV_ERR_UNSUPPORTED, "%s: flags 0x%x (only CHECKED and SIMT_ONLY)", n, a.flags);
-    if ((a.flags & PKV_FLAG_CHECKED) && !a.err)
-        return fail(PKV_ERR_INVALID_ARG, "%s: checked mode needs an error flag", n);
+    if (a.flags & ~(PKV_FLAG_CHECKED | PKV_FLAG_SIMT_ONLY | PKV_FLAG_TEST_WAIT_TIMEOUT))
+        return fail(PKV_ERR_UNSUPPORTED, "%s: flags 0x%x (CHECKED, SIMT_ONLY and TEST_WAIT_TIMEOUT only)", n, a.flags);
+    if ((a.flags & (PKV_FLAG_CHECKED | PKV_FLAG_TEST_WAIT_TIMEOUT)) && !a.err)
+        return fail(PKV_ERR_INVALID_ARG, "%s: checked mode and the wait test need an error flag", n);
     ExtPlan pl;
     if (!(a.flags & PKV_FLAG_SIMT_ONLY))
         pl = plan_ext(a.batch, a.max_q_rows, a.num_q_heads, a.num_kv_heads, a.head_dim, a.max_kv_len, a.window,
                       a.num_sinks, a.fp8, current_device_sms());
+    if ((a.flags & PKV_FLAG_TEST_WAIT_TIMEOUT) && (pl.tile || (a.flags & PKV_FLAG_SIMT_ONLY)))
+        return fail(PKV_ERR_UNSUPPORTED, "%s: the wait test runs on the few-row kernel only", n);
     if (pl.ws_bytes > 0 && (!a.workspace || a.workspace_bytes < pl.ws_bytes || !aligned(a.workspace, 256)))
         return fail(PKV_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned", n, pl.ws_bytes);
     if (pl.tile && static_cast<int64_t>(a.batch) * pl.splits > 65535)
@@ -901,8 +908,9 @@ pkv_status ext_attention(const ExtArgs& a) {
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
     p.scale_stride = a.scale_stride;
-    p.window = a.window;
+    p.window = std::min(a.window, std::max(a.max_kv_len, 1));  // a longer one hides nothing either
     p.num_sinks = a.num_sinks;
+    p.test_wait_timeout = (a.flags & PKV_FLAG_TEST_WAIT_TIMEOUT) != 0;
     if (a.flags & PKV_FLAG_SIMT_ONLY) return from_cuda(pkv::launch_attn_simt_ext(p, a.stream), n);
 
     CUtensorMap tk, tv;

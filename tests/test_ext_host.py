@@ -61,6 +61,7 @@ COMMON = [
     (dict(odt=pkv.PKV_F16), UNSUPPORTED), (dict(batch=70000), UNSUPPORTED), (dict(pstride=1000), INVALID),
     (dict(pstride=32 * 8 * 128 + 4), INVALID), (dict(q=ODD), INVALID), (dict(k=ODD), INVALID), (dict(qts=4), INVALID),
     (dict(out=ODD), INVALID), (dict(bts=3), INVALID), (dict(flags=pkv.PKV_FLAG_CHECKED), INVALID),
+    (dict(flags=pkv.PKV_FLAG_TEST_WAIT_TIMEOUT), INVALID),
     (dict(flags=pkv.PKV_FLAG_STREAM_K), UNSUPPORTED), (dict(batch=0), pkv.PKV_OK), (dict(mq=0), pkv.PKV_OK)]
 
 
@@ -77,6 +78,27 @@ def test_fp8_refusals(L, kw, want):
 def test_window_refusals(L, kw, want):
     assert attend(L, False, **kw) == want
     assert (pkv.last_error() == "") == (want == pkv.PKV_OK)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_workspaces(L, fp8):
+    """A workspace where the call needs one: none for a short cache, partial
+    states for a long one, the expanded pages of an 8-bit prompt chunk."""
+    def size(batch, rows, kv, window=0 if fp8 else 10 ** 6, heads=(32, 8), D=128, flags=0):
+        f = pkv.paged_attention_fp8_workspace_size if fp8 else pkv.paged_attention_window_workspace_size
+        return f(batch, rows, *heads, D, kv, window, 0, flags)
+    assert size(2, 1, 100) == 0 and size(0, 1, 100) == 0 and size(2, 1, 0) == 0
+    assert size(2, 1, 10 ** 5, flags=pkv.PKV_FLAG_SIMT_ONLY) == 0
+    long = size(2, 1, 10 ** 5)
+    assert long > 0 and size(200, 1, 10 ** 5) > long
+    chunk = size(4, 2048, 8192)
+    if fp8:
+        assert chunk >= 2 * 4 * 8192 * 8 * 128 * 2
+        assert size(4, 2048, 8192, window=1000) < chunk  # only the window's pages are expanded
+    kw = dict(flags=0, mk=8192, bts=256, ws=FAKE, wsb=1 << 40)
+    assert attend(L, fp8, mq=200, mk=8192, bts=256, flags=0, ws=None) == (WORKSPACE if fp8 or size(2, 200, 8192, window=50) else 4)
+    assert attend(L, fp8, **{**kw, "ws": ctypes.c_void_p(0x1010)}, mq=1, window=0 if fp8 else 8192) == WORKSPACE  # misaligned
+    assert attend(L, fp8, **{**kw, "wsb": 100}, mq=1, window=0 if fp8 else 8192) == WORKSPACE                    # too small
 
 
 def test_binding_refusals(L):

@@ -271,3 +271,131 @@ def test_window_without_reach_is_causal():
                         q_real=t["q_real"], lse=rl, max_q_rows=1, max_kv_len=300, workspace=ws)
     check(c, out, lse)
     check(c, ref, rl)
+
+
+# ------------------------------------------------------------------ the cut line of keys
+@pytest.mark.parametrize("fp8,window,new,D,Hkv", [
+    (True, 0, (1, 1), 128, 2), (False, 1800, (1, 1), 128, 2), (True, 0, (2, 6), 128, 2), (True, 2500, (1, 1), 64, 3)])
+def test_more_units_than_ctas(fp8, window, new, D, Hkv):
+    """Enough (sequence, head) units that part of the keys is taken by ticket;
+    the same bits whoever takes which."""
+    kv, real, rows = ragged(30, 170, new, (1, 3600), pad=1 if new[1] > 1 else 0)
+    kv[5], real[5], rows[5] = 0, 0, 1
+    real[6] = rows[6] = 0
+    kv[7] = 3600
+    c = Case(kv, real, rows, 4 * Hkv, Hkv, D, fp8, window=window, sinks=5 if window else 0, seed=31)
+    ref = c.reference()
+    t = c.on("cuda")
+    out = torch.empty(sum(rows), c.Hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(sum(rows), c.Hq, device="cuda")
+    wide = torch.full((len(kv), 200), -1, dtype=torch.int32, device="cuda")
+    wide[:, :t["table"].shape[1]] = t["table"]
+    t["table"] = wide
+    call(c, t, out, lse, max_kv_len=6400)
+    torch.cuda.synchronize()
+    check(c, out, lse, ref)
+    for _ in range(3):
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        call(c, t, o2, l2, max_kv_len=6400)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def call_bounds(c, max_kv_len):
+    """A call whose table is as wide as a larger host bound asks for."""
+    t = c.on("cuda")
+    wide = torch.full((len(c.kv), (max_kv_len + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    wide[:, :t["table"].shape[1]] = t["table"]
+    t["table"] = wide
+    out = torch.empty(sum(c.rows), c.Hq, c.D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(sum(c.rows), c.Hq, device="cuda")
+    call(c, t, out, lse, max_kv_len=max_kv_len)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("batch,kv", [(300, (1, 900)), (2100, (1, 120))])
+def test_large_batches(batch, kv):
+    """More sequences than a CTA, and than the planner's shared memory, looks through."""
+    lens, real, rows = ragged(32, batch, (1, 1), kv)
+    c = Case(lens, real, rows, 4, 1, 128, True, seed=33)
+    check(c, *call_bounds(c, 4000))
+
+
+@pytest.mark.parametrize("fp8,new", [(True, (5, 12)), (False, (1, 3)), (True, (17, 20))])
+def test_several_row_tiles(fp8, new):
+    """Row tiles of 8 and 16 on long rows, few and many of them."""
+    kv, real, rows = ragged(34, 6, new, (2000, 5000), pad=2)
+    c = Case(kv, real, rows, 8, 2, 128, fp8, window=0 if fp8 else 3000, sinks=0 if fp8 else 9, seed=35)
+    check(c, *run(c))
+
+
+def test_large_group():
+    """More query heads a K/V head than the tile kernel takes."""
+    c = Case([300, 40], [3, 2], [3, 4], 160, 2, 128, True, seed=36)
+    check(c, *run(c))
+    c = Case([300, 140], [40, 30], [40, 30], 80, 1, 64, False, window=50, sinks=2, seed=37)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_extreme_bounds(new, fp8):
+    """The largest window and sink counts, rows below key 0, an empty cache."""
+    c = Case([max(1, new - 2), 50], [new, new], [new, new], 8, 2, 128, fp8, window=2 ** 31 - 1, sinks=2 ** 31 - 1,
+             seed=38)
+    check(c, *run(c))
+    c = Case([70, 50], [new, new], [new, new], 8, 2, 128, fp8, window=1, sinks=2 ** 31 - 1, seed=39)
+    check(c, *run(c))
+    c = Case([0, 0], [new, 0], [new, 2], 8, 2, 128, fp8, window=0 if fp8 else 4, seed=40)
+    t = c.on("cuda")
+    out, lse = (torch.full(s, 5.0, dtype=d, device="cuda") for s, d in
+                (((new + 2, 8, 128), torch.bfloat16), ((new + 2, 8), torch.float32)))
+    kw = dict(q_real=t["q_real"], lse=lse, max_q_rows=max(c.rows), max_kv_len=0, window=c.window)
+    if fp8:
+        pkv.paged_attention_fp8(t["q"], t["k_pool"], t["v_pool"], t["k_scale"], t["v_scale"], t["table"], t["kv_lens"],
+                                t["q_indptr"], out, **kw)
+    else:
+        pkv.paged_attention_window(t["q"], t["k_pool"], t["v_pool"], t["table"], t["kv_lens"], t["q_indptr"], out, **kw)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("kv", [100, 6000])
+def test_wait_that_runs_out(kv):
+    """The failure path: consumers give up on a barrier nothing completes, the
+    error bit is set, every warp winds down, and the next call is unharmed."""
+    c = Case([kv, 20], [1, 1], [1, 1], 8, 2, 128, True, seed=41)
+    t = c.on("cuda")
+    out = torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(2, 8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = call(c, t, out, lse, flags=pkv.PKV_FLAG_TEST_WAIT_TIMEOUT, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == pkv.PKV_ERRBIT_TIMEOUT
+    err.zero_()
+    call(c, t, out, lse, err=err, workspace=ws)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    check(c, out, lse)
+    with pytest.raises(pkv.PkvError):  # the tile kernel has no such hook
+        big = Case([kv], [50], [50], 8, 2, 128, True, seed=42)
+        call(big, big.on("cuda"), torch.zeros(50, 8, 128, dtype=torch.bfloat16, device="cuda"),
+             torch.zeros(50, 8, device="cuda"), flags=pkv.PKV_FLAG_TEST_WAIT_TIMEOUT, err=err)
+
+
+def test_nan_scores_stay_in_their_rows():
+    """NaN in one sequence's query shows in its rows only."""
+    for new in (1, 3, 60):
+        c = Case([200, 300], [new, new], [new, new], 8, 2, 128, True, seed=43)
+        ref = c.reference()
+        t = c.on("cuda")
+        t["q"][0, 3, 5] = float("nan")
+        out = torch.empty(2 * new, 8, 128, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(2 * new, 8, device="cuda")
+        call(c, t, out, lse)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[0, 3]).all() and torch.isnan(lse[0, 3])
+        out[0, 3] = torch.from_numpy(ref[0][0, 3]).to(out)
+        lse[0, 3] = float(ref[1][0, 3])
+        check(c, out, lse, ref)

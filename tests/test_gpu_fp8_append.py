@@ -33,7 +33,7 @@ class Cache:
             x64 = np.clip(src[w].double().numpy(), -top, top)
             for b in range(len(kv)):
                 n = min(kv[b], max_kv)
-                first = n - real[b]
+                first = kv[b] - real[b]
                 for p in range(max(first, 0) // P, (max(n, 0) + P - 1) // P):
                     lo, hi = max(first, p * P, 0), min(n, (p + 1) * P)
                     if hi <= lo or real[b] <= 0:
