@@ -1159,13 +1159,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_rows_plan_kernel(const __gr
 }
 
 // Joins the partial states of the units that pieces cut: block (unit, four of
-// its rows), kJoinParts warps a row that take every kJoinParts-th state, a lane
-// D / 32 dimensions.
-constexpr int kJoinParts = 4;
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinParts * 128) attn_rows_join_kernel(const __grid_constant__ RowsArgs a) {
-    constexpr int DPL = D / 32, kAhead = 32 / kJoinParts;
-    __shared__ float part_o[kJoinParts - 1][4][D];
+// its rows), PARTS warps a row that take every PARTS-th state, a lane D / 32
+// dimensions.  One part where the units are many (a handful of states each,
+// and a wave of blocks), four for few long units (up to a hundred each).
+template <int D, int ROWS, int PARTS>
+__global__ void __launch_bounds__(PARTS * 128) attn_rows_join_kernel(const __grid_constant__ RowsArgs a) {
+    constexpr int DPL = D / 32, kAhead = 8;
+    __shared__ float part_o[PARTS > 1 ? PARTS - 1 : 1][4][D];
     const AttnParams& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x;
@@ -1191,35 +1191,43 @@ __global__ void __launch_bounds__(kJoinParts * 128) attn_rows_join_kernel(const 
         for (int k0 = 0; k0 < cut.y; k0 += 32) {
             const int n = min(32, cut.y - k0);
             const float e = lane < n ? __ldcg(lse + static_cast<int64_t>(k0 + lane) * ROWS) : -INFINITY;
-            float v[kAhead][DPL];
+            float w = 0.f;
+#pragma unroll 1
+            for (int x0 = 0; x0 < n; x0 += PARTS * kAhead) {
+                float v[kAhead][DPL];
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const int k = kJoinParts * x + part;
-                const float* src = o + static_cast<int64_t>(k0 + k) * (ROWS * D);
-                if constexpr (DPL == 4) {
-                    const float4 u = k < n ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[x][0] = u.x;
-                    v[x][1] = u.y;
-                    v[x][2] = u.z;
-                    v[x][3] = u.w;
-                } else {
-                    const float2 u = k < n ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-                    v[x][0] = u.x;
-                    v[x][1] = u.y;
+                for (int x = 0; x < kAhead; ++x) {
+                    const int k = x0 + PARTS * x + part;
+                    const float* src = o + static_cast<int64_t>(k0 + k) * (ROWS * D);
+                    if constexpr (DPL == 4) {
+                        const float4 u = k < n ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v[x][0] = u.x;
+                        v[x][1] = u.y;
+                        v[x][2] = u.z;
+                        v[x][3] = u.w;
+                    } else {
+                        const float2 u = k < n ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                        v[x][0] = u.x;
+                        v[x][1] = u.y;
+                    }
                 }
-            }
-            const float Mn = fmaxf(M, warp_max(e));
-            const float ref = Mn == -INFINITY ? 0.f : Mn;
-            const float w = fast_exp2(e - ref), f = fast_exp2(M - ref);
-            M = Mn;
-            L = fmaf(L, f, warp_sum(w));
+                if (x0 == 0) {
+                    const float Mn = fmaxf(M, warp_max(e));
+                    const float ref = Mn == -INFINITY ? 0.f : Mn;
+                    const float f = fast_exp2(M - ref);
+                    w = fast_exp2(e - ref);
+                    M = Mn;
+                    L = fmaf(L, f, warp_sum(w));
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) O[i] *= f;
+                    for (int i = 0; i < DPL; ++i) O[i] *= f;
+                }
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const float wx = __shfl_sync(0xffffffffu, w, kJoinParts * x + part);
+                for (int x = 0; x < kAhead; ++x) {
+                    const float wx = __shfl_sync(0xffffffffu, w, (x0 + PARTS * x + part) & 31);
+                    if (x0 + PARTS * x + part < n)
 #pragma unroll
-                for (int i = 0; i < DPL; ++i) O[i] = fmaf(wx, v[x][i], O[i]);
+                        for (int i = 0; i < DPL; ++i) O[i] = fmaf(wx, v[x][i], O[i]);
+                }
             }
         }
         if (part > 0)
@@ -1232,7 +1240,7 @@ __global__ void __launch_bounds__(kJoinParts * 128) attn_rows_join_kernel(const 
 #pragma unroll
     for (int i = 0; i < DPL; ++i) {
 #pragma unroll
-        for (int x = 0; x < kJoinParts - 1; ++x) O[i] += part_o[x][row][lane * DPL + i];
+        for (int x = 0; x < PARTS - 1; ++x) O[i] += part_o[x][row][lane * DPL + i];
         O[i] *= inv;
     }
     const int64_t ot = static_cast<int64_t>(q0 + R / G) * p.num_q_heads + kvh * G + R % G;
@@ -1281,9 +1289,10 @@ cudaError_t launch_rows(const RowsArgs& a, const void* tk, const void* tv, cudaS
     e = cudaLaunchKernelEx(&cfg, kern, mk, mv, a);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(units, C::kRows / 4);
-    cfg.blockDim = dim3(kJoinParts * 128);
+    cfg.blockDim = dim3(a.even ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<D, C::kRows>, a);
+    return cudaLaunchKernelEx(&cfg, a.even ? attn_rows_join_kernel<D, C::kRows, 4> : attn_rows_join_kernel<D, C::kRows, 1>,
+                              a);
 }
 
 // The workspace of the cut line.
