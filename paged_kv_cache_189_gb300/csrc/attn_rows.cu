@@ -22,16 +22,19 @@
 //    16-bit ldmatrix; a byte permute separates the two dimensions it pairs.
 //  * q is bf16; for 8-bit pools each row is brought to 2^8 by a power of two
 //    (undone in the score's factor) and held in f16: exact but for elements
-//    2^-22 below the row's largest.
+//    2^-22 below the row's largest.  A segment's rows sit in shared memory in
+//    fragment order, staged once for all consumers.
 //  * Weights are rounded once: to bf16 for bf16 pools, and w = 2^(a - M) vs to
 //    f16 for 8-bit ones, M following a + log2(vs), so w stays at or below 2^9
 //    whatever the scales.  Sums, maxima and outputs are f32.
 //  * Per CTA one warp looks up pages and scales ahead, 32 chunks at a time, and
 //    one fills a ring of chunks (32 keys in 8 bits, 16 in bf16) by TMA, so the
-//    chain length -> table -> scale stays off the copies' path; each consumer
-//    warp owns every kWarps-th stage and keeps its own softmax state: no
-//    barrier joins the consumers until a unit's end.  2 CTAs an SM keep 192 KB
-//    in flight.
+//    chain length -> table -> scale stays off the copies' path; each of four
+//    consumer warps owns every fourth stage and keeps its own softmax state: no
+//    barrier joins the consumers until a unit's end.  2 CTAs an SM (3 at 64-wide
+//    heads) keep 128 KB in flight; 192 KB, six consumers at 128 registers, or
+//    two chunks a step were no faster (107, 114 and 121 us on the first case
+//    below).
 //  * Work: a unit is (sequence, K/V head, tile of 8 or 16 rows); its chunks are
 //    the pages its rows see.  All units' chunks form one line, laid out on the
 //    device (a captured call replays with other lengths), and the line is cut
@@ -44,7 +47,14 @@
 //    joins them in the line's order, so results do not depend on who took which
 //    ticket.  (Joined by the CTA that completes a unit instead, the last CTAs
 //    ended up to 75 us after the others on three sequences of 10^5 keys.)
-//    Small calls skip all this: one CTA a unit.
+//    Small calls skip all this: the resident CTAs take whole units in turn, the
+//    next one's chunks on their way while one is joined.
+// Measured (copy peak 6694 GB/s): 64 sequences of 513-8193 keys, 32 / 8 heads of
+// 128, 8 bits, 524 MB: 107 us, 0.73 of the peak (the first chunk arrives after
+// 6 us, the CTAs stream at 0.93 of it and end within 13 us of each other, the
+// join takes 6); the same with 4 tokens a sequence 131 us, bound by the chunk's
+// chain of dependent steps at 8 warps an SM; 3 sequences of 60000-131072 keys
+// 85 us (0.75); bf16 through a 4096-key window, 1020 MB: 168 us (0.91).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -99,7 +109,7 @@ struct Cfg {
 
 struct RowsArgs {
     AttnParams p;
-    int ctas;       // CTAs that share the line (0: one CTA a unit)
+    int ctas;       // CTAs that share the line (0: whole units)
     int tiles_max;  // row tiles of a sequence at the host bound
     bool even;      // all pieces fixed
     // written by the planner
@@ -671,12 +681,6 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                     if (w.left == 0) break;
                 }
             }
-        } else {
-            const int x = blockIdx.x;
-            w.mt = x % a.tiles_max;
-            w.kvh = (x / a.tiles_max) % Hkv;
-            w.b = x / a.tiles_max / Hkv;
-            w.left = w.mt < sequence<C::kRows>(p, w.b, G).tiles ? 0x7fffffff : 0;
         }
         const Line line(T, max(a.ctas, 1), a.even);
         const int pieces = line.pieces();
@@ -684,9 +688,16 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
         bool alive = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)); };
         for (bool fixed = true; alive; fixed = false) {
-            // ---- the next piece, by ticket
-            if (a.ctas == 0 && !fixed) break;
-            if (a.ctas > 0 && !(fixed && self && piece < line.first)) {
+            // ---- the next piece, by ticket; in a small call every gridDim-th unit, whole
+            if (a.ctas == 0) {
+                if (!fixed) piece += gridDim.x;
+                if (piece >= a.tiles_max * Hkv * p.batch) break;
+                w.mt = piece % a.tiles_max;
+                w.kvh = (piece / a.tiles_max) % Hkv;
+                w.b = piece / a.tiles_max / Hkv;
+                w.at = 0;
+                w.left = w.mt < sequence<C::kRows>(p, w.b, G).tiles ? 0x7fffffff : 0;
+            } else if (!(fixed && self && piece < line.first)) {
                 if (!planned) await_planner();
                 if (!fixed || piece >= line.first) {
                     int tk = 0;
@@ -1254,7 +1265,7 @@ __global__ void __launch_bounds__(PARTS * 128) attn_rows_join_kernel(const __gri
 }
 
 template <int D, bool FP8, int NT>
-cudaError_t launch_rows(const RowsArgs& a, const void* tk, const void* tv, cudaStream_t s) {
+cudaError_t launch_rows(const RowsArgs& a, int resident, const void* tk, const void* tv, cudaStream_t s) {
     using C = Cfg<D, FP8, NT>;
     auto kern = attn_rows_kernel<D, FP8, NT>;
     static DeviceOnce opted;
@@ -1269,7 +1280,7 @@ cudaError_t launch_rows(const RowsArgs& a, const void* tk, const void* tv, cudaS
     const CUtensorMap &mk = *static_cast<const CUtensorMap*>(tk), &mv = *static_cast<const CUtensorMap*>(tv);
     const unsigned units = static_cast<unsigned>(a.tiles_max * a.p.num_kv_heads * a.p.batch);
     if (a.ctas == 0) {
-        kern<<<units, C::kThreads, C::kBytes, s>>>(mk, mv, a);
+        kern<<<std::min(units, static_cast<unsigned>(resident)), C::kThreads, C::kBytes, s>>>(mk, mv, a);
         return cudaGetLastError();
     }
     attn_rows_plan_kernel<C::kRows, C::kKeys><<<1, kPlanThreads, 0, s>>>(a);
@@ -1317,7 +1328,7 @@ struct RowsSpace {
 
 }  // namespace
 
-// One CTA a unit while a unit is short (kDirectBytes of K and V at the host
+// Whole units while a unit is short (kDirectBytes of K and V at the host
 // bound, what a CTA streams in about 6 us) or the rows alone make units enough (more than kCutTiles
 // tiles a sequence, whose places the planner would add up one by one); else
 // the cut line.
@@ -1334,8 +1345,9 @@ RowsPlan plan_attn_rows(int batch, int max_q_rows, int Hq, int Hkv, int D, int m
     int64_t keys = max_kv_len;
     if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + R + std::min(num_sinks, max_kv_len) + 62);
     const double places = static_cast<double>(pl.units) * (std::min<double>(keys, max_kv_len) / 16 + 3);
+    pl.resident = (D == 64 && pl.row_tiles == 1 ? Cfg<64, true, 1>::kCtasPerSm : Cfg<128, true, 1>::kCtasPerSm) * sms;
     if (keys * 2 * D * (fp8 ? 1 : 2) <= kDirectBytes || pl.tiles > kCutTiles || places > 2e9) return pl;  // the line is counted in 32 bits
-    pl.ctas = (D == 64 && pl.row_tiles == 1 ? Cfg<64, true, 1>::kCtasPerSm : Cfg<128, true, 1>::kCtasPerSm) * sms;
+    pl.ctas = pl.resident;
     pl.ws_bytes = RowsSpace(batch, pl.units, pl.ctas, R, D).bytes;
     return pl;
 }
@@ -1359,7 +1371,7 @@ cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* work
         a.frag_o = reinterpret_cast<float*>(w + x.frag_o);
     }
 #define PKV_ROWS(D_, F_, N_) \
-    if (p.head_dim == D_ && p.kv_fp8 == F_ && pl.row_tiles == N_) return launch_rows<D_, F_, N_>(a, tk, tv, s);
+    if (p.head_dim == D_ && p.kv_fp8 == F_ && pl.row_tiles == N_) return launch_rows<D_, F_, N_>(a, pl.resident, tk, tv, s);
     PKV_ROWS(128, true, 1) PKV_ROWS(128, true, 2) PKV_ROWS(128, false, 1) PKV_ROWS(128, false, 2)
     PKV_ROWS(64, true, 1) PKV_ROWS(64, true, 2) PKV_ROWS(64, false, 1) PKV_ROWS(64, false, 2)
 #undef PKV_ROWS

@@ -234,11 +234,13 @@ cudaError_t launch_attn_simt_ext(const AttnParams& p, cudaStream_t s);
 
 // Few query rows per sequence over bf16 or fp8 pools with a window and sinks
 // (mma.sync, TMA-fed rings per warp).  The plan's row tile is 8 * row_tiles
-// (query row, grouped head) pairs; ctas = 0 runs one CTA per unit, else that
-// many CTAs share the units' keys (a planner before and a join behind them).
+// (query row, grouped head) pairs; ctas = 0: the resident CTAs take whole
+// units in turn, else that many share the units' keys (a planner before and a
+// join behind them).
 struct RowsPlan {
     int row_tiles;
     int64_t tiles, units;  // row tiles of a sequence, units of the call, at the host bounds
+    int resident;          // CTAs that run at once
     int ctas;
     size_t ws_bytes;
 };
