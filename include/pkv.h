@@ -255,7 +255,8 @@ pkv_status paged_attention(const void* q, int64_t q_token_stride, int64_t q_head
  * grew later by more than its own magnitude allows.
  *
  * A page that receives rows must belong to one sequence (copy a shared last
- * page first); slots past the last key, and pages that receive no row, keep
+ * page first: its slots with copy_kv_slots, the pools' bytes taken as 2-byte
+ * elements of half the head_dim, and its scale rows); slots past the last key, and pages that receive no row, keep
  * their bytes and scale.  Padding rows, positions below 0 or at or past
  * max_kv_len and block-table entries outside [0, num_pages) are skipped (the
  * last two also set PKV_ERRBIT_LEN / PKV_ERRBIT_PAGE with PKV_FLAG_CHECKED).
@@ -301,8 +302,8 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  *
  * The softmax weights are rounded once before the P.V product: to f16 (2^-11
  * relative) by the few-row kernel, to bf16 (2^-8 at most) by the tile kernel;
- * sums, maxima and the LSE are f32.  Calls whose rows x grouped heads are many
- * first expand the visible pages to bf16 in the workspace (code * scale, exact
+ * sums, maxima and the LSE are f32.  The same call gives the same bits every
+ * time.  Calls whose rows x grouped heads are many first expand the visible pages to bf16 in the workspace (code * scale, exact
  * for the power-of-two scales kv_append_fp8 writes).
  *
  *  workspace      paged_attention_fp8_workspace_size(...) bytes, 256-byte

@@ -693,8 +693,8 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
     if (block_table_stride < pages_needed)
         return fail(PKV_ERR_INVALID_ARG, "append: block_table_stride %lld < %lld pages for max_kv_len",
                     (long long)block_table_stride, (long long)pages_needed);
-    if ((static_cast<int64_t>(max_q_rows) / 32 + 2) * 2 * num_kv_heads > 0x7fffffffLL)
-        return fail(PKV_ERR_UNSUPPORTED, "append: too many pages times K/V heads");
+    if ((static_cast<int64_t>(max_q_rows) / 32 + 2) * 2 * num_kv_heads > 0x7fffffffLL || max_kv_len > 0x7fffff00)
+        return fail(PKV_ERR_UNSUPPORTED, "append: too many pages times K/V heads, or too many keys");
     if ((flags & PKV_FLAG_CHECKED) && !err)
         return fail(PKV_ERR_INVALID_ARG, "append: checked mode needs an error flag");
     pkv::AppendArgs a{{k_src, v_src}, src_token_stride, src_head_stride, src_dtype, block_table,
@@ -837,8 +837,8 @@ pkv_status ext_attention(const ExtArgs& a) {
         return fail(PKV_ERR_INVALID_ARG, "%s: sinks need a window", n);
     if (a.out_dtype != PKV_BF16 && a.out_dtype != PKV_F32)
         return fail(PKV_ERR_UNSUPPORTED, "%s: output dtype must be bf16 or f32", n);
-    if (a.batch > 65535 || a.num_kv_heads > 65535)
-        return fail(PKV_ERR_UNSUPPORTED, "%s: batch or K/V heads above 65535", n);
+    if (a.batch > 65535 || a.num_kv_heads > 65535 || a.max_kv_len > 0x7fffff00)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: batch or K/V heads above 65535, or keys above 2^31 - 256", n);
     const int esz = a.fp8 ? 1 : 2;
     if (a.page_stride < static_cast<int64_t>(a.page_size) * a.num_kv_heads * a.head_dim ||
         (a.page_stride * esz) % 16)

@@ -231,3 +231,29 @@ def test_append_in_a_graph():
         c.append([x.cpu() for x in src], table.cpu().numpy(), kv.tolist(), [1, 1], [0, 1, 2], 96, TOP[torch.bfloat16])
         kv += 1
     c.same()
+
+
+def test_fork_of_a_partly_filled_page():
+    """Two samples of one prompt: the whole page shared, the partly filled one
+    copied (slots and scales), then each appends its own tokens."""
+    H, D = 2, 64
+    c = Cache(8, H, D, seed=9)
+    g = np.random.default_rng(10)
+    top = TOP[torch.bfloat16]
+    prompt = [torch.from_numpy(g.standard_normal((45, H, D))).to(torch.bfloat16) for _ in "kv"]
+    table = np.array([[3, 5]], dtype=np.int32)
+    indptr = append(c, prompt, table, [45], [45], [45])
+    c.append(prompt, table, [45], [45], indptr, 64, top)
+    # page 5 -> 6: the pools' bytes as 2-byte elements
+    pools = [p.view(torch.uint8).view(torch.bfloat16) for p in c.pools]
+    slots = torch.arange(32, dtype=torch.int64, device="cuda")
+    pkv.copy_kv_slots(pools[0], pools[1], 5 * 32 + slots, 6 * 32 + slots)
+    for w in range(2):
+        c.dev_scales[w][6] = c.dev_scales[w][5]
+        c.codes[w][6], c.scales[w][6] = c.codes[w][5], c.scales[w][5]
+    fork = np.array([[3, 5], [3, 6]], dtype=np.int32)
+    for n in range(4):
+        src = [torch.from_numpy(g.standard_normal((2, H, D)) * 10 ** n).to(torch.bfloat16) for _ in "kv"]
+        indptr = append(c, src, fork, [46 + n] * 2, [1, 1], [1, 1], max_kv=64)
+        c.append(src, fork, [46 + n] * 2, [1, 1], indptr, 64, top)
+    c.same()
