@@ -26,6 +26,7 @@
 // to 8 with spills (16.4) and a second read instead of registers (16.9).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <algorithm>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
@@ -252,8 +253,10 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 8)
 
 template <typename T>
 cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
-    // n rows touch at most (n + 30) / 32 + 1 pages, whatever slot they start at
-    const int pages = (a.max_q_rows + kPage - 2) / kPage + 1;
+    // n rows touch at most (n + 30) / 32 + 1 pages, whatever slot they start at,
+    // and none past the cache's bound (either limit may be close to 2^31)
+    const int64_t touched = (static_cast<int64_t>(a.max_q_rows) + kPage - 2) / kPage + 1;
+    const int pages = static_cast<int>(std::min<int64_t>(touched, (static_cast<int64_t>(a.max_kv_len) + kPage - 1) / kPage));
     const int64_t items = static_cast<int64_t>(pages) * 2 * a.num_kv_heads;
     const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps), a.batch);
     if (a.head_dim == 128) append_fp8_kernel<T, 128><<<grid, kWarps * 32, 0, s>>>(a, pages);

@@ -153,6 +153,19 @@ def test_empty_and_bounds():
     c.same()
 
 
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 31 - 31, 1000])
+def test_row_bound_far_above_the_rows(bound):
+    c = Cache(6, 2, 64, seed=9)
+    g = torch.Generator().manual_seed(10)
+    src = [torch.randn(41, 2, 64, generator=g).bfloat16() for _ in "kv"]
+    table, kv, real = np.array([[4, 1, 2], [0, 5, 3]]), [70, 7], [36, 5]
+    pkv.kv_append_fp8(src[0].cuda(), src[1].cuda(), i32(table), i32(kv), i32([0, 36, 41]), c.pools[0], c.pools[1],
+                      c.dev_scales[0], c.dev_scales[1], max_q_rows=bound, max_kv_len=96)
+    torch.cuda.synchronize()
+    c.append(src, table, kv, real, [0, 36, 41], 96, torch.finfo(torch.bfloat16).max)
+    c.same()
+
+
 @pytest.mark.parametrize("bad", [10 ** 6, -3])
 def test_bad_page_is_skipped(bad):
     c = Cache(8, 2, 64, seed=4)
