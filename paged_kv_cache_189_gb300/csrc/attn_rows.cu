@@ -781,6 +781,9 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
             }
         }
         if (!alive && lane == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        // the join waits for this grid alone and reads what the planner wrote, so
+        // a look-up that gave up before it needed the planner waits for it here
+        if (a.ctas > 0 && !planned) await_planner();
         // the end marks (where a wait gave up, the readers' own waits run out too)
         const int bs = nbatch % kBatches, ds = nseg % kDescs;
         if (nbatch < kBatches || wait(&bempty[bs], (nbatch / kBatches - 1) & 1)) {
@@ -1365,7 +1368,7 @@ cudaError_t launch_attn_rows(const AttnParams& p, const RowsPlan& pl, void* work
         char* w = static_cast<char*>(workspace);
         a.ticket = reinterpret_cast<int*>(w + x.ticket);
         a.cuts = reinterpret_cast<int2*>(w + x.cuts);
-            a.seq_at = reinterpret_cast<int*>(w + x.seq_at);
+        a.seq_at = reinterpret_cast<int*>(w + x.seq_at);
         a.starts = reinterpret_cast<int4*>(w + x.starts);
         a.frag_lse = reinterpret_cast<float*>(w + x.frag_lse);
         a.frag_o = reinterpret_cast<float*>(w + x.frag_o);
