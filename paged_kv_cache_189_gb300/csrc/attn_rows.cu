@@ -33,8 +33,8 @@
 //    consumer warps owns every fourth stage and keeps its own softmax state: no
 //    barrier joins the consumers until a unit's end.  2 CTAs an SM (3 at 64-wide
 //    heads) keep 128 KB in flight; 192 KB, six consumers at 128 registers, or
-//    two chunks a step were no faster (107, 114 and 121 us on the first case
-//    below).
+//    two chunks a step were no faster (107, 114 and 121 us where the first case
+//    below took 107).
 //  * Work: a unit is (sequence, K/V head, tile of 8 or 16 rows); its chunks are
 //    the pages its rows see.  All units' chunks form one line, laid out on the
 //    device (a captured call replays with other lengths), and the line is cut
@@ -50,11 +50,12 @@
 //    Small calls skip all this: the resident CTAs take whole units in turn, the
 //    next one's chunks on their way while one is joined.
 // Measured (copy peak 6694 GB/s): 64 sequences of 513-8193 keys, 32 / 8 heads of
-// 128, 8 bits, 524 MB: 107 us, 0.73 of the peak (the first chunk arrives after
+// 128, 8 bits, 524 MB: 105 us, 0.75 of the peak (the first chunk arrives after
 // 6 us, the CTAs stream at 0.93 of it and end within 13 us of each other, the
-// join takes 6); the same with 4 tokens a sequence 131 us, bound by the chunk's
-// chain of dependent steps at 8 warps an SM; 3 sequences of 60000-131072 keys
-// 85 us (0.75); bf16 through a 4096-key window, 1020 MB: 168 us (0.91).
+// join takes 6); the same with 4 tokens a sequence 120 us, bound by the chunk's
+// chain of dependent steps at 8 warps an SM (one CTA of ten consumers an SM:
+// 154, nothing streams while it joins a unit); 3 sequences of 60000-131072 keys
+// 86 us (0.75); bf16 through a 4096-key window, 1020 MB: 167 us (0.91).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -81,7 +82,7 @@ struct Cfg {
     // 64-wide heads leave registers and ring space for a third CTA
     static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 3 : 2;
     static constexpr int kRingBytes = (kCtasPerSm == 3 ? 48 : 64) * 1024;
-    static constexpr int kRedRows = 4;                   // rows joined at a time
+    static constexpr int kRedRows = 8;                   // rows joined at a time: a tile
     static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kKeys = FP8 ? 32 : 16;          // keys of a chunk
     static constexpr int kTile = kKeys * D * (FP8 ? 1 : 2);
@@ -983,21 +984,19 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
             *abort_flag = 1;
         }
         constexpr int RR = C::kRedRows, RS = C::kRedStride;
-        auto put_rows = [&](int rg) {  // rows RR rg .. RR rg + RR - 1
-            if (t / (RR / 2) == rg % (8 / RR)) {
-                float* r0 = red + (warp * RR + 2 * (t % (RR / 2))) * RS;
+        auto put_rows = [&](int rg) {  // rows RR rg .. RR rg + RR - 1: tile rg
+            float* r0 = red + (warp * RR + 2 * t) * RS;
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const float(&o)[4] = st.o[rg / (8 / RR)][c];
-                    if constexpr (FP8) {
-                        *reinterpret_cast<float2*>(r0 + 16 * c + 2 * g) = make_float2(o[0], o[2]);
-                        *reinterpret_cast<float2*>(r0 + RS + 16 * c + 2 * g) = make_float2(o[1], o[3]);
-                    } else {
-                        r0[16 * c + g] = o[0];
-                        r0[16 * c + 8 + g] = o[2];
-                        r0[RS + 16 * c + g] = o[1];
-                        r0[RS + 16 * c + 8 + g] = o[3];
-                    }
+            for (int c = 0; c < D / 16; ++c) {
+                const float(&o)[4] = st.o[rg][c];
+                if constexpr (FP8) {
+                    *reinterpret_cast<float2*>(r0 + 16 * c + 2 * g) = make_float2(o[0], o[2]);
+                    *reinterpret_cast<float2*>(r0 + RS + 16 * c + 2 * g) = make_float2(o[1], o[3]);
+                } else {
+                    r0[16 * c + g] = o[0];
+                    r0[16 * c + 8 + g] = o[2];
+                    r0[RS + 16 * c + g] = o[1];
+                    r0[RS + 16 * c + 8 + g] = o[3];
                 }
             }
         };
@@ -1018,10 +1017,13 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
         }
         const int rows_here = min(C::kRows, s.nrows * G - R0);
         // rows RR rg .. RR rg + RR - 1 of the warps' states in red / red_m / red_l: joined and written,
-        // as the result or as a partial state
+        // as the result or as a partial state; four dimensions a thread (a row's
+        // factors are computed by each of its threads: with two dimensions each
+        // and four rows at a time, 16-row calls took 131 us instead of 120, with
+        // eight dimensions 120 too)
         auto join_rows = [&](int rg) {
-            for (int e = threadIdx.x; e < RR * D / 2; e += NW * 32) {
-                const int rr = e / (D / 2), d = (e - rr * (D / 2)) * 2;
+            for (int e = threadIdx.x; e < RR * D / 4; e += NW * 32) {
+                const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
                 const int r = RR * rg + rr;
                 if (r >= rows_here) continue;
                 const int tok = (R0 + r) / G, h = s.kvh * G + (R0 + r) % G;
@@ -1029,7 +1031,7 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
 #pragma unroll
                 for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * C::kRows + r]);
                 float L = 0.f, Lb = 0.f;
-                float2 O = make_float2(0.f, 0.f);
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (tok < s.qreal) {
                     // (no visible key: every l and o is 0, or NaN where a score was)
                     const float ref = M == -INFINITY ? 0.f : M;
@@ -1039,11 +1041,13 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                         // number: which warp had the first depends on what came before
                         const int w = (turn + k) % NW;
                         const float f = fast_exp2(red_m[w * C::kRows + r] - ref);
-                        const float2 o = *reinterpret_cast<const float2*>(red + (w * RR + rr) * RS + d);
+                        const float4 o = *reinterpret_cast<const float4*>(red + (w * RR + rr) * RS + d);
                         L = fmaf(f, red_l[w * C::kRows + r], L);
                         if constexpr (!FP8) Lb = fmaf(f, red_lb[w * C::kRows + r], Lb);
                         O.x = fmaf(f, o.x, O.x);
                         O.y = fmaf(f, o.y, O.y);
+                        O.z = fmaf(f, o.z, O.z);
+                        O.w = fmaf(f, o.w, O.w);
                     }
                 }
                 // bf16 weights: normalised by the sum of the rounded ones
@@ -1051,17 +1055,19 @@ __global__ void __launch_bounds__((Cfg<D, FP8, NT>::kThreads), (Cfg<D, FP8, NT>:
                 const float inv = div > 0.f ? 1.0f / div : (div == div ? 0.f : div);
                 O.x *= inv;
                 O.y *= inv;
+                O.z *= inv;
+                O.w *= inv;
                 const float lse2 = L == 0.f ? -INFINITY : M + __log2f(L);
                 if (s.frag < 0) {
                     const int64_t ot = static_cast<int64_t>(s.r0 + tok) * p.num_q_heads + h;
-                    if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + ot * D + d) = O;
+                    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ot * D + d) = O;
                     else
-                        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + ot * D + d) =
-                            pack_bf16x2(O.x, O.y);
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + ot * D + d) =
+                            make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
                     if (p.lse && d == 0) p.lse[ot] = lse2 * kLn2;
                 } else {
                     const int64_t fr = static_cast<int64_t>(s.frag) * C::kRows + r;
-                    __stcg(reinterpret_cast<float2*>(a.frag_o + fr * D + d), O);
+                    __stcg(reinterpret_cast<float4*>(a.frag_o + fr * D + d), O);
                     if (d == 0) __stcg(a.frag_lse + fr, lse2);
                 }
             }
