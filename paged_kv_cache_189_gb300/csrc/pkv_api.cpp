@@ -720,9 +720,9 @@ struct ExtPlan {
 // runs.  It reads the cache once per 16 of them (through L2), the tile kernel
 // once, but an 8-bit one only after its expansion to bf16.  Measured (us,
 // few-row / tile): 64 sequences of 2000-4000 keys, 32 / 8 heads of 128: 8 bits
-// 331 / 382 at 64 pairs, 379 / 382 at 80, 467 / 380 at 96; bf16 through a
-// 1024-key window 91 / 109 at 16, 141 / 98 at 32.  One sequence of 30000 keys,
-// 8 bits: 58 / 124 at 80.
+// 297 / 382 at 64 pairs, 338 / 383 at 80, 421 / 380 at 96; bf16 through a
+// 1024-key window 73 / 109 at 16, 117 / 99 at 32.  One sequence of 30000 keys,
+// 8 bits: 56 / 123 at 80.
 constexpr int kFewRowsFp8 = 80, kFewRowsBf16 = 16;
 
 ExtPlan plan_ext(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
