@@ -407,7 +407,11 @@ def _scales(k_scale, v_scale, n, H):
     if (k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or k_scale.shape != (n, H) or
             v_scale.shape != (n, H) or v_scale.stride() != st or (H > 1 and st[1] != 1)):
         raise ValueError("scales must be float32 [num_pages, num_kv_heads] with unit head stride, K's and V's alike")
-    return max(st[0], H)
+    if n <= 1:  # one page: whatever its stride says, nothing is taken by it
+        return H
+    if st[0] < H:
+        raise ValueError("scales of different pages must not overlap (an expanded tensor needs a copy)")
+    return st[0]
 
 
 def _tables(block_table, kv_lens, q_indptr, q_real, batch, keys):
