@@ -155,9 +155,10 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 8)
     const int first = max(kv_len, 0) - max(real, 0);  // position of the first new row (may be below 0)
     // new rows end here: as many as there are, below the host bounds
     const int last = min(first + min(min(real, rows), a.max_q_rows), a.max_kv_len);
-    if (real <= 0 || first >= last) return;
-    const int pos0 = (max(first, 0) / kPage + t) * kPage;  // this page's first position
-    if (pos0 >= last) return;
+    if (real <= 0 || first >= last || last <= 0) return;
+    const int logical = max(first, 0) / kPage + t;
+    if (logical > (last - 1) / kPage) return;  // in pages: at the widest bounds the position would pass 2^31
+    const int pos0 = logical * kPage;          // this page's first position
     const int begin = max(first - pos0, 0), end = min(last - pos0, kPage);  // slots that receive rows
 
     const int sub = lane / kLanes, col = (lane % kLanes) * kVec;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 8)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) v[s] = row(s);
     }
-    const int page = a.block_table[b * a.block_table_stride + pos0 / kPage];
+    const int page = a.block_table[b * a.block_table_stride + logical];
     if (page < 0 || page >= a.num_pages) {
         if (a.checked && lane == 0) set_err(a.err, PKV_ERRBIT_PAGE);
         return;
