@@ -90,12 +90,16 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
     const int64_t st = static_cast<int64_t>(row) * H + h;
     const float* lses = p.ws_lse + st * p.num_splits;
     float m = -INFINITY;
-    for (int s = 0; s < nsplit; ++s) m = fmaxf(m, lses[s]);
+    bool nan = false;  // windowed and expanded calls: a state whose scores are NaN makes its row NaN
+    for (int s = 0; s < nsplit; ++s) {
+        m = fmaxf(m, lses[s]);  // (passes NaN over)
+        nan |= p.even_splits && lses[s] != lses[s];
+    }
     float acc[DPL];
 #pragma unroll
     for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
     float wsum = 0.f;
-    if (m != -INFINITY) {
+    if (m != -INFINITY || nan) {
         for (int s = 0; s < nsplit; ++s) {
             const float w = __expf(lses[s] - m);
             wsum += w;
@@ -104,7 +108,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
             for (int j = 0; j < DPL; ++j) acc[j] += w * o[j];
         }
     }
-    const float inv = wsum > 0.f ? 1.0f / wsum : 0.f;
+    const bool any = nan || wsum > 0.f;
+    const float inv = any ? 1.0f / wsum : 0.f;
     const int64_t ob = st * D + lane * DPL;
     if (p.out_f32) {
         float* out = static_cast<float*>(p.out) + ob;
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
 #pragma unroll
         for (int j = 0; j < DPL; j += 2) out[j / 2] = pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
     }
-    if (p.lse && lane == 0) p.lse[st] = wsum > 0.f ? m + __logf(wsum) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[st] = any ? m + __logf(wsum) : -INFINITY;
 }
 
 }  // namespace
