@@ -823,6 +823,9 @@ pkv_status ext_attention(const ExtArgs& a) {
     if (!a.q || !a.k_pool || !a.v_pool || !a.block_table || !a.kv_lens || !a.q_indptr || !a.out ||
         (a.fp8 && (!a.k_scale || !a.v_scale)))
         return fail(PKV_ERR_INVALID_ARG, "%s: null pointer", n);
+    // (a tensor map has one page at least, and page num_pages stands for one that is not there)
+    if (a.num_pages == 0 && a.max_kv_len > 0)
+        return fail(PKV_ERR_INVALID_ARG, "%s: a pool without pages, for up to %d keys", n, a.max_kv_len);
     if (a.page_size != 32)
         return fail(PKV_ERR_UNSUPPORTED, "%s: page_size %d (only 32-token pages)", n, a.page_size);
     if (a.head_dim != 64 && a.head_dim != 128)

@@ -1,0 +1,18 @@
+"""Sizes at the edges of what paged_attention_fp8 and paged_attention_window
+take, on the host: nothing here reaches a GPU."""
+import pytest
+
+from paged_kv_cache_189_gb300 import pkv
+from test_ext_host import L, attend  # noqa: F401  (L is a fixture)
+
+INVALID, UNSUPPORTED = pkv.PKV_ERR_INVALID_ARG, pkv.PKV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("mq", [1, 200])
+@pytest.mark.parametrize("flags", [0, pkv.PKV_FLAG_SIMT_ONLY])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_a_pool_without_pages(L, fp8, flags, mq):  # noqa: F811
+    """A look-up that fails reads the page behind the pool's last, which the
+    copies fill with zeros: of no pages there is no such page."""
+    assert attend(L, fp8, pages=0, mq=mq, flags=flags) == INVALID
+    assert "without pages" in pkv.last_error()
