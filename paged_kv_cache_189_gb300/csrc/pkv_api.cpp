@@ -724,6 +724,8 @@ struct ExtPlan {
 // 1024-key window 73 / 109 at 16, 117 / 99 at 32.  One sequence of 30000 keys,
 // 8 bits: 56 / 123 at 80.
 constexpr int kFewRowsFp8 = 80, kFewRowsBf16 = 16;
+// keys and query rows of a sequence: rounded up to tiles they stay in 32 bits
+constexpr int kExtMost = 0x7fffff00;
 
 ExtPlan plan_ext(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
                  bool fp8, int sms) {
@@ -761,7 +763,7 @@ ExtPlan plan_ext(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_l
 size_t ext_workspace(int batch, int max_q_rows, int Hq, int Hkv, int D, int max_kv_len, int window, int num_sinks,
                      bool fp8, unsigned flags) {
     if (batch <= 0 || max_q_rows <= 0 || Hkv <= 0 || Hq < Hkv || max_kv_len < 0 || window < 0 || num_sinks < 0 ||
-        (D != 64 && D != 128))
+        (D != 64 && D != 128) || max_q_rows > kExtMost || max_kv_len > kExtMost)
         return 0;
     if (flags & PKV_FLAG_SIMT_ONLY) return 0;
     return plan_ext(batch, max_q_rows, Hq, Hkv, D, max_kv_len, window, num_sinks, fp8, current_device_sms()).ws_bytes;
@@ -840,8 +842,8 @@ pkv_status ext_attention(const ExtArgs& a) {
         return fail(PKV_ERR_INVALID_ARG, "%s: sinks need a window", n);
     if (a.out_dtype != PKV_BF16 && a.out_dtype != PKV_F32)
         return fail(PKV_ERR_UNSUPPORTED, "%s: output dtype must be bf16 or f32", n);
-    if (a.batch > 65535 || a.num_kv_heads > 65535 || a.max_kv_len > 0x7fffff00)
-        return fail(PKV_ERR_UNSUPPORTED, "%s: batch or K/V heads above 65535, or keys above 2^31 - 256", n);
+    if (a.batch > 65535 || a.num_kv_heads > 65535 || a.max_kv_len > kExtMost || a.max_q_rows > kExtMost)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: batch or K/V heads above 65535, or keys or query rows above 2^31 - 256", n);
     const int esz = a.fp8 ? 1 : 2;
     if (a.page_stride < static_cast<int64_t>(a.page_size) * a.num_kv_heads * a.head_dim ||
         (a.page_stride * esz) % 16)
