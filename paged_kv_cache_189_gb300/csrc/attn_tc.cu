@@ -287,6 +287,12 @@ __device__ __forceinline__ TileGeom tile_geometry(const AttnParams& p, int TQ, i
     return g;
 }
 
+// A row's place among the split states: by its sequence and its row there, as
+// the packed rows may start anywhere; grouped rows by their token.
+__device__ __forceinline__ int64_t state_row(const AttnParams& p, const TileGeom& g, int row_in_seq) {
+    return p.grp_perm ? g.r0 + row_in_seq : static_cast<int64_t>(g.b) * p.max_q_rows + row_in_seq;
+}
+
 // Columns [32c, 32c + 32) of one row's normalised output (or split partial).
 template <int D>
 __device__ __forceinline__ void store_row_chunk(const AttnParams& p, const TileGeom& g, int row_in_seq,
@@ -307,8 +313,9 @@ __device__ __forceinline__ void store_row_chunk(const AttnParams& p, const TileG
     if (p.num_splits == 1) {
         base = static_cast<float*>(p.out) + st * D;
     } else {
-        if (g.r0 + row_in_seq >= static_cast<int64_t>(p.batch) * p.max_q_rows) return;
-        base = p.ws_o + (st * p.num_splits + g.split) * D;
+        const int64_t row = state_row(p, g, row_in_seq);
+        if (row >= static_cast<int64_t>(p.batch) * p.max_q_rows) return;
+        base = p.ws_o + ((row * p.num_q_heads + h) * p.num_splits + g.split) * D;
     }
     float4* dst = reinterpret_cast<float4*>(base + c * 32);
 #pragma unroll
@@ -316,12 +323,13 @@ __device__ __forceinline__ void store_row_chunk(const AttnParams& p, const TileG
 }
 __device__ __forceinline__ void store_row_lse(const AttnParams& p, const TileGeom& g, int row_in_seq,
                                               int h, float lse) {
-    const int64_t st = static_cast<int64_t>(g.r0 + row_in_seq) * p.num_q_heads + h;
     if (p.num_splits == 1) {
-        if (p.lse) p.lse[st] = lse;
-    } else if (g.r0 + row_in_seq < static_cast<int64_t>(p.batch) * p.max_q_rows) {
-        p.ws_lse[st * p.num_splits + g.split] = lse;
+        if (p.lse) p.lse[static_cast<int64_t>(g.r0 + row_in_seq) * p.num_q_heads + h] = lse;
+        return;
     }
+    const int64_t row = state_row(p, g, row_in_seq);
+    if (row < static_cast<int64_t>(p.batch) * p.max_q_rows)
+        p.ws_lse[(row * p.num_q_heads + h) * p.num_splits + g.split] = lse;
 }
 
 // ---------------------------------------------------------------------------

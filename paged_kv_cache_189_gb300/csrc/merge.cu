@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
     const int nrows = p.q_indptr[b + 1] - r0;
     if (row_in_seq >= nrows) return;
     const int row = r0 + row_in_seq;
-    if (row >= static_cast<int64_t>(p.batch) * p.max_q_rows) return;  // workspace bound
+    // where the tile kernel left the row's states: by sequence and row, grouped by token
+    const int64_t ws_row = p.grp_perm ? row : static_cast<int64_t>(b) * p.max_q_rows + row_in_seq;
+    if (ws_row >= static_cast<int64_t>(p.batch) * p.max_q_rows) return;  // workspace bound
     int nsplit = p.num_splits;  // grouped mode, windowed calls: every split wrote a state for every token
     if (!p.grp_perm && !p.even_splits) {
         const int qreal = p.q_real ? p.q_real[b] : nrows;
@@ -88,7 +90,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
         nsplit = min(p.num_splits, (kv_len + p.split_keys - 1) / p.split_keys);
     }
     const int64_t st = static_cast<int64_t>(row) * H + h;
-    const float* lses = p.ws_lse + st * p.num_splits;
+    const int64_t ws_st = ws_row * H + h;
+    const float* lses = p.ws_lse + ws_st * p.num_splits;
     float m = -INFINITY;
     bool nan = false;  // windowed and expanded calls: a state whose scores are NaN makes its row NaN
     for (int s = 0; s < nsplit; ++s) {
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(AttnParams p) {
         for (int s = 0; s < nsplit; ++s) {
             const float w = __expf(lses[s] - m);
             wsum += w;
-            const float* o = p.ws_o + (st * p.num_splits + s) * D + lane * DPL;
+            const float* o = p.ws_o + (ws_st * p.num_splits + s) * D + lane * DPL;
 #pragma unroll
             for (int j = 0; j < DPL; ++j) acc[j] += w * o[j];
         }
