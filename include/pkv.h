@@ -287,10 +287,12 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  * Same rows, masks, outputs and conventions as paged_attention (q and out must
  * not overlap), with
  *   k_j = k_scale[page(j), head] * code,  v_j = v_scale[page(j), head] * code
- * (any finite f32 scales >= 0).  window = 0 attends as `mask` says.  window > 0
- * (mask PKV_MASK_CAUSAL only): the row at position p = kv_len - q_real + i sees
- * the keys j <= p with j > p - window (its own key and the window - 1 before
- * it) or j < num_sinks (the first tokens, which stay visible).
+ * (finite f32 scales >= 0).  V scales are best 0 or between 2^-90 and 2^90: smaller
+ * ones leave an output an absolute error of up to 2^-106 for each key, larger ones
+ * may make it infinite; the LSE has its accuracy with any.  window = 0 attends as
+ * `mask` says.  window > 0 (mask PKV_MASK_CAUSAL only): the row at position
+ * p = kv_len - q_real + i sees the keys j <= p with j > p - window (its own key and
+ * the window - 1 before it) or j < num_sinks (the first tokens, which stay visible).
  * num_sinks = 0 without a window.
  *
  * Pages whose keys no row of the call sees are not read: their block-table
