@@ -287,8 +287,8 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  * Same rows, masks, outputs and conventions as paged_attention (q and out must
  * not overlap), with
  *   k_j = k_scale[page(j), head] * code,  v_j = v_scale[page(j), head] * code
- * (finite f32 scales >= 0).  V scales are best 0 or between 2^-90 and 2^90: smaller
- * ones leave an output an absolute error of up to 2^-106 for each key, larger ones
+ * (finite f32 scales >= 0).  V scales are best 0 or between 2^-80 and 2^90: smaller
+ * ones leave an output an absolute error of up to 2^-102 for each key, larger ones
  * may make it infinite; the LSE has its accuracy with any.  window = 0 attends as
  * `mask` says.  window > 0 (mask PKV_MASK_CAUSAL only): the row at position
  * p = kv_len - q_real + i sees the keys j <= p with j > p - window (its own key and
@@ -302,11 +302,14 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  * the same sequence does not must be finite: a row's weight for it is zero, and
  * zero times infinity or NaN is NaN.
  *
- * The softmax weights are rounded once before the P.V product: to f16 (2^-11
- * relative) by the few-row kernel, to bf16 (2^-8 at most) by the tile kernel;
- * sums, maxima and the LSE are f32.  The same call gives the same bits every
- * time.  Calls whose rows x grouped heads are many first expand the visible pages to bf16 in the workspace (code * scale, exact
- * for the power-of-two scales kv_append_fp8 writes).
+ * The softmax weights are rounded once before the P.V product: to bf16 (2^-8
+ * relative at most) by the tile kernel and over bf16 pools; by the few-row kernel
+ * over 8-bit pools to f16, times the V scale of their page (2^-11 relative from
+ * 2^-20 of the row's largest such product on, smaller ones to within 2^-31 of
+ * it); sums, maxima and the LSE are f32.  The same call gives the same bits every
+ * time.  Calls whose rows x grouped heads are many first expand the visible pages
+ * to bf16 in the workspace (code * scale, exact for the power-of-two scales
+ * kv_append_fp8 writes).
  *
  *  workspace      paged_attention_fp8_workspace_size(...) bytes, 256-byte
  *                 aligned; one workspace must not serve two calls in flight

@@ -25,8 +25,9 @@
 //    2^-22 below the row's largest.  A segment's rows sit in shared memory in
 //    fragment order, staged once for all consumers.
 //  * Weights are rounded once: to bf16 for bf16 pools, and w = 2^(a - M) vs to
-//    f16 for 8-bit ones, M following a + log2(vs), so w stays at or below 2^9
-//    for V scales of up to 2^90.  Sums, maxima and outputs are f32.
+//    f16 for 8-bit ones, M following a + log2(vs) - 6, so the largest w lies
+//    between 2^6 and 2^15 for V scales of 2^-80 to 2^90.  Sums, maxima and outputs
+//    are f32.
 //  * Per CTA one warp looks up pages and scales ahead, 32 chunks at a time, and
 //    one fills a ring of chunks (32 keys in 8 bits, 16 in bf16) by TMA, so the
 //    chain length -> table -> scale stays off the copies' path; each of four
@@ -68,12 +69,15 @@ namespace {
 
 constexpr int kPage = 32;
 constexpr float kLazy = 8.0f;         // move the reference only past 2^8 growth
-// 8-bit pools: M follows a + log2(vs) for V scales of 2^kLowScale to 2^kHighScale.
-// The sums of 2^(a - M), whose largest summand is 2^-90 to 2^98, then neither
-// vanish nor overflow for 2^29 keys.  Smaller scales (0 too) round the weights to
-// within 2^-106 of an output a key; larger ones overflow f16 to infinity, where
-// without kHighScale the sums would underflow and a row come out as zero.
-constexpr float kLowScale = -90.0f, kHighScale = 90.0f;
+// 8-bit pools: M follows a + log2(vs) - kWeightUp for V scales of 2^kLowScale to
+// 2^kHighScale.  A state's largest weight w is then 2^6 at least and below 2^15,
+// whatever vs in that range: f16 keeps 11 bits of weights down to 2^-20 of it (from
+// 2^-14 on without kWeightUp).  The sums of 2^(a - M), whose largest summand is
+// 2^-84 to 2^94, neither vanish nor overflow for as many keys as there can be.
+// Smaller scales (0 too) round the weights to within 2^-102 of an output a key;
+// larger ones overflow f16 to infinity, where without kHighScale the sums would
+// underflow and a row come out as zero.
+constexpr float kWeightUp = 6.0f, kLowScale = -80.0f, kHighScale = 90.0f;
 // PKV_FLAG_TEST_WAIT_TIMEOUT: the limit of the waits that are meant to run out
 // (consumers on a barrier nothing completes, the other warps' as they follow)
 constexpr uint64_t kTestWaitNs = 20000, kWaitNs = 2000000000ull;
@@ -408,10 +412,10 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, uint32_t qb, const 
             for (int e = 0; e < 4; ++e) s[0][j][e] += s[1][j][e];
     }
     // ---- weights
-    float lv = 0.f;  // log2 of the V scale, rounded down
+    float lv = 0.f;  // what M adds to a: log2 of the V scale, rounded down, less kWeightUp
     if constexpr (FP8) {
         const float e = static_cast<float>(static_cast<int>((__float_as_uint(ch.vs) >> 23) & 255u) - 127);
-        lv = fminf(fmaxf(e, kLowScale), kHighScale);
+        lv = fminf(fmaxf(e, kLowScale), kHighScale) - kWeightUp;
     }
     uint32_t pb[NT][MI][2];
     bool moved = false;
