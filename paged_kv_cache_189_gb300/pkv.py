@@ -443,6 +443,14 @@ def _states(q, out, lse, D):
     return st
 
 
+def _scratch(workspace, err):
+    """The tensors whose bytes are written without regard to their type."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("the workspace must be dense")
+    if err is not None and (err.dtype is not _I32 or not err.numel()):
+        raise ValueError("err must be an int32")
+
+
 def _on_device(tensors):
     """All on the current CUDA device: the launch goes there."""
     devs = {t.get_device() for t in tensors if t is not None}
@@ -485,6 +493,7 @@ def kv_append_fp8(k_src, v_src, block_table, kv_lens, q_indptr, k_pool, v_pool, 
     if k_src.dtype not in (_BF16, torch.float16, _F32):
         raise ValueError("sources must be bf16, f16 or f32")
     batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    _scratch(None, err)
     dev = _on_device((k_src, v_src, block_table, kv_lens, q_indptr, q_real, k_pool, v_pool, k_scale, v_scale, err))
     status = lib().kv_append_fp8(
         k_src.data_ptr(), v_src.data_ptr(), _dtype(k_src), st[0], st[1], block_table.data_ptr(), table_stride,
@@ -514,6 +523,7 @@ def paged_attention_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_len
     scale_stride = _scales(k_scale, v_scale, n, H)
     st = _states(q, out, lse, D)
     batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    _scratch(workspace, err)
     dev = _on_device((q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, q_real, out, lse,
                       workspace, err))
     status = lib().paged_attention_fp8(
@@ -543,6 +553,7 @@ def paged_attention_window(q, k_pool, v_pool, block_table, kv_lens, q_indptr, ou
         raise ValueError("pools must be bf16")
     st = _states(q, out, lse, D)
     batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    _scratch(workspace, err)
     dev = _on_device((q, k_pool, v_pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err))
     status = lib().paged_attention_window(
         q.data_ptr(), st[0], st[1], k_pool.data_ptr(), v_pool.data_ptr(), n, P, page_stride,

@@ -35,3 +35,46 @@ def test_scales_that_reach_past_their_storage(scales):
     and the append write, past the tensor."""
     with pytest.raises(ValueError):
         pkv._scales(scales, scales, *scales.shape)
+
+
+def args(op, **kw):
+    """A call whose tensors fit but for `kw`, and for not being on a GPU."""
+    pool = torch.zeros(N, 32, H, D, dtype=torch.bfloat16 if op == "window" else torch.uint8)
+    one = torch.ones(1, dtype=torch.int32)
+    a = dict(block_table=torch.zeros(1, 1, dtype=torch.int32), kv_lens=one, q_indptr=torch.tensor([0, 1]).int(),
+             k_pool=pool, v_pool=pool, max_q_rows=1, max_kv_len=1)
+    if op != "window":
+        a.update(k_scale=torch.ones(N, H), v_scale=torch.ones(N, H))
+    if op == "append":
+        a.update(k_src=torch.zeros(1, H, D), v_src=torch.zeros(1, H, D))
+    else:
+        a.update(q=torch.zeros(1, 2 * H, D, dtype=torch.bfloat16), out=torch.zeros(1, 2 * H, D))
+    if op == "window":
+        a.update(window=4)
+    a.update(kw)
+    return a
+
+
+CALL = {"append": pkv.kv_append_fp8, "fp8": pkv.paged_attention_fp8, "window": pkv.paged_attention_window}
+
+
+@pytest.mark.parametrize("op", CALL)
+def test_tensors_that_fit(op):
+    """The calls below are refused for what they change: this one only for its device."""
+    with pytest.raises(ValueError, match="CUDA device"):
+        CALL[op](**args(op))
+
+
+@pytest.mark.parametrize("op", ["fp8", "window"])
+def test_workspaces_that_reach_past_their_storage(op):
+    """An expanded tensor counts more bytes than it has."""
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            CALL[op](**args(op, workspace=ws))
+
+
+@pytest.mark.parametrize("op", CALL)
+@pytest.mark.parametrize("err", [torch.zeros(1, dtype=torch.uint8), torch.zeros(1), torch.zeros(0, dtype=torch.int32)])
+def test_error_flags(op, err):
+    with pytest.raises(ValueError, match="err"):
+        CALL[op](**args(op, err=err))
