@@ -436,11 +436,17 @@ def _states(q, out, lse, D):
     shape, st = q.shape, q.stride()
     if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != D or st[2] != 1:
         raise ValueError("q must be bf16 [rows, num_q_heads, head_dim] with unit last stride")
-    if out.shape != shape or not out.is_contiguous():
-        raise ValueError("out must be dense with the shape of q")
+    if out.shape != shape or not out.is_contiguous() or out.dtype not in _DTYPES:
+        raise ValueError("out must be dense bf16 or float32 with the shape of q")
     if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse must be dense float32 [rows, num_q_heads]")
     return st
+
+
+def _mask(name):
+    if name not in MASKS:
+        raise ValueError(f"mask {name!r} (one of {', '.join(MASKS)})")
+    return MASKS[name]
 
 
 def _scratch(workspace, err):
@@ -524,12 +530,13 @@ def paged_attention_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, kv_len
     st = _states(q, out, lse, D)
     batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
     _scratch(workspace, err)
+    mask = _mask(mask)
     dev = _on_device((q, k_pool, v_pool, k_scale, v_scale, block_table, kv_lens, q_indptr, q_real, out, lse,
                       workspace, err))
     status = lib().paged_attention_fp8(
         q.data_ptr(), st[0], st[1], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         scale_stride, n, P, page_stride, block_table.data_ptr(), table_stride, kv_lens.data_ptr(),
-        q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, q.shape[1], H, D, MASKS[mask],
+        q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, q.shape[1], H, D, mask,
         causal_block, window, num_sinks, scale, out.data_ptr(), _dtype(out), _address(lse), _address(workspace),
         _bytes(workspace), flags, _address(err), _launch_stream(stream, dev))
     if status:

@@ -65,6 +65,19 @@ def test_tensors_that_fit(op):
         CALL[op](**args(op))
 
 
+@pytest.mark.parametrize("dtype", [torch.float64, torch.int32, torch.uint8])
+@pytest.mark.parametrize("op", ["fp8", "window"])
+def test_output_types(op, dtype):
+    with pytest.raises(ValueError, match="out must be"):
+        CALL[op](**args(op, out=torch.zeros(1, 2 * H, D).to(dtype)))
+
+
+@pytest.mark.parametrize("mask", ["Causal", "", None, 1])
+def test_mask_names(mask):
+    with pytest.raises(ValueError, match="one of none, causal, block_causal"):
+        CALL["fp8"](**args("fp8", mask=mask))
+
+
 @pytest.mark.parametrize("op", ["fp8", "window"])
 def test_workspaces_that_reach_past_their_storage(op):
     """An expanded tensor counts more bytes than it has."""
