@@ -7,18 +7,20 @@ headline workload is the GQA decode batch (64 sequences, 32 query / 8 K/V
 heads, head_dim 128, 32-token pages, cached lengths U[512, 8192], one new
 token each); the metric is the K/V bytes the attention reads per second
 (paged decode KV GB/s), with queries/s and the fraction of the measured HBM
-peak alongside.  The same JSON line carries, under ``workloads``, every other
-workload measured the same way (chunked causal prefill and the block-causal
-video step in prefill TFLOP/s; the shared-prefix step, its one-launch form and
-the plain-decode ablation, multi-token decode and tiny decode in KV GB/s; the
-exact-window denoising forward in prefill TFLOP/s), each with its roofline,
-clocks, end-to-end figure and the fp64 oracle's time on the host cores.
+peak alongside.  Every other workload is measured the same way (chunked causal
+prefill and the block-causal video step in prefill TFLOP/s; the shared-prefix
+step, its one-launch form and the plain-decode ablation, multi-token decode and
+tiny decode in KV GB/s; the exact-window denoising forward in prefill TFLOP/s).
+The same JSON line carries each one's value, unit, ms per step and roofline
+fraction under ``workloads``; a JSON line on stderr has their whole entries, with
+roofline, clocks, end-to-end figure and the fp64 oracle's time on the host cores.
 
 Usage: ``python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 [--workload NAME] [--only]``.  ``--only`` measures just ``--workload``.
 Under torchrun every rank runs its own independent replica of each workload
 (seed + rank: weak scaling with no collective on the data path); rank 0 prints
-one JSON line.  ``--impl reference`` times the fp64 CPU oracle on a bounded
+one JSON line on stdout, short enough (under 3000 characters) for whoever keeps
+only the end of a log.  ``--impl reference`` times the fp64 CPU oracle on a bounded
 sample of the same workload instead.
 """
 from __future__ import annotations
@@ -1186,11 +1188,30 @@ def run_ours(args):
                            if k not in ("n_gpus", "higher_is_better", "scaling", "vs_baseline", "data",
                                         "dtype", "warmup")}
     if rank == 0:
-        if extra:
-            line["workloads"] = extra
-        print(json.dumps(line), flush=True)
+        report(line, extra)
     barrier(dist)
     return 0
+
+
+def _rounded(x):
+    """Floats to seven significant digits, all the way down."""
+    if isinstance(x, float):
+        return float(f"{x:.7g}")
+    if isinstance(x, dict):
+        return {k: _rounded(v) for k, v in x.items()}
+    return [_rounded(v) for v in x] if isinstance(x, (list, tuple)) else x
+
+
+def report(line, extra):
+    """The result on stdout as one line of under 3000 characters: the headline
+    workload's entry, and of the others value, unit, ms per step and roofline
+    fraction.  The others' whole entries go to stderr, before it."""
+    line = dict(line)
+    if extra:
+        print(json.dumps({"workloads": extra}), file=sys.stderr, flush=True)
+        line["workloads"] = {name: [float(f"{e['value']:.5g}"), e["unit"], float(f"{e['ms_per_step']:.4g}"),
+                                    float(f"{e['roofline']['frac']:.3g}")] for name, e in extra.items()}
+    print(json.dumps(_rounded(line)), flush=True)
 
 
 def packed_device(tensors, dev):
