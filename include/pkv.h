@@ -307,10 +307,12 @@ pkv_status kv_append_fp8(const void* k_src, const void* v_src, pkv_dtype src_dty
  * over 8-bit pools to f16, times the V scale of their page (2^-11 relative from
  * 2^-20 of the row's largest such product on, smaller ones to within 2^-31 of
  * it); sums, maxima and the LSE are f32.  The same call gives the same bits every
- * time.  Calls whose rows x grouped heads are many first expand the visible pages
- * to bf16 in the workspace (code * scale, exact for the power-of-two scales
- * kv_append_fp8 writes).
+ * time.  A NaN score makes its own row's output and LSE NaN.  Calls whose rows x
+ * grouped heads are many first expand the visible pages to bf16 in the workspace
+ * (code * scale, exact for the power-of-two scales kv_append_fp8 writes).
  *
+ *  num_pages      at least 1 where max_kv_len is not 0
+ *  max_q_rows, max_kv_len  at most 2^31 - 256
  *  workspace      paged_attention_fp8_workspace_size(...) bytes, 256-byte
  *                 aligned; one workspace must not serve two calls in flight
  *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY (a generic kernel without

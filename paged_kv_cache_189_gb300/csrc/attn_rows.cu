@@ -32,10 +32,10 @@
 //    one fills a ring of chunks (32 keys in 8 bits, 16 in bf16) by TMA, so the
 //    chain length -> table -> scale stays off the copies' path; each of four
 //    consumer warps owns every fourth stage and keeps its own softmax state: no
-//    barrier joins the consumers until a unit's end.  2 CTAs an SM (3 at 64-wide
-//    heads) keep 128 KB in flight; 192 KB, six consumers at 128 registers, or
-//    two chunks a step were no faster (107, 114 and 121 us where the first case
-//    below took 107).
+//    barrier joins the consumers until a unit's end.  2 CTAs an SM keep 128 KB in
+//    flight (3 at 64-wide heads and 8 rows: 144 KB); 192 KB, six consumers at 128
+//    registers, or two chunks a step were no faster (107, 114 and 121 us, of an
+//    earlier build that took 107 for the first case below).
 //  * Work: a unit is (sequence, K/V head, tile of 8 or 16 rows); its chunks are
 //    the pages its rows see.  All units' chunks form one line, laid out on the
 //    device (a captured call replays with other lengths), and the line is cut
@@ -54,9 +54,12 @@
 // 128, 8 bits, 524 MB: 105 us, 0.75 of the peak (the first chunk arrives after
 // 6 us, the CTAs stream at 0.93 of it and end within 13 us of each other, the
 // join takes 6); the same with 4 tokens a sequence 120 us, bound by the chunk's
-// chain of dependent steps at 8 warps an SM (one CTA of ten consumers an SM:
-// 154, nothing streams while it joins a unit); 3 sequences of 60000-131072 keys
-// 86 us (0.75); bf16 through a 4096-key window, 1020 MB: 167 us (0.91).
+// chain of dependent steps at 8 consumer warps an SM (the four that look up and
+// copy hold 168 registers a thread too; one CTA of ten consumers an SM: 154, nothing
+// streams while it joins a unit); 3 sequences of 60000-131072 keys 86 us (0.75);
+// bf16 through a 4096-key window, 1020 MB: 167 us (0.91).  Rows beyond 16 walk and
+// widen the keys again: 93, 161, 212, 283 and 321 us at 16, 32, 48, 64 and 80 rows
+// of 64 sequences of 2000-4000 keys (400 MB).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -88,7 +91,8 @@ constexpr int kBatches = 1;           // batches of 32 chunks it may be ahead
 template <int D, bool FP8, int NT>
 struct Cfg {
     static constexpr int kWarps = 4;                     // consumers
-    // 64-wide heads leave registers and ring space for a third CTA
+    // 64-wide heads leave ring space for a third CTA, at 96 registers a thread
+    // (8-bit pools spill 36 bytes at that)
     static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 3 : 2;
     static constexpr int kRingBytes = (kCtasPerSm == 3 ? 48 : 64) * 1024;
     static constexpr int kRedRows = 8;                   // rows joined at a time: a tile
@@ -96,7 +100,7 @@ struct Cfg {
     static constexpr int kKeys = FP8 ? 32 : 16;          // keys of a chunk
     static constexpr int kTile = kKeys * D * (FP8 ? 1 : 2);
     static constexpr int kStage = 2 * kTile;             // K, V
-    static constexpr int kStages = kRingBytes / kStage;  // 12 (head dim 128), 24 (64)
+    static constexpr int kStages = kRingBytes / kStage;  // 8 (head dim 128), 16 (64; 12 with three CTAs)
     static constexpr int kOwn = kStages / kWarps;        // stages of one consumer
     static constexpr int kRows = 8 * NT;
     static constexpr int kRedStride = D + 4;

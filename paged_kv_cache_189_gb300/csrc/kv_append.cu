@@ -16,14 +16,17 @@
 // lanes a row) are all loaded at once, before the page is looked up, and stay
 // in registers between the maximum (packed, two elements an instruction) and
 // the conversion: every source byte is read once.  4-byte rows would take 128
-// registers; they are read a second time, from cache.
+// registers; they are loaded twice, both times marked for early eviction as the
+// others are.
 // Bound: HBM for chunks (2 bytes read and 1 written per bf16 element), launch
 // and one chain of dependent loads (lengths, page id, old scale) for one token
 // per sequence.  Measured: 48.3 MB of four ragged prompt chunks (eight heads of
-// 128) 13 us, 0.56 of the copy peak, about 4 of them the chain and the launch;
-// one token into each of 64 sequences 6 us.  Streaming loads took the chunks
-// from 14.6 to 13 us (the rows are read once); 4 blocks of 4 warps an SM beat 5
-// to 8 with spills (16.4) and a second read instead of registers (16.9).
+// 128) 13 us, 0.56 of the copy peak, from bf16 or f16 rows (1040 blocks on the 608
+// places there are, two waves, each with the chain of loads: about 4 us with the
+// launch); 80.6 MB from f32 rows 32 us, 0.38 of it; one token into each of 64
+// sequences 6 us.  Streaming loads took the 2-byte chunks from 14.6 to 13 us (the
+// rows are read once); 4 blocks of 4 warps an SM beat 5 to 8 with spills (16.4) and
+// a second read instead of registers (16.9).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <algorithm>

@@ -719,10 +719,14 @@ struct ExtPlan {
 // (query row, grouped head) pairs of a K/V head up to which the few-row kernel
 // runs.  It reads the cache once per 16 of them (through L2), the tile kernel
 // once, but an 8-bit one only after its expansion to bf16.  Measured (us,
-// few-row / tile): 64 sequences of 2000-4000 keys, 32 / 8 heads of 128: 8 bits
-// 297 / 382 at 64 pairs, 338 / 383 at 80, 421 / 380 at 96; bf16 through a
-// 1024-key window 73 / 109 at 16, 117 / 99 at 32.  One sequence of 30000 keys,
-// 8 bits: 56 / 123 at 80.
+// few-row / tile), 32 / 8 heads of 128: 64 sequences of 2000-4000 keys, 8 bits
+// 283 / 380 at 64 pairs, 321 / 381 at 80, 399 / 379 at 96; bf16 through a
+// 1024-key window 72 / 111 at 16, 115 / 99 at 32.  Four such sequences: 8 bits
+// 39 / 44 at 80, 41 / 44 at 96, 58 / 51 at 128; bf16 21 / 25 at 16, 23 / 23 at 32,
+// 27 / 25 at 48.  16 sequences of 2000-8000 keys, 16 / 2 heads of 64, 8 bits: 49 / 51
+// at 96, 53 / 49 at 128.  The rule counts pairs, not units: for one sequence of
+// 30000 keys, 8 bits, it is right at 80 (58 / 125) and takes the slower kernel
+// beyond (66 / 116 at 96, 80 / 118 at 128).
 constexpr int kFewRowsFp8 = 80, kFewRowsBf16 = 16;
 // keys and query rows of a sequence: rounded up to tiles they stay in 32 bits
 constexpr int kExtMost = 0x7fffff00;
