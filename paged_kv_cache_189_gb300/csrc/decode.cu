@@ -525,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
     const int Hkv = p.num_kv_heads;
     const int SK = p.split_keys;
     const int S_ = p.num_splits;
-    const int64_t rows_bound = static_cast<int64_t>(p.batch) * p.max_q_rows;
 
     if ((smem_u32(smem) & 1023u) != 0) {  // never expected; refuse rather than misread tiles
         if (threadIdx.x == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
@@ -782,14 +781,16 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
                     if (p.out_f32) static_cast<float*>(p.out)[st * D + dd] = O;
                     else static_cast<__nv_bfloat16*>(p.out)[st * D + dd] = __float2bfloat16_rn(O);
                     if (p.lse && dd == 0) p.lse[st] = lse;
-                } else if (d.r0 < rows_bound) {
-                    p.ws_o[(st * S_ + d.split) * D + dd] = O;
-                    if (dd == 0) p.ws_lse[st * S_ + d.split] = lse;
+                } else {
+                    // by sequence and head: the packed rows may start anywhere
+                    const int64_t ws = (static_cast<int64_t>(bh) * G + g) * S_ + d.split;
+                    p.ws_o[ws * D + dd] = O;
+                    if (dd == 0) p.ws_lse[ws] = lse;
                 }
             }
             consumer_sync();  // red_o is rewritten by the next round
         }
-        if (partial && d.r0 < rows_bound) {
+        if (partial) {
             // the last split of this (sequence, K/V head) to finish merges all
             __threadfence();
             consumer_sync();
@@ -805,8 +806,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks)
                 for (int e = threadIdx.x; e < G * D; e += kWarps * 32) {
                     const int g = e / D, dd = e - (e / D) * D;
                     const int64_t st = static_cast<int64_t>(d.r0) * Hq + d.kvh * G + g;
-                    const float* lses = p.ws_lse + st * S_;
-                    const float* os = p.ws_o + st * S_ * D + dd;
+                    const int64_t ws_st = static_cast<int64_t>(bh) * G + g;
+                    const float* lses = p.ws_lse + ws_st * S_;
+                    const float* os = p.ws_o + ws_st * S_ * D + dd;
                     // the splits' states eight at a time, all loads in flight
                     // together, merged online (one chunk: max first, then sums)
                     float M = -INFINITY, L = 0.f, O = 0.f;

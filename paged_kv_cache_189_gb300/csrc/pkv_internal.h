@@ -171,8 +171,8 @@ struct AttnParams {
     float* lse;
     int num_splits;
     int split_keys;    // keys per split (multiple of the key tile)
-    float* ws_o;       // [rows_bound][Hq][splits][D] partial outputs (splits > 1)
-    float* ws_lse;     // [rows_bound][Hq][splits]
+    float* ws_o;       // [batch * max_q_rows][Hq][splits][D] partial outputs (splits > 1)
+    float* ws_lse;     // [batch * max_q_rows][Hq][splits]
     int* ws_counters;  // decode: [0] unit ticket, [1 + b*Hkv + h] finished splits
     bool planned;      // decode: units taken from the planned order (else split-major)
     bool checked;

@@ -56,3 +56,23 @@ def test_rows_behind_others_without_a_window(new, splits):
                         workspace=ws)
     torch.cuda.synchronize()
     hold(c, out, lse, 777)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 5])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 2, 64)])
+@pytest.mark.parametrize("before", [1, 1000])
+def test_decode_rows_behind_others(before, Hq, Hkv, D, splits):
+    """The decode kernel of paged_attention, its keys split or not."""
+    kv = [5200, 6100, 33]
+    c = Case(kv, [1] * 3, [1] * 3, Hq, Hkv, D, False, window=max(kv), seed=62)
+    t, out, lse = moved(c, before)
+    ws = torch.full((pkv.paged_attention_workspace_size(3, 1, Hq, Hkv, D, max(kv), splits),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    for _ in range(2):  # the split counts are left as they were found
+        out.fill_(9)
+        lse.fill_(9)
+        pkv.paged_attention(t["q"], t["k_pool"], t["v_pool"], t["table"], t["kv_lens"], t["q_indptr"], out,
+                            q_real=t["q_real"], lse=lse, max_q_rows=1, max_kv_len=max(kv), num_splits=splits,
+                            workspace=ws)
+        torch.cuda.synchronize()
+        hold(c, out, lse, before)
