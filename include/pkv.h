@@ -644,6 +644,189 @@ pkv_status merge_attn_states(const void* o_a, const float* lse_a, const void* o_
 pkv_status rotate_rows(void* x, int64_t rows, int64_t cols, int64_t row_stride,
                        int elem_size, int64_t shift, void* stream);
 
+/*
+ * assign_step_pages -- the block tables and slot maps of a serving step, built
+ * on the device from the requests' lengths.
+ *
+ * Sequence b holds kv_lens[b] keys in its first ceil(kv_lens[b] / 32) pages of
+ * block_table and asks for new_lens[b] more; new_lens[b] < 0 says that it has
+ * finished, 0 that it waits.  free_pages[0 .. *num_free) is a stack of free
+ * pages, its top last.
+ *  1. Finished sequences give their pages back: in the order of sequences and
+ *     of their pages, each is pushed onto the stack.
+ *  2. need[b] = ceil((kv_lens[b] + new_lens[b]) / 32) - ceil(kv_lens[b] / 32) for
+ *     new_lens[b] > 0, else 0.  A request is granted when
+ *       the sum of new_lens > 0 up to and with it is at most max_tokens,
+ *       its pages fit block_table_stride, and
+ *       need[b] = 0, or the sum of need up to and with it is at most the
+ *       stack's height after step 1 (so a sequence with room in its last page
+ *       is never held up).
+ *     A request that is not granted takes nothing; the caller asks again.
+ *  3. Granted requests take their pages from the stack's top, in the order of
+ *     sequences and of their pages, into block_table[b][ceil(kv_lens[b] / 32)...].
+ *  4. kv_lens_out[b] = the keys with this step's (0 for a finished sequence),
+ *     *num_free_out = the stack's height, q_indptr[0 .. batch] = running sum of
+ *     the granted tokens.  For token t of sequence b (q_indptr[b] <= t <
+ *     q_indptr[b + 1]): positions[t] = kv_lens[b] + t - q_indptr[b], slots[t] = its
+ *     slot, as kv_scatter_slots, rope_write_kv_paged and kv_append_latent take
+ *     them.  slots[t] = -1, positions[t] = 0 for q_indptr[batch] <= t < max_tokens.
+ * Other table entries and the stack's entries below its height stay as they
+ * are; a finished sequence's table row is not cleared.  With kv_lens_out and
+ * num_free_out apart from the inputs the same call gives the same results
+ * again; they may also be the inputs themselves (a step replayed in a CUDA graph).
+ *
+ *  new_lens, kv_lens, kv_lens_out   device int32 [batch]
+ *  num_free, num_free_out           device int32
+ *  free_pages       device int32 [free_capacity], room for every page that is
+ *                   pushed: pushes past free_capacity are dropped
+ *  block_table      device int32 [batch][block_table_stride]
+ *  q_indptr         device int32 [batch + 1]
+ *  slots, positions device int64 [max_tokens]
+ *  batch            at most 4096; max_tokens at most 2^30
+ *  err              nullable device int32: a pushed page that was dropped, a
+ *                   negative length or *num_free outside [0, free_capacity] (both
+ *                   taken as the nearest valid value) OR PKV_ERRBIT_PAGE; a
+ *                   request refused for max_tokens or block_table_stride ORs
+ *                   PKV_ERRBIT_LEN
+ */
+pkv_status assign_step_pages(const int32_t* new_lens, const int32_t* kv_lens,
+                             const int32_t* num_free, int32_t* free_pages, int64_t free_capacity,
+                             int32_t* block_table, int64_t block_table_stride, int batch,
+                             int max_tokens, int page_size, int32_t* kv_lens_out,
+                             int32_t* num_free_out, int32_t* q_indptr, int64_t* slots,
+                             int64_t* positions, int32_t* err, void* stream);
+
+/*
+ * kv_append_latent -- normalise, rotate and write this step's latent rows.
+ *
+ * The latent cache keeps one row of latent_dim + rope_dim elements a token,
+ * shared by all heads: a normalised vector from which every head's keys and
+ * values are projections, and a rotary key part.  Page p starts at element
+ * p * page_stride and holds 32 such rows, dense.
+ *
+ * For t in [0, num_tokens), x = source row t, n = latent_dim:
+ *   r = 1 / sqrt(mean(x[0 .. n)^2) + eps)
+ *   row[i]     = x[i] * r * norm_weight[i]  (norm_weight NULL: row[i] = x[i])
+ *   row[n ...] = the rope_dim rotary elements of x, rotated to positions[t]
+ *   pool slot slots[t] <- row   (slots[t] < 0: not written)
+ *   q_out[t, h, :] = q_pe[t, h, :] rotated to positions[t], every head
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin) with cos = cos_sin[
+ * position][i], sin = cos_sin[position][rope_dim / 2 + i] for pair i: elements
+ * (i, i + rope_dim / 2), or (2 i, 2 i + 1) with `interleaved`, in place.  All in
+ * f32, rounded to bf16 once.
+ *
+ *  src           device bf16, row t at t * src_stride
+ *  norm_weight   device bf16 [latent_dim] or NULL
+ *  positions     device int64 [num_tokens]; outside [0, max_position) they are
+ *                clamped (and PKV_ERRBIT_LEN with PKV_FLAG_CHECKED)
+ *  cos_sin       device f32 [max_position][rope_dim]
+ *  slots         device int64 [num_tokens]; slots at or past num_pages * 32 are
+ *                skipped (and PKV_ERRBIT_SLOT with PKV_FLAG_CHECKED)
+ *  q_pe, q_out   device bf16, element (t, h, i) at t * token_stride + h *
+ *                head_stride + i; num_heads = 0: neither is used.  q_out may be
+ *                q_pe (with its strides), else they must not overlap
+ *  latent_dim 512, rope_dim 64, page_size 32; 16-byte aligned pointers, strides
+ *  multiples of 8
+ */
+pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tokens,
+                            const void* norm_weight, float eps, const int64_t* positions,
+                            const float* cos_sin, int64_t max_position, int interleaved,
+                            const int64_t* slots, void* pool, int64_t num_pages, int page_size,
+                            int64_t page_stride, int latent_dim, int rope_dim, const void* q_pe,
+                            int64_t q_pe_token_stride, int64_t q_pe_head_stride, void* q_out,
+                            int64_t q_out_token_stride, int64_t q_out_head_stride, int num_heads,
+                            unsigned flags, int32_t* err, void* stream);
+
+/*
+ * paged_attention_latent -- attention over the paged latent rows themselves
+ * (absorbed form: the per-head key projection is folded into the queries, the
+ * value projection is applied to the output by the caller).
+ *
+ * Rows, lengths, padding and outputs as in paged_attention, with one K/V head
+ * whose key j is the whole latent row c_j and whose value is its first
+ * latent_dim elements:
+ *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . c_j) c_j[0 .. latent_dim)
+ *   lse[r, h]    = ln sum_j exp(scale * q[r, h] . c_j)
+ * mask PKV_MASK_NONE or PKV_MASK_CAUSAL.  The softmax weights are rounded once
+ * to bf16 before the product with the values (2^-8 relative at most), and the
+ * output is divided by the sum of the rounded ones; sums, maxima and the LSE
+ * are f32.  The same call gives the same bits every time.
+ *
+ * The bytes of slots past the last key, and the scores of masked keys, never
+ * reach a result; block-table entries of pages that no row sees may hold
+ * anything, and an entry outside [0, num_pages) is read as a page of zeros (and
+ * PKV_ERRBIT_PAGE with PKV_FLAG_CHECKED).  The row of a key that one query row
+ * sees and another does not must be finite.  A NaN score makes its own row's
+ * output and LSE NaN.
+ *
+ *  q              device bf16 [rows][num_heads][latent_dim + rope_dim] with any
+ *                 token / head stride of whole 16 bytes; must not overlap out
+ *  pool           device bf16 pages, 16-byte aligned, page_stride >= 32 *
+ *                 (latent_dim + rope_dim), a multiple of 8
+ *  scale          > 0 and finite (the wide latent rows give no default)
+ *  out            device [rows][num_heads][latent_dim], bf16 or f32 (dense)
+ *  workspace      paged_attention_latent_workspace_size(...) bytes, 256-byte
+ *                 aligned; one workspace must not serve two calls in flight
+ *  max_q_rows * num_heads, max_kv_len  at most 2^31 - 256
+ *  latent_dim 512, rope_dim 64, page_size 32
+ *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY (a generic kernel without
+ *                 a workspace)
+ */
+size_t paged_attention_latent_workspace_size(int batch, int max_q_rows, int num_heads,
+                                             int max_kv_len, int latent_dim, int rope_dim,
+                                             unsigned flags);
+pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const void* pool, int64_t num_pages, int page_size,
+                                  int64_t page_stride, const int32_t* block_table,
+                                  int64_t block_table_stride, const int32_t* kv_lens,
+                                  const int32_t* q_indptr, const int32_t* q_real, int batch,
+                                  int max_q_rows, int max_kv_len, int num_heads, int latent_dim,
+                                  int rope_dim, pkv_mask mask, float scale, void* out,
+                                  pkv_dtype out_dtype, float* lse, void* workspace,
+                                  size_t workspace_bytes, unsigned flags, int32_t* err, void* stream);
+
+/*
+ * ragged_attention_latent -- attention over keys and values expanded from
+ * latent rows (prompts: the projections cost less than wide scores).
+ *
+ * Sequence b's query rows are q_indptr[b] .. q_indptr[b + 1] - 1 of q, its keys
+ * rows kv_indptr[b] .. kv_indptr[b + 1] - 1 of k, k_pe and v; the query rows are
+ * the last keys' (row i at position kv - rows + i).  Head h's key j is k[j, h]
+ * (nope_dim elements) followed by k_pe[j] (rope_dim elements, the same for all
+ * heads), as q[r, h] lies:
+ *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . key_j) v[j, h, :]
+ *   lse[r, h]    = ln sum_j exp(scale * q[r, h] . key_j)
+ * over the visible keys (PKV_MASK_NONE: all; PKV_MASK_CAUSAL: j <= kv - rows + i).
+ * Rows that see no key: out = 0, lse = -inf.  Rounding, masked scores and NaN as
+ * in paged_attention_latent; V rows of keys that no row of the call sees may
+ * hold anything.  out and lse are joined with those over a cached prefix by
+ * merge_attn_states.
+ *
+ *  q              device bf16, element (r, h, d) at r * q_token_stride + h *
+ *                 q_head_stride + d
+ *  k, v           device bf16 [num_keys][num_heads][...] with token and head
+ *                 strides of their own (slices of one projection's output)
+ *  k_pe           device bf16, row j at j * k_pe_stride
+ *  num_keys       rows of k, k_pe and v; rows past it count as zeros
+ *  max_q_rows, max_kv_len  HOST upper bounds per sequence (rows and keys beyond
+ *                 them are not attended: longer rows stay unwritten)
+ *  scale          > 0 and finite
+ *  out            device [rows][num_heads][v_dim], bf16 or f32 (dense)
+ *  nope_dim 128, rope_dim 64, v_dim 128; pointers 16-byte aligned, strides
+ *  multiples of 8
+ *  flags          PKV_FLAG_CHECKED (lengths beyond the bounds OR PKV_ERRBIT_LEN),
+ *                 PKV_FLAG_SIMT_ONLY
+ */
+pkv_status ragged_attention_latent(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                   const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                   const void* k_pe, int64_t k_pe_stride, const void* v,
+                                   int64_t v_token_stride, int64_t v_head_stride, int64_t num_keys,
+                                   const int32_t* q_indptr, const int32_t* kv_indptr, int batch,
+                                   int max_q_rows, int max_kv_len, int num_heads, int nope_dim,
+                                   int rope_dim, int v_dim, pkv_mask mask, float scale, void* out,
+                                   pkv_dtype out_dtype, float* lse, unsigned flags, int32_t* err,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

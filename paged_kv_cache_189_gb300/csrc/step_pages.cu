@@ -1,0 +1,211 @@
+// step_pages.cu -- assign_step_pages: a step's block tables, query ranges and
+// slot map from the requests' lengths, in one launch.
+//
+// The rules are running sums over the batch (tokens asked for, pages needed,
+// pages given back), so every CTA of one cluster reads all lengths and computes
+// them for itself; only the writes are shared out.  One cluster barrier
+// separates reading the inputs and pushing the finished sequences' pages from
+// everything that is written over them or read from the stack.  A call is
+// latency: launch, lengths, four block scans, stack or table look-up, store.
+#include <cooperative_groups.h>
+
+#include "latent.h"
+#include "pkv_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMaxPer = 8;  // sequences a thread holds: 4096 / 512
+constexpr int kCluster = 8;
+
+// Exclusive running sum over the block of one 64-bit value a thread; the total in *total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
+    __shared__ int64_t part[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous scan's parts have been read
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? part[w] : 0;
+        all += part[w];
+    }
+    *total = all;
+    return before + x - v;
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t keys) { return (keys + 31) >> 5; }
+
+__global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArgs a) {
+    // per sequence: end of its tokens, first page number it takes (or gives back), keys before the step
+    extern __shared__ int32_t state[];
+    int32_t* tok_end = state;
+    int32_t* page_at = state + a.batch;
+    int32_t* kv_of = state + 2 * a.batch;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+    const int tid = threadIdx.x;
+    const int per = (a.batch + kThreads - 1) / kThreads;
+    const int64_t stride = a.block_table_stride;
+
+    int kv[kMaxPer], ask[kMaxPer];  // ask < 0: finished
+    int64_t tokens = 0, need = 0, back = 0;
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxPer; ++k) {
+        const int b = tid * per + k;
+        kv[k] = ask[k] = 0;
+        if (k >= per || b >= a.batch) continue;
+        kv[k] = a.kv_lens[b];
+        ask[k] = a.new_lens[b];
+        if (kv[k] < 0) {
+            kv[k] = 0;
+            bad |= PKV_ERRBIT_PAGE;
+        }
+        tokens += max(ask[k], 0);
+        if (ask[k] > 0) need += pages_of(int64_t(kv[k]) + ask[k]) - pages_of(kv[k]);
+        if (ask[k] < 0) back += min(pages_of(kv[k]), stride);
+    }
+    const int free_in = *a.num_free;
+    const int64_t height = min(max(int64_t(free_in), int64_t(0)), a.free_capacity);
+    if (height != free_in) bad |= PKV_ERRBIT_PAGE;
+    int64_t total, back_total;
+    int64_t token_sum = block_scan(tokens, &total);
+    int64_t need_sum = block_scan(need, &total);
+    int64_t back_sum = block_scan(back, &back_total);
+    const int64_t top = min(height + back_total, a.free_capacity);
+    if (height + back_total > a.free_capacity) bad |= PKV_ERRBIT_PAGE;
+
+    int take[kMaxPer];
+    int64_t took = 0, granted = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxPer; ++k) {
+        take[k] = 0;
+        const int b = tid * per + k;
+        if (k >= per || b >= a.batch) continue;
+        if (ask[k] < 0) {
+            page_at[b] = static_cast<int32_t>(back_sum);
+            back_sum += min(pages_of(kv[k]), stride);
+        } else if (ask[k] > 0) {
+            const int64_t n = pages_of(int64_t(kv[k]) + ask[k]) - pages_of(kv[k]);
+            token_sum += ask[k];
+            need_sum += n;
+            const bool room = token_sum <= a.max_tokens && pages_of(int64_t(kv[k]) + ask[k]) <= stride;
+            if (!room) bad |= PKV_ERRBIT_LEN;
+            if (room && (n == 0 || need_sum <= top)) take[k] = static_cast<int>(n);
+            else ask[k] = 0;
+            took += take[k];
+            granted += ask[k];
+        }
+    }
+    int64_t took_total, granted_total;
+    int64_t took_sum = block_scan(took, &took_total);
+    int64_t token_end = block_scan(granted, &granted_total);
+#pragma unroll
+    for (int k = 0; k < kMaxPer; ++k) {
+        const int b = tid * per + k;
+        if (k >= per || b >= a.batch) continue;
+        if (ask[k] >= 0) page_at[b] = static_cast<int32_t>(took_sum);
+        took_sum += take[k];
+        token_end += max(ask[k], 0);
+        tok_end[b] = static_cast<int32_t>(token_end);
+        kv_of[b] = ask[k] < 0 ? -1 - kv[k] : kv[k];  // finished: below zero
+    }
+    if (bad && rank == 0) set_err(a.err, bad);
+    __syncthreads();
+
+    // finished sequences' pages onto the stack, a warp a sequence
+    const int lane = tid & 31;
+    const int wid = rank * (kThreads / 32) + (tid >> 5), warps = ranks * (kThreads / 32);
+    if (back_total > 0) {
+        for (int b = wid; b < a.batch; b += warps) {
+            if (kv_of[b] >= 0) continue;
+            const int64_t held = min(pages_of(-1 - int64_t(kv_of[b])), stride);
+            for (int64_t i = lane; i < held; i += 32)
+                if (height + page_at[b] + i < a.free_capacity)
+                    a.free_pages[height + page_at[b] + i] = a.block_table[b * stride + i];
+        }
+        __threadfence();
+    }
+    cluster.sync();
+
+    // page number n of those taken lies n below the top
+    auto stack_page = [&](int64_t n) { return a.free_pages[top - 1 - n]; };
+    if (took_total > 0) {
+        for (int b = wid; b < a.batch; b += warps) {
+            if (kv_of[b] < 0) continue;
+            const int64_t held = pages_of(kv_of[b]);
+            const int64_t new_keys = int64_t(tok_end[b]) - (b > 0 ? tok_end[b - 1] : 0);
+            const int64_t count = pages_of(kv_of[b] + new_keys) - held;
+            for (int64_t i = lane; i < count; i += 32) a.block_table[b * stride + held + i] = stack_page(page_at[b] + i);
+        }
+    }
+    for (int64_t t = rank * kThreads + tid; t < a.max_tokens; t += ranks * kThreads) {
+        int64_t pos = 0, slot = -1;
+        if (t < granted_total) {
+            int lo = 0, hi = a.batch - 1;  // the first sequence whose tokens end past t
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (tok_end[mid] > t) hi = mid;
+                else lo = mid + 1;
+            }
+            pos = int64_t(kv_of[lo]) + t - (lo > 0 ? tok_end[lo - 1] : 0);
+            const int64_t lp = pos >> 5, held = pages_of(kv_of[lo]);
+            const int64_t page = lp < held ? a.block_table[lo * stride + lp] : stack_page(page_at[lo] + lp - held);
+            slot = page * 32 + (pos & 31);
+        }
+        a.slots[t] = slot;
+        a.positions[t] = pos;
+    }
+    if (rank == 0) {
+        for (int b = tid; b < a.batch; b += kThreads) {
+            const int end = tok_end[b], begin = b > 0 ? tok_end[b - 1] : 0;
+            a.q_indptr[b + 1] = end;
+            a.kv_lens_out[b] = kv_of[b] < 0 ? 0 : kv_of[b] + (end - begin);
+        }
+        if (tid == 0) {
+            a.q_indptr[0] = 0;
+            *a.num_free_out = static_cast<int32_t>(top - took_total);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_step_pages(const StepPagesArgs& a, cudaStream_t s) {
+    // one CTA writes 2048 tokens in four rounds; more are shared out over a cluster
+    const bool wide = a.max_tokens > 2048 || a.batch > 256;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = wide ? kCluster : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(wide ? kCluster : 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.batch) * 12;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static DeviceOnce opted;  // 4096 sequences take 48 KB beside the scans' parts
+    int dev = 0, done = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = opted.get(dev, &done, [&](int, int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(step_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 12);
+    });
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, step_pages_kernel, a);
+}
+
+}  // namespace pkv

@@ -33,7 +33,9 @@ EXPORTED = ("pkv_status_string", "pkv_last_error", "kv_scatter_slots",
             "causal_layout", "plan_shared_prefix", "shared_prefix_attention",
             "shared_prefix_attention_workspace_size", "pkv_plan_attention", "kv_append_fp8",
             "paged_attention_fp8_workspace_size", "paged_attention_fp8",
-            "paged_attention_window_workspace_size", "paged_attention_window")
+            "paged_attention_window_workspace_size", "paged_attention_window", "assign_step_pages",
+            "kv_append_latent", "paged_attention_latent_workspace_size", "paged_attention_latent",
+            "ragged_attention_latent")
 NO_ALLOC_SCRATCH_BYTES = 32 << 20
 
 _vp, _i64, _i32, _u32, _f32, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
@@ -78,6 +80,17 @@ _SIGNATURES = {
     "paged_attention_window": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _vp, _vp,
                                       _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp,
                                       _vp, _sz, _u32, _vp, _vp]),
+    "assign_step_pages": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _vp]),
+    "kv_append_latent": (_i32, [_vp, _i64, _i64, _vp, _f32, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _i64,
+                                _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _u32, _vp, _vp]),
+    "paged_attention_latent_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _u32]),
+    "paged_attention_latent": (_i32, [_vp, _i64, _i64, _vp, _i64, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _i32,
+                                      _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp, _vp, _sz, _u32,
+                                      _vp, _vp]),
+    "ragged_attention_latent": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
+                                       _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp,
+                                       _u32, _vp, _vp]),
 }
 
 _lib = None
@@ -570,3 +583,162 @@ def paged_attention_window(q, k_pool, v_pool, block_table, kv_lens, q_indptr, ou
         _launch_stream(stream, dev))
     if status:
         _check("paged_attention_window", status)
+
+
+# ----------------------------------------------------------------------------
+LATENT_DIM, LATENT_ROPE = 512, 64
+NOPE_DIM, EXPANDED_V = 128, 128
+_I64 = torch.int64
+
+
+def _vector(t, name, dtype, count):
+    if t.dtype is not dtype or t.numel() < count or not t.is_contiguous():
+        raise ValueError(f"{name} must be dense {dtype} with room for {count}")
+
+
+def _row_strides(shape, st, width):
+    """Token and head stride of a [tokens, heads, width] tensor; axes of one
+    element take the dense stride (theirs may say anything)."""
+    head = st[1] if shape[1] > 1 else width
+    return (st[0] if shape[0] > 1 else head * shape[1]), head
+
+
+def _latent_pool(pool):
+    """Pages and page stride of a latent pool."""
+    shape, st = pool.shape, pool.stride()
+    if pool.dtype is not _BF16 or len(shape) != 3 or shape[2] != LATENT_DIM + LATENT_ROPE:
+        raise ValueError("the pool must be bf16 [num_pages, page_size, 512 + 64]")
+    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError("pool slots must be dense")
+    return shape[0], shape[1], st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, kv_lens_out, num_free_out, q_indptr,
+                      slots, positions, err=None, stream=None):
+    """Block tables, query ranges and slot map of a step, built on the device:
+    ``new_lens [batch]`` tokens are asked for by sequences of ``kv_lens`` keys
+    (below zero: finished), pages come from and go back to the stack
+    ``free_pages[:num_free]`` (see ``include/pkv.h``).  ``kv_lens_out`` and
+    ``num_free_out`` may be the inputs themselves."""
+    batch, tokens, shape = new_lens.numel(), slots.numel(), block_table.shape
+    _vector(new_lens, "new_lens", _I32, batch)
+    _vector(kv_lens, "kv_lens", _I32, batch)
+    _vector(num_free, "num_free", _I32, 1)
+    _vector(free_pages, "free_pages", _I32, 0)
+    _vector(kv_lens_out, "kv_lens_out", _I32, batch)
+    _vector(num_free_out, "num_free_out", _I32, 1)
+    _vector(q_indptr, "q_indptr", _I32, batch + 1)
+    _vector(slots, "slots", _I64, tokens)
+    _vector(positions, "positions", _I64, tokens)
+    if block_table.dtype is not _I32 or len(shape) != 2 or shape[0] < batch or not block_table.is_contiguous():
+        raise ValueError("block_table must be dense int32 [batch, pages]: its width bounds a sequence's pages")
+    _scratch(None, err)
+    dev = _on_device((new_lens, kv_lens, num_free, free_pages, block_table, kv_lens_out, num_free_out, q_indptr, slots,
+                      positions, err))
+    status = lib().assign_step_pages(
+        new_lens.data_ptr(), kv_lens.data_ptr(), num_free.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+        block_table.data_ptr(), shape[1], batch, tokens, 32, kv_lens_out.data_ptr(), num_free_out.data_ptr(),
+        q_indptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), _address(err), _launch_stream(stream, dev))
+    if status:
+        _check("assign_step_pages", status)
+
+
+def kv_append_latent(src, positions, cos_sin, slots, pool, *, norm_weight=None, eps=1e-6, q_pe=None, q_out=None,
+                     interleaved=False, checked=False, err=None, stream=None):
+    """Normalise ``src[:, :512]`` by its root mean square (with
+    ``norm_weight``), rotate ``src[:, 512:]`` and write the rows into pool slots
+    ``slots``; rotate ``q_pe [T, H, 64]`` into ``q_out`` (see ``include/pkv.h``)."""
+    n, P, page_stride = _latent_pool(pool)
+    shape, st = src.shape, src.stride()
+    if src.dtype is not _BF16 or len(shape) != 2 or shape[1] != LATENT_DIM + LATENT_ROPE or st[1] != 1:
+        raise ValueError("src must be bf16 [tokens, 512 + 64] with unit last stride")
+    T, heads, qs, os = shape[0], 0, (0, 0), (0, 0)
+    _vector(positions, "positions", _I64, T)
+    _vector(slots, "slots", _I64, T)
+    if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or cos_sin.shape[1] != LATENT_ROPE or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be dense float32 [max_position, 64]")
+    if norm_weight is not None:
+        _vector(norm_weight, "norm_weight", _BF16, LATENT_DIM)
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out come together")
+    if q_pe is not None:
+        for t in (q_pe, q_out):
+            if t.dtype is not _BF16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != LATENT_ROPE or t.stride(2) != 1:
+                raise ValueError("q_pe and q_out must be bf16 [tokens, heads, 64] with unit last stride")
+        if q_out.shape != q_pe.shape:
+            raise ValueError("q_pe and q_out must have the same shape")
+        heads = q_pe.shape[1]
+        qs, os = _row_strides(q_pe.shape, q_pe.stride(), LATENT_ROPE), _row_strides(q_out.shape, q_out.stride(), LATENT_ROPE)
+    _scratch(None, err)
+    dev = _on_device((src, positions, cos_sin, slots, pool, norm_weight, q_pe, q_out, err))
+    status = lib().kv_append_latent(
+        src.data_ptr(), st[0] if T > 1 else shape[1], T, _address(norm_weight), eps, positions.data_ptr(),
+        cos_sin.data_ptr(), cos_sin.shape[0], int(interleaved), slots.data_ptr(), pool.data_ptr(), n, P, page_stride,
+        LATENT_DIM, LATENT_ROPE, _address(q_pe), qs[0], qs[1], _address(q_out), os[0], os[1], heads,
+        PKV_FLAG_CHECKED if checked else 0, _address(err), _launch_stream(stream, dev))
+    if status:
+        _check("kv_append_latent", status)
+
+
+def paged_attention_latent_workspace_size(batch, max_q_rows, num_heads, max_kv_len, flags=0) -> int:
+    return int(lib().paged_attention_latent_workspace_size(batch, max_q_rows, num_heads, max_kv_len, LATENT_DIM,
+                                                           LATENT_ROPE, flags))
+
+
+def _wide_states(q, out, lse, width, value):
+    """Token and head stride of packed query rows of ``width`` whose outputs have ``value`` elements."""
+    shape = q.shape
+    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != width or q.stride(2) != 1:
+        raise ValueError(f"q must be bf16 [rows, num_heads, {width}] with unit last stride")
+    if out.shape != (shape[0], shape[1], value) or not out.is_contiguous() or out.dtype not in _DTYPES:
+        raise ValueError(f"out must be dense bf16 or float32 [rows, num_heads, {value}]")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be dense float32 [rows, num_heads]")
+    return _row_strides(shape, q.stride(), width)
+
+
+def paged_attention_latent(q, pool, block_table, kv_lens, q_indptr, out, *, q_real=None, lse=None, batch=None,
+                           max_q_rows, max_kv_len, mask="causal", scale, workspace=None, flags=0, err=None,
+                           stream=None):
+    """Attention of absorbed queries ``q [rows, H, 512 + 64]`` over the latent
+    rows of ``pool``, into ``out [rows, H, 512]`` (bf16 or f32) and ``lse``."""
+    n, P, page_stride = _latent_pool(pool)
+    st = _wide_states(q, out, lse, LATENT_DIM + LATENT_ROPE, LATENT_DIM)
+    batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
+    _scratch(workspace, err)
+    mask = _mask(mask)
+    dev = _on_device((q, pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err))
+    status = lib().paged_attention_latent(
+        q.data_ptr(), st[0], st[1], pool.data_ptr(), n, P, page_stride, block_table.data_ptr(), table_stride,
+        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, q.shape[1],
+        LATENT_DIM, LATENT_ROPE, mask, scale, out.data_ptr(), _dtype(out), _address(lse), _address(workspace),
+        _bytes(workspace), flags, _address(err), _launch_stream(stream, dev))
+    if status:
+        _check("paged_attention_latent", status)
+
+
+def ragged_attention_latent(q, k, k_pe, v, q_indptr, kv_indptr, out, *, lse=None, batch=None, max_q_rows, max_kv_len,
+                            mask="causal", scale, flags=0, err=None, stream=None):
+    """Attention of ``q [rows, H, 128 + 64]`` over ragged expanded keys ``k
+    [keys, H, 128]`` with the shared ``k_pe [keys, 64]`` and values ``v [keys, H,
+    128]``, into ``out [rows, H, 128]`` (bf16 or f32) and ``lse``."""
+    st = _wide_states(q, out, lse, NOPE_DIM + LATENT_ROPE, EXPANDED_V)
+    heads, keys = q.shape[1], k.shape[0]
+    for t, shape in ((k, (keys, heads, NOPE_DIM)), (v, (keys, heads, EXPANDED_V)), (k_pe, (keys, LATENT_ROPE))):
+        if t.dtype is not _BF16 or t.shape != shape or t.stride(-1) != 1:
+            raise ValueError("k, v and k_pe must be bf16 [keys, num_heads, 128], the same and [keys, 64], unit last stride")
+    ks, vs = _row_strides(k.shape, k.stride(), NOPE_DIM), _row_strides(v.shape, v.stride(), EXPANDED_V)
+    if batch is None:
+        batch = q_indptr.numel() - 1
+    _vector(q_indptr, "q_indptr", _I32, batch + 1)
+    _vector(kv_indptr, "kv_indptr", _I32, batch + 1)
+    _scratch(None, err)
+    mask = _mask(mask)
+    dev = _on_device((q, k, k_pe, v, q_indptr, kv_indptr, out, lse, err))
+    status = lib().ragged_attention_latent(
+        q.data_ptr(), st[0], st[1], k.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), k_pe.stride(0) if keys > 1 else LATENT_ROPE,
+        v.data_ptr(), vs[0], vs[1], keys, q_indptr.data_ptr(), kv_indptr.data_ptr(), batch, max_q_rows, max_kv_len, heads,
+        NOPE_DIM, LATENT_ROPE, EXPANDED_V, mask, scale, out.data_ptr(), _dtype(out), _address(lse), flags, _address(err),
+        _launch_stream(stream, dev))
+    if status:
+        _check("ragged_attention_latent", status)
