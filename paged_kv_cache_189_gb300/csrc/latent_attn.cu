@@ -1,12 +1,798 @@
-// latent_attn.cu -- attention over paged latent rows and over expanded keys.
+// latent_attn.cu -- paged_attention_latent on the tensor cores (tcgen05 / TMEM,
+// TMA-fed): every head reads the same latent rows, so a sequence's (query row,
+// head) pairs are the columns of two matrix products with the keys as rows:
+//   S^T [64 keys x N] = C [64 x 576] Q^T,   O^T [512 x N] += C[:, :512]^T P^T
+// over 64-key tiles (two pages) with a running maximum and sum per column.
+//
+// Keys stand in the M dimension because a decode step has few columns (16 heads
+// shared out over GPUs, 128 on one) and TMEM has no room for 128 rows of O beside
+// S (128 x 512 f32 is all of it), while O^T takes 4 N columns.  A latent tile is
+// read from DRAM once and used twice from shared memory: K-major for S^T, and as
+// the same bytes MN-major for O^T.
+//
+// A CTA holds N = 16, 32 or 64 columns; more are held by a cluster of two CTAs,
+// each of which loads one page of every tile for both (multicast).  The keys of
+// all sequences are one line of tiles that the clusters share out evenly: a
+// cluster works through its share segment by segment (a segment is a range of
+// one column group's tiles) and leaves a partial state where a group's tiles
+// were cut; a second launch joins those.
+//
+// Roles (192 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
+// TMA producer, warp 5 the MMA issuer.  Every wait gives up after ~2 s.
+#include <cuda.h>
+
 #include "latent.h"
+#include "tc.cuh"
 
 namespace pkv {
+namespace {
 
-LatentPlan plan_latent(int, int, int, int, int) { return LatentPlan{}; }
+constexpr int kThreads = 192;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kProducerWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr int kKeys = 64;                  // keys of a tile
+constexpr int kHalf = kKeys * 128;         // 64 keys x 64 dims
+constexpr int kBlock = 2 * kHalf;          // 64 keys x 128 dims
+constexpr int kBlocks = kLatentDim / 128;  // value blocks of a tile (the rotary half block is apart)
+constexpr int kRopeBlock = kLatentDim / 64;
+constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
+constexpr int kMinShare = 2;               // tiles a cluster takes at least
 
-cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan&, void*, const void*, cudaStream_t s) {
-    return launch_latent_simt(p, s);
+// Shared memory.  N = 64 leaves room for two tiles exactly: they are taken in
+// groups of two (both S^T, then both O^T products), so that one tile's softmax
+// runs beside the other's products and the first blocks are free again early.
+template <int N>
+struct Dim {
+    static constexpr int kGroup = N == 64 ? 2 : 1;
+    static constexpr int kV = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of value blocks
+    static constexpr int kR = N == 64 ? 1 : 3;                  // ring of rotary blocks
+    static constexpr int kQBlock = N * 128;                     // N columns x 64 dims
+    static constexpr int kPBytes = kKeys * N * 2;
+    static constexpr int kVOff = 0;
+    static constexpr int kROff = kVOff + kV * kBlock;
+    static constexpr int kQOff = kROff + kR * kHalf;
+    static constexpr int kPOff = kQOff + 9 * kQBlock;
+    static constexpr int kBarOff = kPOff + kGroup * kPBytes;
+    static constexpr int kNumBars = 2 * kV + 2 * kR + 1 + 2 * kGroup + 3;
+    static constexpr int kRedOff = kBarOff + ((kNumBars * 8 + 127) / 128) * 128;  // [4][N] per-warp maxima or sums
+    static constexpr int kColOff = kRedOff + 4 * N * 4;   // [N] factors (rescale, then 1 / sum)
+    static constexpr int kLimOff = kColOff + N * 4;       // [N] keys each column sees
+    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 6 warp totals, 6 + the cluster's first unit
+    static constexpr int kBytes = kPlanOff + 96;
+    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+    static constexpr uint32_t kSCol = 4 * N;              // S^T behind O^T's four blocks
+    static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
+};
+
+// A unit: column group `g` of sequence `b`.
+struct Unit {
+    int b, r0, kv, qreal, cols, c0;  // cols: the sequence's columns; c0: the group's first
+    int vis, tiles;                  // keys its last real row sees
+};
+
+struct Sched {
+    int workers, groups, cols;  // clusters, column groups a sequence may have, columns of a group
+    int4* dir;                  // [workers] where each cluster starts: unit, tile in it, its tiles, share
+    float* lse;                 // [workers][2][cols] partial states: a first and a last segment
+    float* o;                   // [workers][2][cols][512]
+};
+
+__device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, int u) {
+    Unit w;
+    w.b = u / sc.groups;
+    w.r0 = p.q_indptr[w.b];
+    const int nrows = max(0, min(p.q_indptr[w.b + 1] - w.r0, p.max_q_rows));
+    w.qreal = max(0, min(p.q_real ? p.q_real[w.b] : nrows, nrows));
+    w.kv = min(max(p.kv_lens[w.b], 0), p.max_kv_len);
+    w.cols = nrows * p.heads;
+    w.c0 = (u - w.b * sc.groups) * sc.cols;
+    w.vis = 0;
+    if (w.c0 < w.cols && w.c0 / p.heads < w.qreal) {
+        const int last = min((min(w.c0 + sc.cols, w.cols) - 1) / p.heads, w.qreal - 1);
+        w.vis = p.causal ? max(0, w.kv - w.qreal + last + 1) : w.kv;
+    }
+    w.tiles = (w.vis + kKeys - 1) / kKeys;
+    return w;
+}
+
+// The segments of one cluster's share, in order; every role walks them alike.
+struct Segments {
+    int u, o;
+    int64_t left;
+    Unit w;
+    int j0, j1;
+    __device__ __forceinline__ bool next(const LatentParams& p, const Sched& sc) {
+        if (left <= 0) return false;
+        w = unit_of(p, sc, u);
+        while (o >= w.tiles) {
+            o = 0;
+            w = unit_of(p, sc, ++u);
+        }
+        j0 = o;
+        j1 = static_cast<int>(min(static_cast<int64_t>(w.tiles), o + left));
+        left -= j1 - j0;
+        o = j1;
+        return true;
+    }
+};
+
+template <int N, int CL>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p, const Sched sc) {
+    using D = Dim<N>;
+    constexpr int G = D::kGroup;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int worker = blockIdx.x / CL;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + D::kBarOff);
+    uint64_t* v_full = bars;
+    uint64_t* v_empty = v_full + D::kV;
+    uint64_t* r_full = v_empty + D::kV;
+    uint64_t* r_empty = r_full + D::kR;
+    uint64_t* q_ready = r_empty + D::kR;
+    uint64_t* s_full = q_ready + 1;   // [G]
+    uint64_t* p_full = s_full + G;    // [G]
+    uint64_t* pv_done = p_full + G;   // the group's first tile
+    uint64_t* o_full = pv_done + 1;
+    uint64_t* mma_done = o_full + 1;
+    float* red = reinterpret_cast<float*>(smem + D::kRedOff);
+    float* colf = reinterpret_cast<float*>(smem + D::kColOff);
+    int* lim = reinterpret_cast<int*>(smem + D::kLimOff);
+    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [6]
+    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 48);         // unit, tile, tmem, abort
+    volatile int* abort_flag = plan + 3;
+
+    // ---- the plan: the line of all units' tiles, and this cluster's share of it
+    const int units = p.batch * sc.groups;
+    const int per = (units + kThreads - 1) / kThreads;
+    const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
+    int64_t mine = 0;
+    for (int u = u0; u < u1; ++u) mine += unit_of(p, sc, u).tiles;
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) plan_tot[warp] = x;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < D::kV; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], CL);
+        }
+        for (int s = 0; s < D::kR; ++s) {
+            mbar_init(&r_full[s], 1);
+            mbar_init(&r_empty[s], CL);
+        }
+        mbar_init(q_ready, kSoftmaxThreads);
+        for (int t = 0; t < G; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], kSoftmaxThreads);
+        }
+        mbar_init(pv_done, 1);
+        mbar_init(o_full, 1);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tc_alloc(reinterpret_cast<uint32_t*>(plan + 2), D::kTmem);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    int64_t before = x - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? plan_tot[w] : 0;
+        total += plan_tot[w];
+    }
+    const int64_t share = max((total + sc.workers - 1) / sc.workers, static_cast<int64_t>(kMinShare));
+    const int64_t start = worker * share;
+    Segments seg0;
+    seg0.left = max(min(share, total - start), static_cast<int64_t>(0));
+    if (start >= before && start < before + mine) {  // one thread at most
+        int64_t at = before;
+        for (int u = u0; u < u1; ++u) {
+            const int t = unit_of(p, sc, u).tiles;
+            if (start < at + t) {
+                plan[0] = u;
+                plan[1] = static_cast<int>(start - at);
+                if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], t, static_cast<int>(share));
+                break;
+            }
+            at += t;
+        }
+    }
+    if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[worker] = make_int4(-1, 0, 0, 0);
+    if (CL > 1) cluster_sync_all();  // the other CTA's barriers are initialised
+    else __syncthreads();
+    seg0.u = plan[0];
+    seg0.o = plan[1];
+    const uint32_t tmem = static_cast<uint32_t>(plan[2]);
+    const uint32_t sbase = smem_u32(smem);
+    // the swizzles need 1024-byte aligned tiles
+    if ((sbase & 1023u) != 0) {
+        if (threadIdx.x == 0) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        seg0.left = 0;
+    }
+
+    // a completed phase passes at once; after one wait gave up, the others do not wait
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity)) return true;
+        *abort_flag = 1;
+        set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        return false;
+    };
+    // a tile's rotary block is used first in even tiles and last in odd ones:
+    // with one buffer its next copy has a tile's time to land
+    Segments it = seg0;
+
+    if (warp == kProducerWarp) {
+        // ============================ producer ==============================
+        if (lane == 0) {
+            prefetch_tmap(&tm);
+            constexpr uint16_t kAll = (1 << CL) - 1;
+            int64_t nv = 0, nr = 0;
+            int n = 0;
+            bool alive = true;
+            while (alive && it.next(p, sc)) {
+                const int32_t* bt = p.block_table + static_cast<int64_t>(it.w.b) * p.block_table_stride;
+                const int last_page = (it.w.vis + 31) / 32;
+                // the tile's pages (a cluster's CTAs look up one each); the sentinel reads as zeros
+                auto fetch = [&](int j, int (&ph)[2 / CL]) {
+#pragma unroll
+                    for (int k = 0; k < 2 / CL; ++k) {
+                        const int lp = 2 * j + (CL > 1 ? rank : k);
+                        ph[k] = static_cast<int>(p.num_pages);
+                        if (lp < last_page) {
+                            const int page = bt[lp];
+                            if (page >= 0 && page < p.num_pages) ph[k] = page;
+                            else if (p.checked) set_err(p.err, PKV_ERRBIT_PAGE);
+                        }
+                    }
+                };
+                int next[2 / CL];
+                fetch(it.j0, next);
+                for (int j = it.j0; alive && j < it.j1; ++j, ++n) {
+                    int ph[2 / CL];
+#pragma unroll
+                    for (int k = 0; k < 2 / CL; ++k) ph[k] = next[k];
+                    if (j + 1 < it.j1) fetch(j + 1, next);
+                    // 64 dims from d0 of the tile's pages to dst
+                    auto copy = [&](uint8_t* dst, uint64_t* bar, int d0) {
+#pragma unroll
+                        for (int k = 0; k < 2 / CL; ++k) {
+                            if constexpr (CL > 1) tma_load_3d_all(dst + rank * 4096, &tm, bar, d0, 0, ph[k], kAll);
+                            else tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
+                        }
+                    };
+                    auto rope = [&] {
+                        const int s = static_cast<int>(nr % D::kR);
+                        if (nr >= D::kR && !wait(&r_empty[s], static_cast<uint32_t>(nr / D::kR - 1) & 1)) return false;
+                        mbar_arrive_expect_tx(&r_full[s], kHalf);
+                        copy(smem + D::kROff + s * kHalf, &r_full[s], kLatentDim);
+                        ++nr;
+                        return true;
+                    };
+                    if ((n & 1) == 0) alive = rope();
+                    for (int b = 0; alive && b < kBlocks; ++b) {
+                        const int s = static_cast<int>(nv % D::kV);
+                        if (nv >= D::kV && !wait(&v_empty[s], static_cast<uint32_t>(nv / D::kV - 1) & 1)) {
+                            alive = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&v_full[s], kBlock);
+                        uint8_t* dst = smem + D::kVOff + s * kBlock;
+                        copy(dst, &v_full[s], b * 128);
+                        copy(dst + kHalf, &v_full[s], b * 128 + 64);
+                        ++nv;
+                    }
+                    if (alive && (n & 1) == 1) alive = rope();
+                }
+            }
+            // do not leave with copies into this CTA's shared memory in flight
+            for (int64_t k = max(int64_t(0), nv - D::kV); k < nv; ++k) mbar_wait(&v_full[k % D::kV], (k / D::kV) & 1);
+            for (int64_t k = max(int64_t(0), nr - D::kR); k < nr; ++k) mbar_wait(&r_full[k % D::kR], (k / D::kR) & 1);
+        }
+    } else if (warp == kMmaWarp) {
+        // =============================== MMA ================================
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = tc_idesc(kKeys, N, false, false);
+            constexpr uint32_t kIdescO = tc_idesc(128, N, true, true);
+            constexpr uint16_t kAll = (1 << CL) - 1;
+            auto release = [&](uint64_t* bar) {
+                if constexpr (CL > 1) tc_commit_all(bar, kAll);
+                else tc_commit(bar);
+            };
+            const uint64_t dq = tc_desc(sbase + D::kQOff, 16, 1024, 128);
+            int64_t nv = 0, nr = 0;  // ring positions of the group's first tile
+            int n = 0, nseg = 0;
+            uint32_t np[G] = {};
+            bool ok = true;
+            while (ok && it.next(p, sc)) {
+                ok = wait(q_ready, nseg++ & 1);
+                for (int j = it.j0; ok && j < it.j1; j += G) {
+                    const int g = min(G, it.j1 - j);
+                    for (int t = 0; ok && t < g; ++t, ++n) {
+                        const uint32_t d = tmem + D::kSCol + t * N;
+                        bool acc = false;
+                        // S^T += 64 dims of the tile at `a` times block qb of the queries
+                        auto half = [&](uint32_t a, int qb) {
+                            const uint64_t da = tc_desc(a, 16, 1024, 128);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                tc_mma(d, da + 2 * kk, dq + ((qb * D::kQBlock + kk * 32) >> 4), kIdescS, acc);
+                                acc = true;
+                            }
+                        };
+                        auto rope = [&] {
+                            const int s = static_cast<int>(nr % D::kR);
+                            ok = ok && wait(&r_full[s], static_cast<uint32_t>(nr / D::kR) & 1);
+                            tc_after_sync();
+                            half(sbase + D::kROff + s * kHalf, kRopeBlock);
+                            release(&r_empty[s]);
+                            ++nr;
+                        };
+                        if ((n & 1) == 0) rope();
+                        for (int b = 0; ok && b < kBlocks; ++b) {
+                            const int64_t q = nv + t * kBlocks + b;
+                            const int s = static_cast<int>(q % D::kV);
+                            ok = wait(&v_full[s], static_cast<uint32_t>(q / D::kV) & 1);
+                            tc_after_sync();
+                            half(sbase + D::kVOff + s * kBlock, 2 * b);
+                            half(sbase + D::kVOff + s * kBlock + kHalf, 2 * b + 1);
+                        }
+                        if (ok && (n & 1) == 1) rope();
+                        tc_commit(&s_full[t]);
+                    }
+                    for (int t = 0; ok && t < g; ++t) {
+                        ok = wait(&p_full[t], np[t]++ & 1);
+                        if (!ok) break;
+                        tc_after_sync();
+                        // P^T: rows of keys, N columns wide, one swizzle row each
+                        const uint64_t dp = tc_desc(sbase + D::kPOff + t * D::kPBytes, 16, 16 * N, 2 * N);
+                        for (int b = 0; b < kBlocks; ++b) {
+                            const int s = static_cast<int>((nv + t * kBlocks + b) % D::kV);
+                            const uint64_t da = tc_desc(sbase + D::kVOff + s * kBlock, kHalf, 1024, 128);
+#pragma unroll
+                            for (int kk = 0; kk < kKeys / 16; ++kk)
+                                tc_mma(tmem + b * N, da + kk * (2048 >> 4), dp + kk * (32 * N >> 4), kIdescO,
+                                       j + t > it.j0 || kk > 0);
+                            release(&v_empty[s]);
+                        }
+                        if (G > 1 && t == 0) tc_commit(pv_done);
+                    }
+                    nv += g * kBlocks;
+                }
+                if (ok) tc_commit(o_full);
+            }
+            // nothing of this thread's still runs in the tensor pipe when the CTA
+            // winds down (after a failed wait the last products may)
+            tc_commit(mma_done);
+            if (!mbar_wait(mma_done, 0)) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        }
+    } else {
+        // ===================== softmax and outputs ==========================
+        // A warp holds 16 keys of the tile (its quadrant's first 16 lanes), a
+        // thread 2 keys and N / 4 columns: maxima and sums stay per thread, and a
+        // column's reference moves (by all threads together) only when a score
+        // passes it by 2^8, so most tiles exchange nothing but that one vote.
+        constexpr int NC = N / 4;
+        const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;
+        const int key_of = 16 * warp + (lane >> 2);  // and 8 further
+        int n = 0, nseg = 0;
+        uint32_t ns[G] = {}, ng = 0;
+        int slot = 0;  // of a partial state: 0 for the share's first segment
+
+        // outputs of units that see no key: zeros
+        auto store_zeros = [&](const Unit& w) {
+            for (int c = 0; c < N; ++c) {
+                const int col = w.c0 + rank * N + c;
+                if (col >= w.cols) break;
+                const int64_t at = static_cast<int64_t>(w.r0) * p.heads + col;
+                const int d = threadIdx.x * 4;
+                if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kLatentDim + d) = make_float4(0, 0, 0, 0);
+                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kLatentDim + d) = make_uint2(0, 0);
+                if (p.lse && threadIdx.x == 0) p.lse[at] = -INFINITY;
+            }
+        };
+        for (int u = worker; u < units; u += sc.workers) {
+            const Unit w = unit_of(p, sc, u);
+            if (p.checked && rank == 0 && threadIdx.x == 0 && w.c0 == 0) {
+                const int rows = p.q_indptr[w.b + 1] - w.r0, kv = p.kv_lens[w.b];
+                if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[w.b] > rows))
+                    set_err(p.err, PKV_ERRBIT_LEN);
+            }
+            if (w.c0 < w.cols && w.tiles == 0) store_zeros(w);
+        }
+
+        while (it.next(p, sc)) {
+            const Unit& w = it.w;
+            const int col0 = w.c0 + rank * N;  // this CTA's first column
+            // ---- limits and queries of the columns.  Those past the last (their
+            // results go nowhere) see what the unit sees, so they mask nothing.
+            if (threadIdx.x < N) {
+                const int i = (col0 + threadIdx.x) / p.heads;
+                int l = w.vis;
+                if (col0 + threadIdx.x < w.cols)
+                    l = i >= w.qreal ? 0 : p.causal ? max(0, w.kv - w.qreal + i + 1) : w.kv;
+                lim[threadIdx.x] = l;
+            }
+            // (the previous segment's S^T products are done with these queries: their S^T was read)
+            const __nv_bfloat16* qbase = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(w.r0) * p.q_token_stride;
+            constexpr int kChunks = kLatentRow / 8;
+#pragma unroll 9
+            for (int idx = threadIdx.x; idx < N * kChunks; idx += kSoftmaxThreads) {
+                const int c = idx / kChunks, ch = idx - c * kChunks, col = col0 + c;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (col < w.cols) {
+                    const int i = col / p.heads;
+                    v = *reinterpret_cast<const uint4*>(qbase + i * p.q_token_stride +
+                                                        static_cast<int64_t>(col - i * p.heads) * p.q_head_stride + ch * 8);
+                }
+                *reinterpret_cast<uint4*>(smem + D::kQOff + (ch >> 3) * D::kQBlock + sw128_offset(c, ch & 7)) = v;
+            }
+            fence_proxy_async_smem();
+            tc_before_sync();
+            mbar_arrive(q_ready);
+            bar_sync(1, kSoftmaxThreads);
+            int lim_min = lim[lane % N];
+            if (N > 32) lim_min = min(lim_min, lim[(lane + 32) % N]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+
+            float m[NC], l[NC], lb[NC];  // column 8 f + 2 (lane % 4) + e is [2 f + e]
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                m[c] = -INFINITY;
+                l[c] = lb[c] = 0.f;
+            }
+            for (int j = it.j0; j < it.j1; ++j, ++n) {
+                const int t = (j - it.j0) % G;
+                const int key0 = j * kKeys;
+                wait(&s_full[t], ns[t]++ & 1);
+                __syncwarp();
+                tc_after_sync();
+                uint32_t v[N / 2];
+                tc_load_frag<N>(tmem + quad + D::kSCol + t * N, v);
+                float s[N / 2];
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) s[e] = __uint_as_float(v[e]) * p.scale_log2;
+                if (key0 + kKeys > lim_min) {
+#pragma unroll
+                    for (int f = 0; f < N / 8; ++f) {
+                        const int2 lm = *reinterpret_cast<const int2*>(lim + 8 * f + 2 * (lane & 3));
+                        const int k = key0 + key_of;
+                        s[4 * f] = k < lm.x ? s[4 * f] : -INFINITY;
+                        s[4 * f + 1] = k < lm.y ? s[4 * f + 1] : -INFINITY;
+                        s[4 * f + 2] = k + 8 < lm.x ? s[4 * f + 2] : -INFINITY;
+                        s[4 * f + 3] = k + 8 < lm.y ? s[4 * f + 3] : -INFINITY;
+                    }
+                }
+                bool past = false;
+#pragma unroll
+                for (int f = 0; f < N / 8; ++f)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) past |= fmaxf(s[4 * f + e], s[4 * f + 2 + e]) > m[2 * f + e] + kLazyRescale;
+                if (bar_any(1, kSoftmaxThreads, past)) {
+                    // new references: the tile's maxima where they pass the old ones by 2^8
+                    float mx[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        mx[c] = fmaxf(s[4 * (c >> 1) + (c & 1)], s[4 * (c >> 1) + 2 + (c & 1)]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+                    }
+                    if (lane < 4) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) red[warp * N + 8 * (c >> 1) + 2 * lane + (c & 1)] = mx[c];
+                    }
+                    bar_sync(1, kSoftmaxThreads);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int at = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
+                        const float tm4 = fmaxf(fmaxf(red[at], red[N + at]), fmaxf(red[2 * N + at], red[3 * N + at]));
+                        float alpha = 1.f;
+                        if (tm4 > m[c] + kLazyRescale) {
+                            alpha = fast_exp2(m[c] - tm4);  // 0 when no key was visible before
+                            m[c] = tm4;
+                        }
+                        l[c] *= alpha;
+                        lb[c] *= alpha;
+                        if (warp == 0 && lane < 4) colf[at] = alpha;
+                    }
+                    // O^T's columns follow once the products issued so far are done: those
+                    // of earlier groups are (this S^T came after them in the pipe)
+                    if (G > 1 && t == 1) wait(pv_done, ng & 1);
+                    __syncwarp();
+                    bar_sync(1, kSoftmaxThreads);
+                    if (j > it.j0) {
+                        tc_after_sync();
+                        for (int c16 = 0; c16 < 4 * N / 16; ++c16) {
+                            uint32_t o[16];
+                            tc_load16(tmem + quad + c16 * 16, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * colf[(c16 * 16 + e) % N]);
+                            tc_store16(tmem + quad + c16 * 16, o);
+                        }
+                        tc_wait_store();
+                    }
+                }
+                // weights, rounded to bf16 for the product; their sums rounded (the
+                // output's divisor) and not (the LSE)
+                uint8_t* pt = smem + D::kPOff + t * D::kPBytes;
+#pragma unroll
+                for (int f = 0; f < N / 8; ++f) {
+                    const float m0 = m[2 * f] == -INFINITY ? 0.f : m[2 * f], m1 = m[2 * f + 1] == -INFINITY ? 0.f : m[2 * f + 1];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float w0 = fast_exp2(s[4 * f + 2 * r] - m0), w1 = fast_exp2(s[4 * f + 2 * r + 1] - m1);
+                        const uint32_t pk = pack_bf16x2(w0, w1);
+                        l[2 * f] += w0;
+                        l[2 * f + 1] += w1;
+                        lb[2 * f] += bf16lo(pk);
+                        lb[2 * f + 1] += bf16hi(pk);
+                        const int k = key_of + 8 * r;
+                        uint32_t at = k * 2 * N + f * 16;
+                        at ^= ((at >> 7) & (N / 8 - 1)) << 4;
+                        *reinterpret_cast<uint32_t*>(pt + at + (lane & 3) * 4) = pk;
+                    }
+                }
+                // rows of keys that no column sees hold whatever the pool holds: zero
+                // them (S^T has been computed), so that 0 * NaN does not reach O^T
+                if (key0 + kKeys > w.vis) {
+                    const int first = w.vis - key0;
+                    for (int idx = threadIdx.x; idx < (kKeys - first) * 64; idx += kSoftmaxThreads) {
+                        const int row = first + (idx >> 6), ch = idx & 63;
+                        const int sl = static_cast<int>((static_cast<int64_t>(n) * kBlocks + (ch >> 4)) % D::kV);
+                        *reinterpret_cast<uint4*>(smem + D::kVOff + sl * kBlock + ((ch >> 3) & 1) * kHalf +
+                                                  sw128_offset(row, ch & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_before_sync();
+                mbar_arrive(&p_full[t]);
+                if (t == G - 1 || j + 1 == it.j1) ++ng;
+            }
+            // ---- the segment's columns: sums over the tile's rows, then O^T / sum
+            const bool whole = it.j0 == 0 && it.j1 == w.tiles;
+            float lsum = 0.f, lbsum = 0.f;  // of column threadIdx.x
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                bar_sync(1, kSoftmaxThreads);  // red has been read
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    float sum = pass == 0 ? l[c] : lb[c];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane < 4) red[warp * N + 8 * (c >> 1) + 2 * lane + (c & 1)] = sum;
+                }
+                bar_sync(1, kSoftmaxThreads);
+                if (threadIdx.x < N) {
+                    const float sum = (red[threadIdx.x] + red[N + threadIdx.x]) + (red[2 * N + threadIdx.x] + red[3 * N + threadIdx.x]);
+                    if (pass == 0) lsum = sum;
+                    else lbsum = sum;
+                }
+            }
+            if (warp == 0 && lane < 4) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) colf[8 * (c >> 1) + 2 * lane + (c & 1)] = m[c];
+            }
+            bar_sync(1, kSoftmaxThreads);
+            if (threadIdx.x < N) {
+                const bool any = lsum != 0.f;  // (NaN stays)
+                const float lse = any ? (colf[threadIdx.x] + __log2f(lsum)) * kLn2 : -INFINITY;
+                const int col = col0 + threadIdx.x;
+                if (whole) {
+                    if (p.lse && col < w.cols) p.lse[static_cast<int64_t>(w.r0) * p.heads + col] = lse;
+                } else {
+                    sc.lse[(static_cast<int64_t>(worker) * 2 + slot) * sc.cols + rank * N + threadIdx.x] = lse;
+                }
+                colf[threadIdx.x] = any ? 1.0f / lbsum : 0.f;
+            }
+            wait(o_full, nseg++ & 1);
+            __syncwarp();
+            bar_sync(1, kSoftmaxThreads);
+            tc_after_sync();
+            const int64_t out_row = static_cast<int64_t>(w.r0) * p.heads + col0;
+            float* part = sc.o + ((static_cast<int64_t>(worker) * 2 + slot) * sc.cols + rank * N) * kLatentDim;
+            const int valid = min(N, w.cols - col0);  // columns that exist (uniform)
+            for (int b = 0; b < kBlocks; ++b) {
+                const int dim = b * 128 + warp * 32 + lane;
+                for (int c0 = 0; c0 < N; c0 += 16) {
+                    uint32_t o[16];
+                    tc_load16(tmem + quad + b * N + c0, o);
+                    float f[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]) * colf[c0 + e];
+                    if (!whole || p.out_f32) {
+                        float* dst = whole ? static_cast<float*>(p.out) + out_row * kLatentDim : part;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c0 + e < valid) dst[static_cast<int64_t>(c0 + e) * kLatentDim + dim] = f[e];
+                    } else {
+                        // lanes exchange one of two columns, so that each stores a pair of dims
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * kLatentDim;
+                        const bool odd = lane & 1;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : f[e + 1], 1);
+                            const uint32_t pk = odd ? pack_bf16x2(got, f[e + 1]) : pack_bf16x2(f[e], got);
+                            const int c = c0 + e + (odd ? 1 : 0);
+                            if (c < valid)
+                                *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(c) * kLatentDim + (dim & ~1)) = pk;
+                        }
+                    }
+                }
+            }
+            slot = 1;  // a later partial segment of this share is its last
+            tc_before_sync();
+        }
+    }
+
+    __syncwarp();
+    tc_before_sync();
+    if (CL > 1) cluster_sync_all();  // the other CTA's copies and commits land here no more
+    else __syncthreads();
+    tc_after_sync();
+    if (warp == kMmaWarp) tc_dealloc(tmem, D::kTmem);
+}
+
+// One CTA a (cut, column): where cluster c starts inside a unit, and the unit
+// began in the cluster before it, the unit's states, one a cluster in line, are
+// joined: out = sum w_i O_i / sum w_i with w_i = e^(lse_i - max).
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentParams p, const Sched sc) {
+    const int c = blockIdx.x + 1, col = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = sc.dir[c];
+    if (d.x < 0 || d.y == 0 || d.y > d.w) return;
+    const Unit w = unit_of(p, sc, d.x);
+    if (w.c0 + col >= w.cols) return;
+    const int64_t share = d.w, at = c * share;  // the unit's tiles lie at [at - d.y, at - d.y + d.z)
+    const int last = static_cast<int>((at - d.y + d.z - 1) / share);
+    const int first_slot = d.y < share ? 1 : 0;
+    const int n = last - c + 2;
+    auto piece = [&](int k) {
+        return (static_cast<int64_t>(c - 1 + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
+    };
+    __shared__ float sh[kJoinThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float m = -INFINITY;
+    for (int k = threadIdx.x; k < n; k += kJoinThreads) m = fmaxf(m, sc.lse[piece(k)]);
+    m = warp_max(m);
+    if (lane == 0) sh[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+    const float mm = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0, 0, 0, 0);
+    float sum = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const int64_t at_k = piece(k);
+        const float wk = fast_exp2((sc.lse[at_k] - mm) * kLog2e);
+        const float4 o = *reinterpret_cast<const float4*>(sc.o + at_k * kLatentDim + threadIdx.x * 4);
+        sum += wk;
+        acc.x = fmaf(wk, o.x, acc.x);
+        acc.y = fmaf(wk, o.y, acc.y);
+        acc.z = fmaf(wk, o.z, acc.z);
+        acc.w = fmaf(wk, o.w, acc.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const int64_t row = static_cast<int64_t>(w.r0) * p.heads + w.c0 + col;
+    if (p.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatentDim + threadIdx.x * 4) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kLatentDim + threadIdx.x * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    if (p.lse && threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : mm + __log2f(sum) * kLn2;
+}
+
+template <int N, int CL>
+cudaLaunchConfig_t config(int workers, cudaLaunchAttribute* attr, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(workers * CL));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Dim<N>::kBytes;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int N, int CL>
+cudaError_t opt_in() {
+    static DeviceOnce opted;
+    int dev = 0, done = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return opted.get(dev, &done, [&](int, int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(latent_attn_kernel<N, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dim<N>::kBytes);
+    });
+}
+
+template <int N, int CL>
+cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, cudaStream_t s) {
+    cudaError_t e = opt_in<N, CL>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config<N, CL>(sc.workers, attr, s);
+    e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap), p, sc);
+    if (e != cudaSuccess || sc.workers == 1) return e;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t jc = {};
+    jc.gridDim = dim3(static_cast<unsigned>(sc.workers - 1), static_cast<unsigned>(sc.cols));
+    jc.blockDim = dim3(kJoinThreads);
+    jc.stream = s;
+    jc.attrs = pdl;
+    jc.numAttrs = 1;
+    return cudaLaunchKernelEx(&jc, latent_join_kernel, p, sc);
+}
+
+// Clusters of two that the current device runs at once (half the SMs where none can be queried).
+int resident_pairs(int sms) {
+    static DeviceOnce pairs;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && opt_in<64, 2>() == cudaSuccess &&
+        pairs.get(dev, &n, [&](int, int* v) {
+            cudaLaunchAttribute attr[1];
+            cudaLaunchConfig_t cfg = config<64, 2>(1, attr, nullptr);
+            return cudaOccupancyMaxActiveClusters(v, latent_attn_kernel<64, 2>, &cfg);
+        }) == cudaSuccess &&
+        n > 0)
+        return n;
+    cudaGetLastError();
+    return sms / 2 > 0 ? sms / 2 : 1;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms) {
+    LatentPlan pl{};
+    const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
+    pl.cols = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
+    pl.cluster = cols <= 64 ? 1 : 2;
+    pl.groups = static_cast<int>((cols + pl.cols * pl.cluster - 1) / (pl.cols * pl.cluster));
+    // no more clusters than shares of the smallest size
+    const int64_t tiles = static_cast<int64_t>(batch) * pl.groups * ((static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys);
+    const int64_t most = pl.cluster == 1 ? sms : resident_pairs(sms);
+    pl.workers = static_cast<int>(max(int64_t(1), min(most, (tiles + kMinShare - 1) / kMinShare)));
+    const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.cluster;
+    pl.ws_bytes = round256(pl.workers * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
+    return pl;
+}
+
+cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void* workspace, const void* tmap,
+                               cudaStream_t s) {
+    Sched sc;
+    sc.workers = pl.workers;
+    sc.groups = pl.groups;
+    sc.cols = pl.cols * pl.cluster;
+    char* w = static_cast<char*>(workspace);
+    sc.dir = reinterpret_cast<int4*>(w);
+    w += round256(pl.workers * sizeof(int4));
+    sc.lse = reinterpret_cast<float*>(w);
+    w += round256(static_cast<size_t>(pl.workers) * 2 * sc.cols * 4);
+    sc.o = reinterpret_cast<float*>(w);
+    if (pl.cluster == 2) return launch<64, 2>(p, sc, tmap, s);
+    if (pl.cols == 64) return launch<64, 1>(p, sc, tmap, s);
+    if (pl.cols == 32) return launch<32, 1>(p, sc, tmap, s);
+    return launch<16, 1>(p, sc, tmap, s);
 }
 
 cudaError_t launch_ragged_attn(const RaggedParams& p, const void*, const void*, const void*, cudaStream_t s) {
