@@ -117,6 +117,19 @@ struct Segments {
     }
 };
 
+// A place in a ring of R buffers and the parity of the phase it is in.
+template <int R>
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == R) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+};
+
 template <int N, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p, const Sched sc) {
@@ -233,10 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kProducerWarp) {
         // ============================ producer ==============================
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tmap(&tm);
             constexpr uint16_t kAll = (1 << CL) - 1;
-            int64_t nv = 0, nr = 0;
+            Ring<D::kV> v;
+            Ring<D::kR> r;
             int n = 0;
             bool alive = true;
             while (alive && it.next(p, sc)) {
@@ -270,37 +284,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
                         }
                     };
+                    // (a fresh barrier's previous phase counts as complete: the first round passes)
                     auto rope = [&] {
-                        const int s = static_cast<int>(nr % D::kR);
-                        if (nr >= D::kR && !wait(&r_empty[s], static_cast<uint32_t>(nr / D::kR - 1) & 1)) return false;
-                        mbar_arrive_expect_tx(&r_full[s], kHalf);
-                        copy(smem + D::kROff + s * kHalf, &r_full[s], kLatentDim);
-                        ++nr;
+                        if (!wait(&r_empty[r.s], r.ph ^ 1)) return false;
+                        mbar_arrive_expect_tx(&r_full[r.s], kHalf);
+                        copy(smem + D::kROff + r.s * kHalf, &r_full[r.s], kLatentDim);
+                        r.next();
                         return true;
                     };
                     if ((n & 1) == 0) alive = rope();
                     for (int b = 0; alive && b < kBlocks; ++b) {
-                        const int s = static_cast<int>(nv % D::kV);
-                        if (nv >= D::kV && !wait(&v_empty[s], static_cast<uint32_t>(nv / D::kV - 1) & 1)) {
+                        if (!wait(&v_empty[v.s], v.ph ^ 1)) {
                             alive = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&v_full[s], kBlock);
-                        uint8_t* dst = smem + D::kVOff + s * kBlock;
-                        copy(dst, &v_full[s], b * 128);
-                        copy(dst + kHalf, &v_full[s], b * 128 + 64);
-                        ++nv;
+                        mbar_arrive_expect_tx(&v_full[v.s], kBlock);
+                        uint8_t* dst = smem + D::kVOff + v.s * kBlock;
+                        copy(dst, &v_full[v.s], b * 128);
+                        copy(dst + kHalf, &v_full[v.s], b * 128 + 64);
+                        v.next();
                     }
                     if (alive && (n & 1) == 1) alive = rope();
                 }
             }
             // do not leave with copies into this CTA's shared memory in flight
-            for (int64_t k = max(int64_t(0), nv - D::kV); k < nv; ++k) mbar_wait(&v_full[k % D::kV], (k / D::kV) & 1);
-            for (int64_t k = max(int64_t(0), nr - D::kR); k < nr; ++k) mbar_wait(&r_full[k % D::kR], (k / D::kR) & 1);
+            // (buffers behind `s` were last filled in this round, the others in the one before)
+            for (int k = 0; k < D::kV; ++k) mbar_wait(&v_full[k], k < v.s ? v.ph : v.ph ^ 1);
+            for (int k = 0; k < D::kR; ++k) mbar_wait(&r_full[k], k < r.s ? r.ph : r.ph ^ 1);
         }
     } else if (warp == kMmaWarp) {
         // =============================== MMA ================================
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdescS = tc_idesc(kKeys, N, false, false);
             constexpr uint32_t kIdescO = tc_idesc(128, N, true, true);
             constexpr uint16_t kAll = (1 << CL) - 1;
@@ -309,64 +323,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else tc_commit(bar);
             };
             const uint64_t dq = tc_desc(sbase + D::kQOff, 16, 1024, 128);
-            int64_t nv = 0, nr = 0;  // ring positions of the group's first tile
+            // tiles as S^T's A operand (keys x dims, K-major) and as O^T's (dims x keys, MN-major)
+            const uint64_t ds = tc_desc(sbase + D::kVOff, 16, 1024, 128), dr = tc_desc(sbase + D::kROff, 16, 1024, 128);
+            const uint64_t dv = tc_desc(sbase + D::kVOff, kHalf, 1024, 128);
+            // P^T: rows of keys, N columns wide, one swizzle row each
+            const uint64_t dp = tc_desc(sbase + D::kPOff, 16, 16 * N, 2 * N);
+            Ring<D::kV> v;
+            Ring<D::kR> r;
             int n = 0, nseg = 0;
-            uint32_t np[G] = {};
+            uint32_t np = 0;  // bit t: parity of tile t's next weights
             bool ok = true;
+            // S^T (+)= 64 dims of the tile times block qb of the queries
+            auto half = [&](uint32_t d, uint64_t da, int qb, bool acc) {
+                const uint64_t db = dq + qb * (D::kQBlock >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) tc_mma(d, da + 2 * kk, db + 2 * kk, kIdescS, acc || kk > 0);
+            };
+            // (loops stay rolled: their code shares the instruction caches with the softmax)
             while (ok && it.next(p, sc)) {
                 ok = wait(q_ready, nseg++ & 1);
                 for (int j = it.j0; ok && j < it.j1; j += G) {
                     const int g = min(G, it.j1 - j);
-                    for (int t = 0; ok && t < g; ++t, ++n) {
+                    int s = v.s;  // the group's first value block
+#pragma unroll 1
+                    for (int t = 0; t < g; ++t, ++n) {
                         const uint32_t d = tmem + D::kSCol + t * N;
-                        bool acc = false;
-                        // S^T += 64 dims of the tile at `a` times block qb of the queries
-                        auto half = [&](uint32_t a, int qb) {
-                            const uint64_t da = tc_desc(a, 16, 1024, 128);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                tc_mma(d, da + 2 * kk, dq + ((qb * D::kQBlock + kk * 32) >> 4), kIdescS, acc);
-                                acc = true;
+#pragma unroll 1
+                        for (int k = 0; k <= kBlocks; ++k) {
+                            if (k == (n & 1) * kBlocks) {
+                                ok = ok && wait(&r_full[r.s], r.ph);
+                                tc_after_sync();
+                                half(d, dr + r.s * (kHalf >> 4), kRopeBlock, k > 0);
+                                release(&r_empty[r.s]);
+                                r.next();
+                            } else {
+                                const int b = k - 1 + (n & 1);
+                                ok = ok && wait(&v_full[v.s], v.ph);
+                                tc_after_sync();
+                                const uint64_t da = ds + v.s * (kBlock >> 4);
+                                half(d, da, 2 * b, k > 0);
+                                half(d, da + (kHalf >> 4), 2 * b + 1, true);
+                                v.next();
                             }
-                        };
-                        auto rope = [&] {
-                            const int s = static_cast<int>(nr % D::kR);
-                            ok = ok && wait(&r_full[s], static_cast<uint32_t>(nr / D::kR) & 1);
-                            tc_after_sync();
-                            half(sbase + D::kROff + s * kHalf, kRopeBlock);
-                            release(&r_empty[s]);
-                            ++nr;
-                        };
-                        if ((n & 1) == 0) rope();
-                        for (int b = 0; ok && b < kBlocks; ++b) {
-                            const int64_t q = nv + t * kBlocks + b;
-                            const int s = static_cast<int>(q % D::kV);
-                            ok = wait(&v_full[s], static_cast<uint32_t>(q / D::kV) & 1);
-                            tc_after_sync();
-                            half(sbase + D::kVOff + s * kBlock, 2 * b);
-                            half(sbase + D::kVOff + s * kBlock + kHalf, 2 * b + 1);
                         }
-                        if (ok && (n & 1) == 1) rope();
                         tc_commit(&s_full[t]);
                     }
-                    for (int t = 0; ok && t < g; ++t) {
-                        ok = wait(&p_full[t], np[t]++ & 1);
-                        if (!ok) break;
+#pragma unroll 1
+                    for (int t = 0; t < g && ok; ++t) {
+                        ok = wait(&p_full[t], (np >> t) & 1);
+                        np ^= 1u << t;
                         tc_after_sync();
-                        // P^T: rows of keys, N columns wide, one swizzle row each
-                        const uint64_t dp = tc_desc(sbase + D::kPOff + t * D::kPBytes, 16, 16 * N, 2 * N);
+                        const uint64_t db = dp + t * (D::kPBytes >> 4);
+#pragma unroll 1
                         for (int b = 0; b < kBlocks; ++b) {
-                            const int s = static_cast<int>((nv + t * kBlocks + b) % D::kV);
-                            const uint64_t da = tc_desc(sbase + D::kVOff + s * kBlock, kHalf, 1024, 128);
+                            const uint64_t da = dv + s * (kBlock >> 4);
 #pragma unroll
                             for (int kk = 0; kk < kKeys / 16; ++kk)
-                                tc_mma(tmem + b * N, da + kk * (2048 >> 4), dp + kk * (32 * N >> 4), kIdescO,
+                                tc_mma(tmem + b * N, da + kk * (2048 >> 4), db + kk * (32 * N >> 4), kIdescO,
                                        j + t > it.j0 || kk > 0);
                             release(&v_empty[s]);
+                            if (++s == D::kV) s = 0;
                         }
                         if (G > 1 && t == 0) tc_commit(pv_done);
                     }
-                    nv += g * kBlocks;
                 }
                 if (ok) tc_commit(o_full);
             }
@@ -384,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int NC = N / 4;
         const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;
         const int key_of = 16 * warp + (lane >> 2);  // and 8 further
-        int n = 0, nseg = 0;
+        int nseg = 0;
+        int vfirst = 0;  // the tile's first value block in the ring
         uint32_t ns[G] = {}, ng = 0;
         int slot = 0;  // of a partial state: 0 for the share's first segment
 
@@ -424,17 +444,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (the previous segment's S^T products are done with these queries: their S^T was read)
             const __nv_bfloat16* qbase = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(w.r0) * p.q_token_stride;
-            constexpr int kChunks = kLatentRow / 8;
-#pragma unroll 9
-            for (int idx = threadIdx.x; idx < N * kChunks; idx += kSoftmaxThreads) {
-                const int c = idx / kChunks, ch = idx - c * kChunks, col = col0 + c;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (col < w.cols) {
-                    const int i = col / p.heads;
-                    v = *reinterpret_cast<const uint4*>(qbase + i * p.q_token_stride +
-                                                        static_cast<int64_t>(col - i * p.heads) * p.q_head_stride + ch * 8);
+            constexpr int kChunks = kLatentRow / 8, kBatch = 9;  // loads in flight a thread
+            for (int i0 = threadIdx.x; i0 < N * kChunks; i0 += kBatch * kSoftmaxThreads) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int idx = i0 + k * kSoftmaxThreads, c = idx / kChunks, ch = idx - c * kChunks, col = col0 + c;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (col < w.cols) {
+                        const int i = col / p.heads;
+                        v[k] = *reinterpret_cast<const uint4*>(qbase + i * p.q_token_stride +
+                                                               static_cast<int64_t>(col - i * p.heads) * p.q_head_stride + ch * 8);
+                    }
                 }
-                *reinterpret_cast<uint4*>(smem + D::kQOff + (ch >> 3) * D::kQBlock + sw128_offset(c, ch & 7)) = v;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int idx = i0 + k * kSoftmaxThreads, c = idx / kChunks, ch = idx - c * kChunks;
+                    *reinterpret_cast<uint4*>(smem + D::kQOff + (ch >> 3) * D::kQBlock + sw128_offset(c, ch & 7)) = v[k];
+                }
             }
             fence_proxy_async_smem();
             tc_before_sync();
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[c] = -INFINITY;
                 l[c] = lb[c] = 0.f;
             }
-            for (int j = it.j0; j < it.j1; ++j, ++n) {
+            for (int j = it.j0; j < it.j1; ++j) {
                 const int t = (j - it.j0) % G;
                 const int key0 = j * kKeys;
                 wait(&s_full[t], ns[t]++ & 1);
@@ -549,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int first = w.vis - key0;
                     for (int idx = threadIdx.x; idx < (kKeys - first) * 64; idx += kSoftmaxThreads) {
                         const int row = first + (idx >> 6), ch = idx & 63;
-                        const int sl = static_cast<int>((static_cast<int64_t>(n) * kBlocks + (ch >> 4)) % D::kV);
+                        const int sl = (vfirst + (ch >> 4)) % D::kV;
                         *reinterpret_cast<uint4*>(smem + D::kVOff + sl * kBlock + ((ch >> 3) & 1) * kHalf +
                                                   sw128_offset(row, ch & 7)) = make_uint4(0, 0, 0, 0);
                     }
@@ -557,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_before_sync();
                 mbar_arrive(&p_full[t]);
+                vfirst = (vfirst + kBlocks) % D::kV;
                 if (t == G - 1 || j + 1 == it.j1) ++ng;
             }
             // ---- the segment's columns: sums over the tile's rows, then O^T / sum
