@@ -17,8 +17,10 @@
 // one column group's tiles) and leaves a partial state where a group's tiles
 // were cut; a second launch joins those.
 //
-// Roles (192 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
-// TMA producer, warp 5 the MMA issuer.  Every wait gives up after ~2 s.
+// Roles (224 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
+// TMA producer, warp 5 issues S^T and warp 6 O^T: a wait costs an issuing thread
+// the time of four small products, so each hides the other's.  Every wait gives
+// up after ~2 s.
 #include <cuda.h>
 
 #include "latent.h"
@@ -27,10 +29,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kProducerWarp = 4;
-constexpr int kMmaWarp = 5;
+constexpr int kScoreWarp = 5;
+constexpr int kValueWarp = 6;
 constexpr int kKeys = 64;                  // keys of a tile
 constexpr int kHalf = kKeys * 128;         // 64 keys x 64 dims
 constexpr int kBlock = 2 * kHalf;          // 64 keys x 128 dims
@@ -39,27 +42,25 @@ constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
 constexpr int kMinShare = 2;               // tiles a cluster takes at least
 
-// Shared memory.  N = 64 leaves room for two tiles exactly: they are taken in
-// groups of two (both S^T, then both O^T products), so that one tile's softmax
-// runs beside the other's products and the first blocks are free again early.
+// Shared memory: the queries, rings of value blocks and of rotary blocks, the
+// weights of two tiles.  N = 64 leaves room for two tiles exactly.
 template <int N>
 struct Dim {
-    static constexpr int kGroup = N == 64 ? 2 : 1;
     static constexpr int kV = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of value blocks
-    static constexpr int kR = N == 64 ? 1 : 3;                  // ring of rotary blocks
+    static constexpr int kR = N == 64 ? 1 : N == 32 ? 2 : 3;    // ring of rotary blocks
     static constexpr int kQBlock = N * 128;                     // N columns x 64 dims
     static constexpr int kPBytes = kKeys * N * 2;
     static constexpr int kVOff = 0;
     static constexpr int kROff = kVOff + kV * kBlock;
     static constexpr int kQOff = kROff + kR * kHalf;
     static constexpr int kPOff = kQOff + 9 * kQBlock;
-    static constexpr int kBarOff = kPOff + kGroup * kPBytes;
-    static constexpr int kNumBars = 2 * kV + 2 * kR + 1 + 2 * kGroup + 3;
+    static constexpr int kBarOff = kPOff + 2 * kPBytes;
+    static constexpr int kNumBars = 2 * kV + 2 * kR + 9;
     static constexpr int kRedOff = kBarOff + ((kNumBars * 8 + 127) / 128) * 128;  // [4][N] per-warp maxima or sums
     static constexpr int kColOff = kRedOff + 4 * N * 4;   // [N] factors (rescale, then 1 / sum)
     static constexpr int kLimOff = kColOff + N * 4;       // [N] keys each column sees
-    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 6 warp totals, 6 + the cluster's first unit
-    static constexpr int kBytes = kPlanOff + 96;
+    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 7 warp totals, the cluster's first unit
+    static constexpr int kBytes = kPlanOff + 80;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kSCol = 4 * N;              // S^T behind O^T's four blocks
     static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
@@ -134,7 +135,6 @@ template <int N, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p, const Sched sc) {
     using D = Dim<N>;
-    constexpr int G = D::kGroup;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -147,16 +147,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* r_full = v_empty + D::kV;
     uint64_t* r_empty = r_full + D::kR;
     uint64_t* q_ready = r_empty + D::kR;
-    uint64_t* s_full = q_ready + 1;   // [G]
-    uint64_t* p_full = s_full + G;    // [G]
-    uint64_t* pv_done = p_full + G;   // the group's first tile
-    uint64_t* o_full = pv_done + 1;
+    uint64_t* s_full = q_ready + 1;   // [2]
+    uint64_t* p_full = s_full + 2;    // [2]
+    uint64_t* pv_done = p_full + 2;   // [2]
+    uint64_t* o_full = pv_done + 2;
     uint64_t* mma_done = o_full + 1;
     float* red = reinterpret_cast<float*>(smem + D::kRedOff);
     float* colf = reinterpret_cast<float*>(smem + D::kColOff);
     int* lim = reinterpret_cast<int*>(smem + D::kLimOff);
-    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [6]
-    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 48);         // unit, tile, tmem, abort
+    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [7]
+    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 56);         // unit, tile, tmem, abort
     volatile int* abort_flag = plan + 3;
 
     // ---- the plan: the line of all units' tiles, and this cluster's share of it
@@ -182,17 +182,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&r_empty[s], CL);
         }
         mbar_init(q_ready, kSoftmaxThreads);
-        for (int t = 0; t < G; ++t) {
+        for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], kSoftmaxThreads);
+            mbar_init(&pv_done[t], 1);
         }
-        mbar_init(pv_done, 1);
         mbar_init(o_full, 1);
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tc_alloc(reinterpret_cast<uint32_t*>(plan + 2), D::kTmem);
+    if (warp == kValueWarp) tc_alloc(reinterpret_cast<uint32_t*>(plan + 2), D::kTmem);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -312,85 +312,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < D::kV; ++k) mbar_wait(&v_full[k], k < v.s ? v.ph : v.ph ^ 1);
             for (int k = 0; k < D::kR; ++k) mbar_wait(&r_full[k], k < r.s ? r.ph : r.ph ^ 1);
         }
-    } else if (warp == kMmaWarp) {
-        // =============================== MMA ================================
+    } else if (warp == kScoreWarp) {
+        // =============================== S^T ================================
         if (elect_one()) {
-            constexpr uint32_t kIdescS = tc_idesc(kKeys, N, false, false);
-            constexpr uint32_t kIdescO = tc_idesc(128, N, true, true);
-            constexpr uint16_t kAll = (1 << CL) - 1;
-            auto release = [&](uint64_t* bar) {
-                if constexpr (CL > 1) tc_commit_all(bar, kAll);
-                else tc_commit(bar);
-            };
+            constexpr uint32_t kIdesc = tc_idesc(kKeys, N, false, false);
             const uint64_t dq = tc_desc(sbase + D::kQOff, 16, 1024, 128);
-            // tiles as S^T's A operand (keys x dims, K-major) and as O^T's (dims x keys, MN-major)
-            const uint64_t ds = tc_desc(sbase + D::kVOff, 16, 1024, 128), dr = tc_desc(sbase + D::kROff, 16, 1024, 128);
-            const uint64_t dv = tc_desc(sbase + D::kVOff, kHalf, 1024, 128);
-            // P^T: rows of keys, N columns wide, one swizzle row each
-            const uint64_t dp = tc_desc(sbase + D::kPOff, 16, 16 * N, 2 * N);
+            const uint64_t dv = tc_desc(sbase + D::kVOff, 16, 1024, 128), dr = tc_desc(sbase + D::kROff, 16, 1024, 128);
             Ring<D::kV> v;
             Ring<D::kR> r;
             int n = 0, nseg = 0;
-            uint32_t np = 0;  // bit t: parity of tile t's next weights
             bool ok = true;
-            // S^T (+)= 64 dims of the tile times block qb of the queries
-            auto half = [&](uint32_t d, uint64_t da, int qb, bool acc) {
-                const uint64_t db = dq + qb * (D::kQBlock >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) tc_mma(d, da + 2 * kk, db + 2 * kk, kIdescS, acc || kk > 0);
-            };
-            // (loops stay rolled: their code shares the instruction caches with the softmax)
             while (ok && it.next(p, sc)) {
                 ok = wait(q_ready, nseg++ & 1);
-                for (int j = it.j0; ok && j < it.j1; j += G) {
-                    const int g = min(G, it.j1 - j);
-                    int s = v.s;  // the group's first value block
-#pragma unroll 1
-                    for (int t = 0; t < g; ++t, ++n) {
-                        const uint32_t d = tmem + D::kSCol + t * N;
-#pragma unroll 1
-                        for (int k = 0; k <= kBlocks; ++k) {
-                            if (k == (n & 1) * kBlocks) {
-                                ok = ok && wait(&r_full[r.s], r.ph);
-                                tc_after_sync();
-                                half(d, dr + r.s * (kHalf >> 4), kRopeBlock, k > 0);
-                                release(&r_empty[r.s]);
-                                r.next();
-                            } else {
-                                const int b = k - 1 + (n & 1);
-                                ok = ok && wait(&v_full[v.s], v.ph);
-                                tc_after_sync();
-                                const uint64_t da = ds + v.s * (kBlock >> 4);
-                                half(d, da, 2 * b, k > 0);
-                                half(d, da + (kHalf >> 4), 2 * b + 1, true);
-                                v.next();
-                            }
-                        }
-                        tc_commit(&s_full[t]);
-                    }
-#pragma unroll 1
-                    for (int t = 0; t < g && ok; ++t) {
-                        ok = wait(&p_full[t], (np >> t) & 1);
-                        np ^= 1u << t;
-                        tc_after_sync();
-                        const uint64_t db = dp + t * (D::kPBytes >> 4);
-#pragma unroll 1
-                        for (int b = 0; b < kBlocks; ++b) {
-                            const uint64_t da = dv + s * (kBlock >> 4);
+                for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
+                    const int t = n & 1;
+                    const uint32_t d = tmem + D::kSCol + t * N;
+                    // S^T (+)= 64 dims of the tile times block qb of the queries
+                    auto half = [&](uint64_t da, int qb, bool acc) {
 #pragma unroll
-                            for (int kk = 0; kk < kKeys / 16; ++kk)
-                                tc_mma(tmem + b * N, da + kk * (2048 >> 4), db + kk * (32 * N >> 4), kIdescO,
-                                       j + t > it.j0 || kk > 0);
-                            release(&v_empty[s]);
-                            if (++s == D::kV) s = 0;
-                        }
-                        if (G > 1 && t == 0) tc_commit(pv_done);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma(d, da + 2 * kk, dq + ((qb * D::kQBlock + kk * 32) >> 4), kIdesc, acc || kk > 0);
+                    };
+                    auto rope = [&](bool acc) {
+                        ok = ok && wait(&r_full[r.s], r.ph);
+                        tc_after_sync();
+                        half(dr + r.s * (kHalf >> 4), kRopeBlock, acc);
+                        if constexpr (CL > 1) tc_commit_all(&r_empty[r.s], (1 << CL) - 1);
+                        else tc_commit(&r_empty[r.s]);
+                        r.next();
+                    };
+                    ok = wait(&p_full[t], ((n >> 1) & 1) ^ 1);  // the softmax has read tile n - 2's scores
+                    if (t == 0) rope(false);
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) {
+                        ok = ok && wait(&v_full[v.s], v.ph);
+                        tc_after_sync();
+                        const uint64_t da = dv + v.s * (kBlock >> 4);
+                        half(da, 2 * b, t == 0 || b > 0);
+                        half(da + (kHalf >> 4), 2 * b + 1, true);
+                        v.next();
                     }
+                    if (t == 1) rope(true);
+                    tc_commit(&s_full[t]);
                 }
-                if (ok) tc_commit(o_full);
             }
             // nothing of this thread's still runs in the tensor pipe when the CTA
             // winds down (after a failed wait the last products may)
+            tc_commit(mma_done);
+            if (!mbar_wait(mma_done, 0)) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        }
+    } else if (warp == kValueWarp) {
+        // =============================== O^T ================================
+        if (elect_one()) {
+            constexpr uint32_t kIdesc = tc_idesc(128, N, true, true);
+            // the tiles once more, as dims x keys; P^T: rows of keys, N columns wide, one swizzle row each
+            const uint64_t dv = tc_desc(sbase + D::kVOff, kHalf, 1024, 128);
+            const uint64_t dp = tc_desc(sbase + D::kPOff, 16, 16 * N, 2 * N);
+            int n = 0, s = 0;
+            bool ok = true;
+            while (ok && it.next(p, sc)) {
+                for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
+                    const int t = n & 1;
+                    ok = wait(&p_full[t], (n >> 1) & 1);
+                    tc_after_sync();
+                    const uint64_t db = dp + t * (D::kPBytes >> 4);
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const uint64_t da = dv + s * (kBlock >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            tc_mma(tmem + b * N, da + kk * (2048 >> 4), db + kk * (32 * N >> 4), kIdesc, j > it.j0 || kk > 0);
+                        if constexpr (CL > 1) tc_commit_all(&v_empty[s], (1 << CL) - 1);
+                        else tc_commit(&v_empty[s]);
+                        if (++s == D::kV) s = 0;
+                    }
+                    tc_commit(&pv_done[t]);
+                }
+                if (ok) tc_commit(o_full);
+            }
             tc_commit(mma_done);
             if (!mbar_wait(mma_done, 0)) set_err(p.err, PKV_ERRBIT_TIMEOUT);
         }
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key_of = 16 * warp + (lane >> 2);  // and 8 further
         int nseg = 0;
         int vfirst = 0;  // the tile's first value block in the ring
-        uint32_t ns[G] = {}, ng = 0;
+        int n = 0;
         int slot = 0;  // of a partial state: 0 for the share's first segment
 
         // outputs of units that see no key: zeros
@@ -478,10 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[c] = -INFINITY;
                 l[c] = lb[c] = 0.f;
             }
-            for (int j = it.j0; j < it.j1; ++j) {
-                const int t = (j - it.j0) % G;
+            for (int j = it.j0; j < it.j1; ++j, ++n) {
+                const int t = n & 1;
                 const int key0 = j * kKeys;
-                wait(&s_full[t], ns[t]++ & 1);
+                wait(&s_full[t], (n >> 1) & 1);
                 __syncwarp();
                 tc_after_sync();
                 uint32_t v[N / 2];
@@ -532,9 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lb[c] *= alpha;
                         if (warp == 0 && lane < 4) colf[at] = alpha;
                     }
-                    // O^T's columns follow once the products issued so far are done: those
-                    // of earlier groups are (this S^T came after them in the pipe)
-                    if (G > 1 && t == 1) wait(pv_done, ng & 1);
+                    // O^T's columns follow once the previous tile's products are done
+                    if (j > it.j0) wait(&pv_done[t ^ 1], ((n - 1) >> 1) & 1);
                     __syncwarp();
                     bar_sync(1, kSoftmaxThreads);
                     if (j > it.j0) {
@@ -552,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // weights, rounded to bf16 for the product; their sums rounded (the
                 // output's divisor) and not (the LSE)
+                wait(&pv_done[t], ((n >> 1) & 1) ^ 1);  // tile n - 2's products are done with this buffer
                 uint8_t* pt = smem + D::kPOff + t * D::kPBytes;
 #pragma unroll
                 for (int f = 0; f < N / 8; ++f) {
@@ -585,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_before_sync();
                 mbar_arrive(&p_full[t]);
                 vfirst = (vfirst + kBlocks) % D::kV;
-                if (t == G - 1 || j + 1 == it.j1) ++ng;
             }
             // ---- the segment's columns: sums over the tile's rows, then O^T / sum
             const bool whole = it.j0 == 0 && it.j1 == w.tiles;
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CL > 1) cluster_sync_all();  // the other CTA's copies and commits land here no more
     else __syncthreads();
     tc_after_sync();
-    if (warp == kMmaWarp) tc_dealloc(tmem, D::kTmem);
+    if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
 
 // One CTA a (cut, column): where cluster c starts inside a unit, and the unit
