@@ -821,8 +821,4 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     return launch<16, 1>(p, sc, tmap, s);
 }
 
-cudaError_t launch_ragged_attn(const RaggedParams& p, const void*, const void*, const void*, cudaStream_t s) {
-    return launch_ragged_simt(p, s);
-}
-
 }  // namespace pkv

@@ -105,8 +105,64 @@ __device__ __forceinline__ void tc_load_frag(uint32_t taddr, uint32_t (&v)[N / 2
                      : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24) : "r"(taddr) : "memory");
     }
 }
+#define PKV_LD32(r) \
+    "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" r "}, "
+// 128 consecutive columns of this thread's lane
+__device__ __forceinline__ void tc_load128(uint32_t taddr, uint32_t (&v)[128]) {
+    asm volatile(
+        PKV_LD32("%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31") "[%128];\n\t"
+        PKV_LD32("%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63") "[%129];\n\t"
+        PKV_LD32("%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+                 "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95") "[%130];\n\t"
+        PKV_LD32("%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+                 "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127") "[%131];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24), PKV_O8(32), PKV_O8(40), PKV_O8(48), PKV_O8(56), PKV_O8(64),
+          PKV_O8(72), PKV_O8(80), PKV_O8(88), PKV_O8(96), PKV_O8(104), PKV_O8(112), PKV_O8(120)
+        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96) : "memory");
+}
+// 32 consecutive columns of this thread's lane; the caller waits for stores
+__device__ __forceinline__ void tc_load32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        PKV_LD32("%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31") "[%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tc_store32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), PKV_I8(0), PKV_I8(8), PKV_I8(16), PKV_I8(24) : "memory");
+}
+#undef PKV_LD32
 #undef PKV_O8
 #undef PKV_I8
+
+// max of three values in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// acc += the two bf16 values of a packed pair, each widened exactly to f32
+__device__ __forceinline__ void add_pair(float2& acc, uint32_t pk) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %0;\n\t"
+        "add.rn.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y) : "r"(pk));
+}
+
+// 16 bytes global -> shared without registers; zeros where `valid` is false
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
 
 // ---------------------------------------------------------------------------
 // clusters

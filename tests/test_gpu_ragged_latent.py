@@ -77,6 +77,12 @@ def test_lengths_beyond_the_bounds_are_reported(flags):
     assert torch.equal(out[:10].cpu(), want[:10]) and (out[30:] == 7).all()
 
 
+@pytest.mark.parametrize("mask", ["causal", "none"])
+def test_more_key_tiles_than_the_ring_repeats_after(mask):
+    """The ring's order of blocks repeats every eight key tiles."""
+    Ragged([300, 20], [2300, 1100], 2, mask=mask, seed=7).check()
+
+
 def test_same_bits_every_time():
     c = Ragged([300, 256], [700, 256], 4, seed=6)
     a, la, _ = c.run()
