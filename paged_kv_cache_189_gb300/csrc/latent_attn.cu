@@ -17,10 +17,11 @@
 // one column group's tiles) and leaves a partial state where a group's tiles
 // were cut; a second launch joins those.
 //
-// Roles (224 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
-// TMA producer, warp 5 issues S^T and warp 6 O^T: a wait costs an issuing thread
-// the time of four small products, so each hides the other's.  Every wait gives
-// up after ~2 s.
+// Roles (256 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
+// TMA producer, warp 5 issues S^T and warp 6 O^T (a wait costs an issuing thread
+// the time of four small products, so each hides the other's), warp 7 loads the
+// next segment's queries while the last one's softmax and outputs still run.
+// Every wait gives up after ~2 s.
 #include <cuda.h>
 
 #include "latent.h"
@@ -29,17 +30,19 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kProducerWarp = 4;
 constexpr int kScoreWarp = 5;
 constexpr int kValueWarp = 6;
+constexpr int kQueryWarp = 7;
 constexpr int kKeys = 64;                  // keys of a tile
 constexpr int kHalf = kKeys * 128;         // 64 keys x 64 dims
 constexpr int kBlock = 2 * kHalf;          // 64 keys x 128 dims
 constexpr int kBlocks = kLatentDim / 128;  // value blocks of a tile (the rotary half block is apart)
 constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
+constexpr int kNoPage = INT32_MIN;         // look-up past the last page: zeros, and no error
 constexpr int kMinShare = 2;               // tiles a cluster takes at least
 
 // Shared memory: the queries, rings of value blocks and of rotary blocks, the
@@ -55,11 +58,11 @@ struct Dim {
     static constexpr int kQOff = kROff + kR * kHalf;
     static constexpr int kPOff = kQOff + 9 * kQBlock;
     static constexpr int kBarOff = kPOff + 2 * kPBytes;
-    static constexpr int kNumBars = 2 * kV + 2 * kR + 9;
+    static constexpr int kNumBars = 2 * kV + 2 * kR + 10;
     static constexpr int kRedOff = kBarOff + ((kNumBars * 8 + 127) / 128) * 128;  // [4][N] per-warp maxima or sums
     static constexpr int kColOff = kRedOff + 4 * N * 4;   // [N] factors (rescale, then 1 / sum)
     static constexpr int kLimOff = kColOff + N * 4;       // [N] keys each column sees
-    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 7 warp totals, the cluster's first unit
+    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 8 warp totals, the cluster's first unit
     static constexpr int kBytes = kPlanOff + 80;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kSCol = 4 * N;              // S^T behind O^T's four blocks
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* r_full = v_empty + D::kV;
     uint64_t* r_empty = r_full + D::kR;
     uint64_t* q_ready = r_empty + D::kR;
-    uint64_t* s_full = q_ready + 1;   // [2]
+    uint64_t* q_free = q_ready + 1;
+    uint64_t* s_full = q_free + 1;    // [2]
     uint64_t* p_full = s_full + 2;    // [2]
     uint64_t* pv_done = p_full + 2;   // [2]
     uint64_t* o_full = pv_done + 2;
@@ -155,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red = reinterpret_cast<float*>(smem + D::kRedOff);
     float* colf = reinterpret_cast<float*>(smem + D::kColOff);
     int* lim = reinterpret_cast<int*>(smem + D::kLimOff);
-    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [7]
-    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 56);         // unit, tile, tmem, abort
+    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [8]
+    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 64);         // unit, tile, tmem, abort
     volatile int* abort_flag = plan + 3;
 
     // ---- the plan: the line of all units' tiles, and this cluster's share of it
@@ -181,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&r_full[s], 1);
             mbar_init(&r_empty[s], CL);
         }
-        mbar_init(q_ready, kSoftmaxThreads);
+        mbar_init(q_ready, 32);
+        mbar_init(q_free, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], kSoftmaxThreads);
@@ -249,63 +254,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             prefetch_tmap(&tm);
             constexpr uint16_t kAll = (1 << CL) - 1;
+            constexpr int kPages = 2 / CL;  // of a tile: a cluster's CTAs look up one each
             Ring<D::kV> v;
             Ring<D::kR> r;
-            int n = 0;
-            bool alive = true;
-            while (alive && it.next(p, sc)) {
-                const int32_t* bt = p.block_table + static_cast<int64_t>(it.w.b) * p.block_table_stride;
-                const int last_page = (it.w.vis + 31) / 32;
-                // the tile's pages (a cluster's CTAs look up one each); the sentinel reads as zeros
-                auto fetch = [&](int j, int (&ph)[2 / CL]) {
+            // The pages are looked up one tile ahead of their copies, on across segments.
+            // (Asking for them in L2 further ahead made every call slower, 70 -> 80 us
+            // for 64 sequences of 16 heads: the queries' loads then wait behind it.)
+            int j = 0, last_page = 0;
+            const int32_t* bt = nullptr;
+            int64_t unseen = seg0.left;
+            it.j1 = 0;
+            auto look_up = [&](int (&ph)[kPages]) {
+                if (unseen-- <= 0) return;
+                if (j >= it.j1) {
+                    it.next(p, sc);
+                    j = it.j0;
+                    bt = p.block_table + static_cast<int64_t>(it.w.b) * p.block_table_stride;
+                    last_page = (it.w.vis + 31) / 32;
+                }
 #pragma unroll
-                    for (int k = 0; k < 2 / CL; ++k) {
-                        const int lp = 2 * j + (CL > 1 ? rank : k);
+                for (int k = 0; k < kPages; ++k) {
+                    const int lp = 2 * j + (CL > 1 ? rank : k);
+                    ph[k] = lp < last_page ? bt[lp] : kNoPage;
+                }
+                ++j;
+            };
+            int next[kPages];
+            look_up(next);
+            bool alive = true;
+            for (int64_t n = 0; alive && n < seg0.left; ++n) {
+                int ph[kPages];
+#pragma unroll
+                for (int k = 0; k < kPages; ++k) {
+                    ph[k] = next[k];
+                    if (ph[k] < 0 || ph[k] >= p.num_pages) {  // the sentinel reads as zeros
+                        if (ph[k] != kNoPage && p.checked) set_err(p.err, PKV_ERRBIT_PAGE);
                         ph[k] = static_cast<int>(p.num_pages);
-                        if (lp < last_page) {
-                            const int page = bt[lp];
-                            if (page >= 0 && page < p.num_pages) ph[k] = page;
-                            else if (p.checked) set_err(p.err, PKV_ERRBIT_PAGE);
-                        }
+                    }
+                }
+                look_up(next);
+                // 64 dims from d0 of the tile's pages to dst
+                auto copy = [&](uint8_t* dst, uint64_t* bar, int d0) {
+#pragma unroll
+                    for (int k = 0; k < kPages; ++k) {
+                        if constexpr (CL > 1) tma_load_3d_all(dst + rank * 4096, &tm, bar, d0, 0, ph[k], kAll);
+                        else tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
                     }
                 };
-                int next[2 / CL];
-                fetch(it.j0, next);
-                for (int j = it.j0; alive && j < it.j1; ++j, ++n) {
-                    int ph[2 / CL];
-#pragma unroll
-                    for (int k = 0; k < 2 / CL; ++k) ph[k] = next[k];
-                    if (j + 1 < it.j1) fetch(j + 1, next);
-                    // 64 dims from d0 of the tile's pages to dst
-                    auto copy = [&](uint8_t* dst, uint64_t* bar, int d0) {
-#pragma unroll
-                        for (int k = 0; k < 2 / CL; ++k) {
-                            if constexpr (CL > 1) tma_load_3d_all(dst + rank * 4096, &tm, bar, d0, 0, ph[k], kAll);
-                            else tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
-                        }
-                    };
-                    // (a fresh barrier's previous phase counts as complete: the first round passes)
-                    auto rope = [&] {
-                        if (!wait(&r_empty[r.s], r.ph ^ 1)) return false;
-                        mbar_arrive_expect_tx(&r_full[r.s], kHalf);
-                        copy(smem + D::kROff + r.s * kHalf, &r_full[r.s], kLatentDim);
-                        r.next();
-                        return true;
-                    };
-                    if ((n & 1) == 0) alive = rope();
-                    for (int b = 0; alive && b < kBlocks; ++b) {
-                        if (!wait(&v_empty[v.s], v.ph ^ 1)) {
-                            alive = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&v_full[v.s], kBlock);
-                        uint8_t* dst = smem + D::kVOff + v.s * kBlock;
-                        copy(dst, &v_full[v.s], b * 128);
-                        copy(dst + kHalf, &v_full[v.s], b * 128 + 64);
-                        v.next();
+                // (a fresh barrier's previous phase counts as complete: the first round passes)
+                auto rope = [&] {
+                    if (!wait(&r_empty[r.s], r.ph ^ 1)) return false;
+                    mbar_arrive_expect_tx(&r_full[r.s], kHalf);
+                    copy(smem + D::kROff + r.s * kHalf, &r_full[r.s], kLatentDim);
+                    r.next();
+                    return true;
+                };
+                if ((n & 1) == 0) alive = rope();
+                for (int b = 0; alive && b < kBlocks; ++b) {
+                    if (!wait(&v_empty[v.s], v.ph ^ 1)) {
+                        alive = false;
+                        break;
                     }
-                    if (alive && (n & 1) == 1) alive = rope();
+                    mbar_arrive_expect_tx(&v_full[v.s], kBlock);
+                    uint8_t* dst = smem + D::kVOff + v.s * kBlock;
+                    copy(dst, &v_full[v.s], b * 128);
+                    copy(dst + kHalf, &v_full[v.s], b * 128 + 64);
+                    v.next();
                 }
+                if (alive && (n & 1) == 1) alive = rope();
             }
             // do not leave with copies into this CTA's shared memory in flight
             // (buffers behind `s` were last filled in this round, the others in the one before)
@@ -355,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t == 1) rope(true);
                     tc_commit(&s_full[t]);
                 }
+                tc_commit(q_free);
             }
             // nothing of this thread's still runs in the tensor pipe when the CTA
             // winds down (after a failed wait the last products may)
@@ -392,6 +409,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_commit(mma_done);
             if (!mbar_wait(mma_done, 0)) set_err(p.err, PKV_ERRBIT_TIMEOUT);
+        }
+    } else if (warp == kQueryWarp) {
+        // ============================= queries ==============================
+        int nseg = 0;
+        while (it.next(p, sc)) {
+            const int col0 = it.w.c0 + rank * N;
+            wait(q_free, (nseg++ & 1) ^ 1);
+            __syncwarp();
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(it.w.r0) * p.q_token_stride;
+            int i = col0 / p.heads, h = col0 - i * p.heads;
+#pragma unroll 2
+            for (int c = 0; c < N; ++c) {  // columns past the last: zeros
+                const bool held = col0 + c < it.w.cols;
+                const __nv_bfloat16* row = held ? q + i * p.q_token_stride + h * p.q_head_stride : q;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int ch = lane + 32 * k;
+                    if (ch < kLatentRow / 8)
+                        copy16_async(sbase + D::kQOff + (ch >> 3) * D::kQBlock + sw128_offset(c, ch & 7),
+                                     row + (held ? ch * 8 : 0), held);
+                }
+                if (++h == p.heads) {
+                    h = 0;
+                    ++i;
+                }
+            }
+            copy_async_wait();
+            fence_proxy_async_smem();
+            mbar_arrive(q_ready);
         }
     } else {
         // ===================== softmax and outputs ==========================
@@ -432,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (it.next(p, sc)) {
             const Unit& w = it.w;
             const int col0 = w.c0 + rank * N;  // this CTA's first column
-            // ---- limits and queries of the columns.  Those past the last (their
+            // ---- limits of the columns.  Those past the last (their
             // results go nowhere) see what the unit sees, so they mask nothing.
             if (threadIdx.x < N) {
                 const int i = (col0 + threadIdx.x) / p.heads;
@@ -441,30 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = i >= w.qreal ? 0 : p.causal ? max(0, w.kv - w.qreal + i + 1) : w.kv;
                 lim[threadIdx.x] = l;
             }
-            // (the previous segment's S^T products are done with these queries: their S^T was read)
-            const __nv_bfloat16* qbase = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(w.r0) * p.q_token_stride;
-            constexpr int kChunks = kLatentRow / 8, kBatch = 9;  // loads in flight a thread
-            for (int i0 = threadIdx.x; i0 < N * kChunks; i0 += kBatch * kSoftmaxThreads) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int idx = i0 + k * kSoftmaxThreads, c = idx / kChunks, ch = idx - c * kChunks, col = col0 + c;
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (col < w.cols) {
-                        const int i = col / p.heads;
-                        v[k] = *reinterpret_cast<const uint4*>(qbase + i * p.q_token_stride +
-                                                               static_cast<int64_t>(col - i * p.heads) * p.q_head_stride + ch * 8);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int idx = i0 + k * kSoftmaxThreads, c = idx / kChunks, ch = idx - c * kChunks;
-                    *reinterpret_cast<uint4*>(smem + D::kQOff + (ch >> 3) * D::kQBlock + sw128_offset(c, ch & 7)) = v[k];
-                }
-            }
-            fence_proxy_async_smem();
-            tc_before_sync();
-            mbar_arrive(q_ready);
             bar_sync(1, kSoftmaxThreads);
             int lim_min = lim[lane % N];
             if (N > 32) lim_min = min(lim_min, lim[(lane + 32) % N]);
@@ -630,28 +652,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int valid = min(N, w.cols - col0);  // columns that exist (uniform)
             for (int b = 0; b < kBlocks; ++b) {
                 const int dim = b * 128 + warp * 32 + lane;
-                for (int c0 = 0; c0 < N; c0 += 16) {
-                    uint32_t o[16];
-                    tc_load16(tmem + quad + b * N + c0, o);
-                    float f[16];
+                constexpr int kCols = N < 32 ? 16 : 32;  // columns read at once
+#pragma unroll 1
+                for (int c0 = 0; c0 < N; c0 += kCols) {
+                    uint32_t o[kCols];
+                    if constexpr (kCols == 16) tc_load16(tmem + quad + b * N + c0, o);
+                    else tc_load32(tmem + quad + b * N + c0, o);
+                    float f[kCols];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]) * colf[c0 + e];
+                    for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * colf[c0 + e];
                     if (!whole || p.out_f32) {
-                        float* dst = whole ? static_cast<float*>(p.out) + out_row * kLatentDim : part;
+                        float* dst = (whole ? static_cast<float*>(p.out) + out_row * kLatentDim : part) +
+                                     static_cast<int64_t>(c0) * kLatentDim + dim;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c0 + e < valid) dst[static_cast<int64_t>(c0 + e) * kLatentDim + dim] = f[e];
+                        for (int e = 0; e < kCols; ++e)
+                            if (c0 + e < valid) dst[e * kLatentDim] = f[e];
                     } else {
                         // lanes exchange one of two columns, so that each stores a pair of dims
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * kLatentDim;
                         const bool odd = lane & 1;
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                             (out_row + c0 + (odd ? 1 : 0)) * kLatentDim + (dim & ~1);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
+                        for (int e = 0; e < kCols; e += 2) {
                             const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : f[e + 1], 1);
                             const uint32_t pk = odd ? pack_bf16x2(got, f[e + 1]) : pack_bf16x2(f[e], got);
-                            const int c = c0 + e + (odd ? 1 : 0);
-                            if (c < valid)
-                                *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(c) * kLatentDim + (dim & ~1)) = pk;
+                            if (c0 + e + (odd ? 1 : 0) < valid) *reinterpret_cast<uint32_t*>(dst + e * kLatentDim) = pk;
                         }
                     }
                 }
@@ -669,56 +694,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
 
-// One CTA a (cut, column): where cluster c starts inside a unit, and the unit
-// began in the cluster before it, the unit's states, one a cluster in line, are
-// joined: out = sum w_i O_i / sum w_i with w_i = e^(lse_i - max).
-constexpr int kJoinThreads = 128;
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentParams p, const Sched sc) {
-    const int c = blockIdx.x + 1, col = blockIdx.y;
+// Four columns a CTA: where cluster c starts inside a unit that began in the
+// cluster before it, the unit's states, one a cluster in line, are joined: out =
+// sum w_i O_i / sum w_i with w_i = e^(lse_i - max).  Of few states each column's
+// group of 128 threads takes all; of many all groups take every fourth state of
+// each column.
+constexpr int kJoinCols = 4;
+constexpr int kJoinFew = 8;
+__global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const LatentParams p, const Sched sc) {
+    const int c = blockIdx.x + 1, g = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = sc.dir[c];
     if (d.x < 0 || d.y == 0 || d.y > d.w) return;
     const Unit w = unit_of(p, sc, d.x);
-    if (w.c0 + col >= w.cols) return;
     const int64_t share = d.w, at = c * share;  // the unit's tiles lie at [at - d.y, at - d.y + d.z)
-    const int last = static_cast<int>((at - d.y + d.z - 1) / share);
+    const int n = static_cast<int>((at - d.y + d.z - 1) / share) - c + 2;
     const int first_slot = d.y < share ? 1 : 0;
-    const int n = last - c + 2;
-    auto piece = [&](int k) {
+    auto piece = [&](int k, int col) {
         return (static_cast<int64_t>(c - 1 + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
     };
-    __shared__ float sh[kJoinThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY;
-    for (int k = threadIdx.x; k < n; k += kJoinThreads) m = fmaxf(m, sc.lse[piece(k)]);
-    m = warp_max(m);
-    if (lane == 0) sh[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
-    const float mm = m == -INFINITY ? 0.f : m;
-    float4 acc = make_float4(0, 0, 0, 0);
-    float sum = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const int64_t at_k = piece(k);
-        const float wk = fast_exp2((sc.lse[at_k] - mm) * kLog2e);
-        const float4 o = *reinterpret_cast<const float4*>(sc.o + at_k * kLatentDim + threadIdx.x * 4);
-        sum += wk;
-        acc.x = fmaf(wk, o.x, acc.x);
-        acc.y = fmaf(wk, o.y, acc.y);
-        acc.z = fmaf(wk, o.z, acc.z);
-        acc.w = fmaf(wk, o.w, acc.w);
+    // the states k0, k0 + step, ... of a column: their weights' sum and weighted sum
+    auto gather = [&](int col, int k0, int step, float& m, float& sum, float4& acc) {
+        m = -INFINITY;
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, sc.lse[piece(k, col)]);
+        m = warp_max(m);
+        if (m == -INFINITY) m = 0.f;
+        sum = 0.f;
+        acc = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int k = k0; k < n; k += step) {
+            const int64_t st = piece(k, col);
+            const float wk = fast_exp2((sc.lse[st] - m) * kLog2e);
+            const float4 o = *reinterpret_cast<const float4*>(sc.o + st * kLatentDim + t * 4);
+            sum += wk;
+            acc.x = fmaf(wk, o.x, acc.x);
+            acc.y = fmaf(wk, o.y, acc.y);
+            acc.z = fmaf(wk, o.z, acc.z);
+            acc.w = fmaf(wk, o.w, acc.w);
+        }
+    };
+    auto store = [&](int col, float m, float sum, const float4& acc) {
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+        const int64_t row = static_cast<int64_t>(w.r0) * p.heads + w.c0 + col;
+        if (p.out_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatentDim + t * 4) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kLatentDim + t * 4) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        if (p.lse && t == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + __log2f(sum) * kLn2;
+    };
+    float m, sum;
+    float4 acc;
+    const int col0 = blockIdx.y * kJoinCols;
+    if (n <= kJoinFew) {
+        if (w.c0 + col0 + g < w.cols) {
+            gather(col0 + g, 0, 1, m, sum, acc);
+            store(col0 + g, m, sum, acc);
+        }
+        return;
     }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    const int64_t row = static_cast<int64_t>(w.r0) * p.heads + w.c0 + col;
-    if (p.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatentDim + threadIdx.x * 4) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    } else {
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kLatentDim + threadIdx.x * 4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    __shared__ float4 sh_o[kJoinCols][128];
+    __shared__ float sh_s[kJoinCols];
+    for (int col = col0; col < col0 + kJoinCols && w.c0 + col < w.cols; ++col) {
+        gather(col, g, kJoinCols, m, sum, acc);
+        sh_o[g][t] = acc;
+        if (t == 0) sh_s[g] = sum;
+        __syncthreads();
+        if (g == 0) {
+#pragma unroll
+            for (int k = 1; k < kJoinCols; ++k) {
+                const float4 o = sh_o[k][t];
+                sum += sh_s[k];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+            }
+            store(col, m, sum, acc);
+        }
+        __syncthreads();
     }
-    if (p.lse && threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : mm + __log2f(sum) * kLn2;
 }
 
 template <int N, int CL>
@@ -760,8 +817,8 @@ cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, cud
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t jc = {};
-    jc.gridDim = dim3(static_cast<unsigned>(sc.workers - 1), static_cast<unsigned>(sc.cols));
-    jc.blockDim = dim3(kJoinThreads);
+    jc.gridDim = dim3(static_cast<unsigned>(sc.workers - 1), static_cast<unsigned>(sc.cols / kJoinCols));
+    jc.blockDim = dim3(128 * kJoinCols);
     jc.stream = s;
     jc.attrs = pdl;
     jc.numAttrs = 1;
