@@ -51,6 +51,7 @@ template <int N>
 struct Dim {
     static constexpr int kV = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of value blocks
     static constexpr int kR = N == 64 ? 1 : N == 32 ? 2 : 3;    // ring of rotary blocks
+    static constexpr int kAhead = N == 64 ? 1 : 0;              // tiles asked for in L2 ahead of their copies
     static constexpr int kQBlock = N * 128;                     // N columns x 64 dims
     static constexpr int kPBytes = kKeys * N * 2;
     static constexpr int kVOff = 0;
@@ -257,9 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kPages = 2 / CL;  // of a tile: a cluster's CTAs look up one each
             Ring<D::kV> v;
             Ring<D::kR> r;
-            // The pages are looked up one tile ahead of their copies, on across segments.
-            // (Asking for them in L2 further ahead made every call slower, 70 -> 80 us
-            // for 64 sequences of 16 heads: the queries' loads then wait behind it.)
+            // The pages are looked up a tile ahead of their use, on across segments.
+            // Where two tiles are all that shared memory holds, pages are asked for in
+            // L2 kAhead tiles before their copies.
+            constexpr int kAhead = D::kAhead;
             int j = 0, last_page = 0;
             const int32_t* bt = nullptr;
             int64_t unseen = seg0.left;
@@ -279,20 +281,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++j;
             };
-            int next[kPages];
-            look_up(next);
-            bool alive = true;
-            for (int64_t n = 0; alive && n < seg0.left; ++n) {
-                int ph[kPages];
+            // checked pages; the sentinel reads as zeros
+            auto ask = [&](int (&ph)[kPages]) {
 #pragma unroll
                 for (int k = 0; k < kPages; ++k) {
-                    ph[k] = next[k];
-                    if (ph[k] < 0 || ph[k] >= p.num_pages) {  // the sentinel reads as zeros
+                    if (ph[k] < 0 || ph[k] >= p.num_pages) {
                         if (ph[k] != kNoPage && p.checked) set_err(p.err, PKV_ERRBIT_PAGE);
                         ph[k] = static_cast<int>(p.num_pages);
+                    } else if (kAhead > 0) {
+                        const char* page = static_cast<const char*>(p.pool) + static_cast<int64_t>(ph[k]) * p.page_stride * 2;
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(page), "r"(32 * kLatentRow * 2) : "memory");
                     }
                 }
-                look_up(next);
+            };
+            int next[kAhead + 1][kPages];
+#pragma unroll
+            for (int k = 0; k <= kAhead; ++k) {
+#pragma unroll
+                for (int q = 0; q < kPages; ++q) next[k][q] = kNoPage;
+                look_up(next[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) ask(next[k]);
+            bool alive = true;
+            for (int64_t n = 0; alive && n < seg0.left; ++n) {
+                ask(next[kAhead]);
+                int ph[kPages];
+#pragma unroll
+                for (int q = 0; q < kPages; ++q) {
+                    ph[q] = next[0][q];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) next[k][q] = next[k + 1][q];
+                    next[kAhead][q] = kNoPage;
+                }
+                look_up(next[kAhead]);
                 // 64 dims from d0 of the tile's pages to dst
                 auto copy = [&](uint8_t* dst, uint64_t* bar, int d0) {
 #pragma unroll
@@ -694,24 +716,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
 
-// Four columns a CTA: where cluster c starts inside a unit that began in the
-// cluster before it, the unit's states, one a cluster in line, are joined: out =
-// sum w_i O_i / sum w_i with w_i = e^(lse_i - max).  Of few states each column's
-// group of 128 threads takes all; of many all groups take every fourth state of
-// each column.
+// Four columns a CTA and cut: where cluster c starts inside a unit, the unit's
+// states, one a cluster in line, are joined: out = sum w_i O_i / sum w_i with w_i =
+// e^(lse_i - max).  Few states: the unit's first cut joins all four columns, a
+// group of 128 threads each.  Many: its first four cuts take a column each, every
+// group a quarter of the states.
 constexpr int kJoinCols = 4;
 constexpr int kJoinFew = 8;
 __global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const LatentParams p, const Sched sc) {
     const int c = blockIdx.x + 1, g = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = sc.dir[c];
-    if (d.x < 0 || d.y == 0 || d.y > d.w) return;
+    if (d.x < 0 || d.y == 0) return;
     const Unit w = unit_of(p, sc, d.x);
     const int64_t share = d.w, at = c * share;  // the unit's tiles lie at [at - d.y, at - d.y + d.z)
-    const int n = static_cast<int>((at - d.y + d.z - 1) / share) - c + 2;
-    const int first_slot = d.y < share ? 1 : 0;
+    const int cut = (d.y - 1) / d.w;             // cuts of the unit before this one
+    const int first = c - 1 - cut;               // the cluster that it begins in
+    const int n = static_cast<int>((at - d.y + d.z - 1) / share) - first + 1;
+    const int first_slot = at - d.y > first * share ? 1 : 0;
+    if (cut > 0 && (n <= kJoinFew || cut >= kJoinCols)) return;
     auto piece = [&](int k, int col) {
-        return (static_cast<int64_t>(c - 1 + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
+        return (static_cast<int64_t>(first + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
     };
     // the states k0, k0 + step, ... of a column: their weights' sum and weighted sum
     auto gather = [&](int col, int k0, int step, float& m, float& sum, float4& acc) {
@@ -757,25 +782,23 @@ __global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const Late
     }
     __shared__ float4 sh_o[kJoinCols][128];
     __shared__ float sh_s[kJoinCols];
-    for (int col = col0; col < col0 + kJoinCols && w.c0 + col < w.cols; ++col) {
-        gather(col, g, kJoinCols, m, sum, acc);
-        sh_o[g][t] = acc;
-        if (t == 0) sh_s[g] = sum;
-        __syncthreads();
-        if (g == 0) {
+    const int col = col0 + cut;
+    if (w.c0 + col >= w.cols) return;
+    gather(col, g, kJoinCols, m, sum, acc);
+    sh_o[g][t] = acc;
+    if (t == 0) sh_s[g] = sum;
+    __syncthreads();
+    if (g > 0) return;
 #pragma unroll
-            for (int k = 1; k < kJoinCols; ++k) {
-                const float4 o = sh_o[k][t];
-                sum += sh_s[k];
-                acc.x += o.x;
-                acc.y += o.y;
-                acc.z += o.z;
-                acc.w += o.w;
-            }
-            store(col, m, sum, acc);
-        }
-        __syncthreads();
+    for (int k = 1; k < kJoinCols; ++k) {
+        const float4 o = sh_o[k][t];
+        sum += sh_s[k];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
     }
+    store(col, m, sum, acc);
 }
 
 template <int N, int CL>
