@@ -17,11 +17,12 @@
 // one column group's tiles) and leaves a partial state where a group's tiles
 // were cut; a second launch joins those.
 //
-// Roles (256 threads, one CTA an SM): warps 0-3 softmax and outputs, warp 4 the
-// TMA producer, warp 5 issues S^T and warp 6 O^T (a wait costs an issuing thread
-// the time of four small products, so each hides the other's), warp 7 loads the
-// next segment's queries while the last one's softmax and outputs still run.
-// Every wait gives up after ~2 s.
+// Roles (one CTA an SM): four softmax and output warps (eight for 64 columns: the
+// softmax of a tile is part of the time its buffers are held), then the TMA
+// producer, the issuers of S^T and of O^T (a wait costs an issuing thread the time
+// of four small products, so each hides the other's) and the loader of the next
+// segment's queries, which runs beside the last one's softmax and outputs.  Every
+// wait gives up after ~2 s.
 #include <cuda.h>
 
 #include "latent.h"
@@ -30,12 +31,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSoftmaxThreads = 128;
-constexpr int kProducerWarp = 4;
-constexpr int kScoreWarp = 5;
-constexpr int kValueWarp = 6;
-constexpr int kQueryWarp = 7;
 constexpr int kKeys = 64;                  // keys of a tile
 constexpr int kHalf = kKeys * 128;         // 64 keys x 64 dims
 constexpr int kBlock = 2 * kHalf;          // 64 keys x 128 dims
@@ -49,6 +44,14 @@ constexpr int kMinShare = 2;               // tiles a cluster takes at least
 // weights of two tiles.  N = 64 leaves room for two tiles exactly.
 template <int N>
 struct Dim {
+    static constexpr int kSoftmaxWarps = N == 64 ? 8 : 4;
+    static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+    static constexpr int kProducerWarp = kSoftmaxWarps;
+    static constexpr int kScoreWarp = kSoftmaxWarps + 1;
+    static constexpr int kValueWarp = kSoftmaxWarps + 2;
+    static constexpr int kQueryWarp = kSoftmaxWarps + 3;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+    static constexpr int kWarpCols = N / (kSoftmaxWarps / 4);   // columns a softmax warp works on
     static constexpr int kV = N == 64 ? 8 : N == 32 ? 10 : 11;  // ring of value blocks
     static constexpr int kR = N == 64 ? 1 : N == 32 ? 2 : 3;    // ring of rotary blocks
     static constexpr int kAhead = N == 64 ? 1 : 0;              // tiles asked for in L2 ahead of their copies
@@ -63,8 +66,8 @@ struct Dim {
     static constexpr int kRedOff = kBarOff + ((kNumBars * 8 + 127) / 128) * 128;  // [4][N] per-warp maxima or sums
     static constexpr int kColOff = kRedOff + 4 * N * 4;   // [N] factors (rescale, then 1 / sum)
     static constexpr int kLimOff = kColOff + N * 4;       // [N] keys each column sees
-    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: 8 warp totals, the cluster's first unit
-    static constexpr int kBytes = kPlanOff + 80;
+    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: warp totals, the cluster's first unit
+    static constexpr int kBytes = kPlanOff + 16 + 8 * (kSoftmaxWarps + 4);
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kSCol = 4 * N;              // S^T behind O^T's four blocks
     static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 256 : 128;
@@ -136,9 +139,12 @@ struct Ring {
 };
 
 template <int N, int CL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p, const Sched sc) {
     using D = Dim<N>;
+    constexpr int kThreads = D::kThreads, kSoftmaxThreads = D::kSoftmaxThreads;
+    constexpr int kProducerWarp = D::kProducerWarp, kScoreWarp = D::kScoreWarp, kValueWarp = D::kValueWarp;
+    constexpr int kQueryWarp = D::kQueryWarp;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red = reinterpret_cast<float*>(smem + D::kRedOff);
     float* colf = reinterpret_cast<float*>(smem + D::kColOff);
     int* lim = reinterpret_cast<int*>(smem + D::kLimOff);
-    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [8]
-    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + 64);         // unit, tile, tmem, abort
+    int64_t* plan_tot = reinterpret_cast<int64_t*>(smem + D::kPlanOff);  // [warps]
+    int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + kThreads / 4);  // unit, tile, tmem, abort
     volatile int* abort_flag = plan + 3;
 
     // ---- the plan: the line of all units' tiles, and this cluster's share of it
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_free, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], kSoftmaxThreads);
+            mbar_init(&p_full[t], D::kSoftmaxWarps);
             mbar_init(&pv_done[t], 1);
         }
         mbar_init(o_full, 1);
@@ -359,7 +365,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<D::kV> v;
             Ring<D::kR> r;
             int n = 0, nseg = 0;
-            bool ok = true;
+            bool ok = true, landed = false;
+            // a block's barrier is probed among the products of the one before it: a
+            // wait between two batches would leave the pipe idle for ~150 cycles
+            auto probe = [&](uint64_t* bar, uint32_t parity) {
+                landed = mbar_test(bar, parity);
+                if (landed) tc_after_sync();
+            };
+            auto settle = [&](uint64_t* bar, uint32_t parity) {
+                if (landed) return;
+                ok = ok && wait(bar, parity);
+                tc_after_sync();
+            };
             while (ok && it.next(p, sc)) {
                 ok = wait(q_ready, nseg++ & 1);
                 for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
@@ -372,26 +389,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_mma(d, da + 2 * kk, dq + ((qb * D::kQBlock + kk * 32) >> 4), kIdesc, acc || kk > 0);
                     };
                     auto rope = [&](bool acc) {
-                        ok = ok && wait(&r_full[r.s], r.ph);
-                        tc_after_sync();
+                        settle(&r_full[r.s], r.ph);
                         half(dr + r.s * (kHalf >> 4), kRopeBlock, acc);
                         if constexpr (CL > 1) tc_commit_all(&r_empty[r.s], (1 << CL) - 1);
                         else tc_commit(&r_empty[r.s]);
                         r.next();
                     };
                     ok = wait(&p_full[t], ((n >> 1) & 1) ^ 1);  // the softmax has read tile n - 2's scores
-                    if (t == 0) rope(false);
+                    if (t == 0) {
+                        rope(false);
+                        probe(&v_full[v.s], v.ph);
+                    }
 #pragma unroll
                     for (int b = 0; b < kBlocks; ++b) {
-                        ok = ok && wait(&v_full[v.s], v.ph);
-                        tc_after_sync();
+                        settle(&v_full[v.s], v.ph);
                         const uint64_t da = dv + v.s * (kBlock >> 4);
                         half(da, 2 * b, t == 0 || b > 0);
-                        half(da + (kHalf >> 4), 2 * b + 1, true);
                         v.next();
+                        // (the rotary block ends odd tiles and begins even ones)
+                        if (b + 1 < kBlocks) probe(&v_full[v.s], v.ph);
+                        else probe(&r_full[r.s], r.ph);
+                        half(da + (kHalf >> 4), 2 * b + 1, true);
                     }
                     if (t == 1) rope(true);
                     tc_commit(&s_full[t]);
+                    if (t == 1) probe(&r_full[r.s], r.ph);
+                    else probe(&v_full[v.s], v.ph);
                 }
                 tc_commit(q_free);
             }
@@ -463,13 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ===================== softmax and outputs ==========================
-        // A warp holds 16 keys of the tile (its quadrant's first 16 lanes), a
-        // thread 2 keys and N / 4 columns: maxima and sums stay per thread, and a
-        // column's reference moves (by all threads together) only when a score
+        // A warp holds 16 keys of the tile (its quadrant's first 16 lanes) and W
+        // columns, a thread 2 keys and W / 4 columns: maxima and sums stay per thread,
+        // and a column's reference moves (by all threads together) only when a score
         // passes it by 2^8, so most tiles exchange nothing but that one vote.
-        constexpr int NC = N / 4;
-        const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;
-        const int key_of = 16 * warp + (lane >> 2);  // and 8 further
+        constexpr int W = D::kWarpCols, NC = W / 4;
+        const int wq = warp & 3, wc = (warp >> 2) * W;  // quadrant, first column
+        const uint32_t quad = static_cast<uint32_t>(wq * 32) << 16;
+        const int key_of = 16 * wq + (lane >> 2);       // and 8 further
+        const int col_of = wc + 2 * (lane & 3);         // [2 f + e] is column col_of + 8 f + e
         int nseg = 0;
         int vfirst = 0;  // the tile's first value block in the ring
         int n = 0;
@@ -481,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int col = w.c0 + rank * N + c;
                 if (col >= w.cols) break;
                 const int64_t at = static_cast<int64_t>(w.r0) * p.heads + col;
-                const int d = threadIdx.x * 4;
+                const int d = (threadIdx.x & 127) * 4;
+                if (threadIdx.x >= 128) break;
                 if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kLatentDim + d) = make_float4(0, 0, 0, 0);
                 else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kLatentDim + d) = make_uint2(0, 0);
                 if (p.lse && threadIdx.x == 0) p.lse[at] = -INFINITY;
@@ -515,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
 
-            float m[NC], l[NC], lb[NC];  // column 8 f + 2 (lane % 4) + e is [2 f + e]
+            float m[NC], l[NC], lb[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 m[c] = -INFINITY;
@@ -527,15 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&s_full[t], (n >> 1) & 1);
                 __syncwarp();
                 tc_after_sync();
-                uint32_t v[N / 2];
-                tc_load_frag<N>(tmem + quad + D::kSCol + t * N, v);
-                float s[N / 2];
+                uint32_t v[W / 2];
+                tc_load_frag<W>(tmem + quad + D::kSCol + t * N + wc, v);
+                float s[W / 2];
 #pragma unroll
-                for (int e = 0; e < N / 2; ++e) s[e] = __uint_as_float(v[e]) * p.scale_log2;
+                for (int e = 0; e < W / 2; ++e) s[e] = __uint_as_float(v[e]) * p.scale_log2;
                 if (key0 + kKeys > lim_min) {
 #pragma unroll
-                    for (int f = 0; f < N / 8; ++f) {
-                        const int2 lm = *reinterpret_cast<const int2*>(lim + 8 * f + 2 * (lane & 3));
+                    for (int f = 0; f < W / 8; ++f) {
+                        const int2 lm = *reinterpret_cast<const int2*>(lim + col_of + 8 * f);
                         const int k = key0 + key_of;
                         s[4 * f] = k < lm.x ? s[4 * f] : -INFINITY;
                         s[4 * f + 1] = k < lm.y ? s[4 * f + 1] : -INFINITY;
@@ -545,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 bool past = false;
 #pragma unroll
-                for (int f = 0; f < N / 8; ++f)
+                for (int f = 0; f < W / 8; ++f)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) past |= fmaxf(s[4 * f + e], s[4 * f + 2 + e]) > m[2 * f + e] + kLazyRescale;
                 if (bar_any(1, kSoftmaxThreads, past)) {
@@ -559,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (lane < 4) {
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) red[warp * N + 8 * (c >> 1) + 2 * lane + (c & 1)] = mx[c];
+                        for (int c = 0; c < NC; ++c) red[wq * N + col_of + 8 * (c >> 1) + (c & 1)] = mx[c];
                     }
                     bar_sync(1, kSoftmaxThreads);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const int at = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
+                        const int at = col_of + 8 * (c >> 1) + (c & 1);
                         const float tm4 = fmaxf(fmaxf(red[at], red[N + at]), fmaxf(red[2 * N + at], red[3 * N + at]));
                         float alpha = 1.f;
                         if (tm4 > m[c] + kLazyRescale) {
@@ -573,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         l[c] *= alpha;
                         lb[c] *= alpha;
-                        if (warp == 0 && lane < 4) colf[at] = alpha;
+                        if (wq == 0 && lane < 4) colf[at] = alpha;
                     }
                     // O^T's columns follow once the previous tile's products are done
                     if (j > it.j0) wait(&pv_done[t ^ 1], ((n - 1) >> 1) & 1);
@@ -581,23 +607,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bar_sync(1, kSoftmaxThreads);
                     if (j > it.j0) {
                         tc_after_sync();
-                        for (int c16 = 0; c16 < 4 * N / 16; ++c16) {
+                        for (int c16 = 0; c16 < kBlocks * W / 16; ++c16) {
+                            const int c = wc + c16 % (W / 16) * 16;
+                            const uint32_t at = tmem + quad + c16 / (W / 16) * N + c;
                             uint32_t o[16];
-                            tc_load16(tmem + quad + c16 * 16, o);
+                            tc_load16(at, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * colf[(c16 * 16 + e) % N]);
-                            tc_store16(tmem + quad + c16 * 16, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * colf[c + e]);
+                            tc_store16(at, o);
                         }
                         tc_wait_store();
                     }
                 }
                 // weights, rounded to bf16 for the product; their sums rounded (the
                 // output's divisor) and not (the LSE)
-                wait(&pv_done[t], ((n >> 1) & 1) ^ 1);  // tile n - 2's products are done with this buffer
+                // tile n - 2's products are done with this buffer of weights (where the ring
+                // holds two tiles, tile n has taken the blocks that they released last)
+                if (D::kV > 2 * kBlocks) wait(&pv_done[t], ((n >> 1) & 1) ^ 1);
                 uint8_t* pt = smem + D::kPOff + t * D::kPBytes;
 #pragma unroll
-                for (int f = 0; f < N / 8; ++f) {
+                for (int f = 0; f < W / 8; ++f) {
                     const float m0 = m[2 * f] == -INFINITY ? 0.f : m[2 * f], m1 = m[2 * f + 1] == -INFINITY ? 0.f : m[2 * f + 1];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -608,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lb[2 * f] += bf16lo(pk);
                         lb[2 * f + 1] += bf16hi(pk);
                         const int k = key_of + 8 * r;
-                        uint32_t at = k * 2 * N + f * 16;
+                        uint32_t at = k * 2 * N + wc * 2 + f * 16;
                         at ^= ((at >> 7) & (N / 8 - 1)) << 4;
                         *reinterpret_cast<uint32_t*>(pt + at + (lane & 3) * 4) = pk;
                     }
@@ -626,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc_before_sync();
-                mbar_arrive(&p_full[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
                 vfirst = (vfirst + kBlocks) % D::kV;
             }
             // ---- the segment's columns: sums over the tile's rows, then O^T / sum
@@ -640,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float sum = pass == 0 ? l[c] : lb[c];
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane < 4) red[warp * N + 8 * (c >> 1) + 2 * lane + (c & 1)] = sum;
+                    if (lane < 4) red[wq * N + col_of + 8 * (c >> 1) + (c & 1)] = sum;
                 }
                 bar_sync(1, kSoftmaxThreads);
                 if (threadIdx.x < N) {
@@ -649,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else lbsum = sum;
                 }
             }
-            if (warp == 0 && lane < 4) {
+            if (wq == 0 && lane < 4) {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) colf[8 * (c >> 1) + 2 * lane + (c & 1)] = m[c];
+                for (int c = 0; c < NC; ++c) colf[col_of + 8 * (c >> 1) + (c & 1)] = m[c];
             }
             bar_sync(1, kSoftmaxThreads);
             if (threadIdx.x < N) {
@@ -673,33 +703,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* part = sc.o + ((static_cast<int64_t>(worker) * 2 + slot) * sc.cols + rank * N) * kLatentDim;
             const int valid = min(N, w.cols - col0);  // columns that exist (uniform)
             for (int b = 0; b < kBlocks; ++b) {
-                const int dim = b * 128 + warp * 32 + lane;
-                constexpr int kCols = N < 32 ? 16 : 32;  // columns read at once
-#pragma unroll 1
-                for (int c0 = 0; c0 < N; c0 += kCols) {
-                    uint32_t o[kCols];
-                    if constexpr (kCols == 16) tc_load16(tmem + quad + b * N + c0, o);
-                    else tc_load32(tmem + quad + b * N + c0, o);
-                    float f[kCols];
+                const int dim = b * 128 + wq * 32 + lane;
+                uint32_t o[W];
+                if constexpr (W == 16) tc_load16(tmem + quad + b * N + wc, o);
+                else tc_load32(tmem + quad + b * N + wc, o);
+                float f[W];
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * colf[c0 + e];
-                    if (!whole || p.out_f32) {
-                        float* dst = (whole ? static_cast<float*>(p.out) + out_row * kLatentDim : part) +
-                                     static_cast<int64_t>(c0) * kLatentDim + dim;
+                for (int e = 0; e < W; ++e) f[e] = __uint_as_float(o[e]) * colf[wc + e];
+                if (!whole || p.out_f32) {
+                    float* dst = (whole ? static_cast<float*>(p.out) + out_row * kLatentDim : part) +
+                                 static_cast<int64_t>(wc) * kLatentDim + dim;
 #pragma unroll
-                        for (int e = 0; e < kCols; ++e)
-                            if (c0 + e < valid) dst[e * kLatentDim] = f[e];
-                    } else {
-                        // lanes exchange one of two columns, so that each stores a pair of dims
-                        const bool odd = lane & 1;
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                             (out_row + c0 + (odd ? 1 : 0)) * kLatentDim + (dim & ~1);
+                    for (int e = 0; e < W; ++e)
+                        if (wc + e < valid) dst[e * kLatentDim] = f[e];
+                } else {
+                    // lanes exchange one of two columns, so that each stores a pair of dims
+                    const bool odd = lane & 1;
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                         (out_row + wc + (odd ? 1 : 0)) * kLatentDim + (dim & ~1);
 #pragma unroll
-                        for (int e = 0; e < kCols; e += 2) {
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : f[e + 1], 1);
-                            const uint32_t pk = odd ? pack_bf16x2(got, f[e + 1]) : pack_bf16x2(f[e], got);
-                            if (c0 + e + (odd ? 1 : 0) < valid) *reinterpret_cast<uint32_t*>(dst + e * kLatentDim) = pk;
-                        }
+                    for (int e = 0; e < W; e += 2) {
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? f[e] : f[e + 1], 1);
+                        const uint32_t pk = odd ? pack_bf16x2(got, f[e + 1]) : pack_bf16x2(f[e], got);
+                        if (wc + e + (odd ? 1 : 0) < valid) *reinterpret_cast<uint32_t*>(dst + e * kLatentDim) = pk;
                     }
                 }
             }
@@ -805,7 +831,7 @@ template <int N, int CL>
 cudaLaunchConfig_t config(int workers, cudaLaunchAttribute* attr, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(workers * CL));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Dim<N>::kThreads);
     cfg.dynamicSmemBytes = Dim<N>::kBytes;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
