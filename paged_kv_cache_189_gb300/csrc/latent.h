@@ -84,8 +84,11 @@ struct LatentPlan {
     size_t ws_bytes;
 };
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms);
+// tmap: the pool as {576, 32, pages}, boxes of a page's 64 columns.  q_boxes: tmap_q holds
+// the queries as {576, heads, rows} in boxes of 64 columns x pl.cols (row, head) pairs,
+// which takes heads that divide pl.cols or are a multiple of it.
 cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void* workspace, const void* tmap,
-                               cudaStream_t s);
+                               const void* tmap_q, bool q_boxes, cudaStream_t s);
 
 // Expanded attention over ragged K and V.
 struct RaggedParams {

@@ -36,6 +36,7 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) %
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 
 constexpr int64_t kMaxCount = (int64_t(1) << 31) - 256;
+constexpr int64_t kMaxStride = (int64_t(1) << 39) / 2 - 8;  // elements: tensor maps hold strides below 2^40 bytes
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -220,7 +221,19 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
     const int box[3] = {64, 32, 1};
     const pkv_status m = make_map(&tm, pool, 3, dims, st, box);
     if (m != PKV_OK) return m;
-    return from_cuda(pkv::launch_latent_attn(p, pl, workspace, &tm, s), "latent attention");
+    // queries as boxes of a CTA's columns, where its (row, head) pairs are whole rows of
+    // heads or a part of one, and the strides can stand in a tensor map
+    CUtensorMap tq = tm;
+    const int hbox = num_heads < pl.cols ? num_heads : pl.cols;
+    bool boxes = (pl.cols % num_heads == 0 || num_heads % pl.cols == 0) && (num_heads == 1 || q_head_stride >= pkv::kLatentRow) &&
+                 q_token_stride >= pkv::kLatentRow && q_token_stride < kMaxStride && q_head_stride < kMaxStride;
+    if (boxes) {
+        const int64_t qd[3] = {pkv::kLatentRow, num_heads, kMaxCount};
+        const int64_t qs[2] = {num_heads == 1 ? int64_t(pkv::kLatentRow) : q_head_stride, q_token_stride};
+        const int qbox[3] = {64, hbox, pl.cols / hbox};
+        boxes = make_map(&tq, q, 3, qd, qs, qbox) == PKV_OK;
+    }
+    return from_cuda(pkv::launch_latent_attn(p, pl, workspace, &tm, &tq, boxes, s), "latent attention");
 }
 
 pkv_status ragged_attention_latent(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
@@ -255,7 +268,6 @@ pkv_status ragged_attention_latent(const void* q, int64_t q_token_stride, int64_
         return fail(PKV_ERR_INVALID_ARG, "ragged attention: 16-byte aligned pointers and strides multiple of 8");
     if (!aligned(q_indptr, 4) || !aligned(kv_indptr, 4))
         return fail(PKV_ERR_INVALID_ARG, "ragged attention: misaligned index pointer");
-    constexpr int64_t kMaxStride = (int64_t(1) << 39) / 2 - 8;  // tensor maps hold strides below 2^40 bytes
     if (k_token_stride > kMaxStride || k_head_stride > kMaxStride || k_pe_stride > kMaxStride ||
         v_token_stride > kMaxStride || v_head_stride > kMaxStride)
         return fail(PKV_ERR_UNSUPPORTED, "ragged attention: strides above 2^39 bytes");

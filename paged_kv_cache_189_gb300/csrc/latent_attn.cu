@@ -84,6 +84,7 @@ struct Sched {
     int4* dir;                  // [workers] where each cluster starts: unit, tile in it, its tiles, share
     float* lse;                 // [workers][2][cols] partial states: a first and a last segment
     float* o;                   // [workers][2][cols][512]
+    bool q_boxes;               // a CTA's columns are a box of the queries' tensor map
 };
 
 __device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, int u) {
@@ -140,7 +141,8 @@ struct Ring {
 
 template <int N, int CL>
 __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p, const Sched sc) {
+    latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q,
+                       const LatentParams p, const Sched sc) {
     using D = Dim<N>;
     constexpr int kThreads = D::kThreads, kSoftmaxThreads = D::kSoftmaxThreads;
     constexpr int kProducerWarp = D::kProducerWarp, kScoreWarp = D::kScoreWarp, kValueWarp = D::kValueWarp;
@@ -462,8 +464,19 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             const int col0 = it.w.c0 + rank * N;
             wait(q_free, (nseg++ & 1) ^ 1);
             __syncwarp();
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(it.w.r0) * p.q_token_stride;
             int i = col0 / p.heads, h = col0 - i * p.heads;
+            if (sc.q_boxes && col0 + N <= it.w.cols) {
+                // whole rows of heads, or a part of one: nine boxes (all of them existing rows)
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_ready, 9 * D::kQBlock);
+                    for (int k = 0; k < 9; ++k)
+                        tma_load_3d(smem + D::kQOff + k * D::kQBlock, &tm_q, q_ready, k * 64, h, it.w.r0 + i);
+                } else {
+                    mbar_arrive(q_ready);
+                }
+                continue;
+            }
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(it.w.r0) * p.q_token_stride;
 #pragma unroll 2
             for (int c = 0; c < N; ++c) {  // columns past the last: zeros
                 const bool held = col0 + c < it.w.cols;
@@ -484,6 +497,8 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(q_ready);
         }
+        // do not leave with copies into this CTA's shared memory in flight
+        if (nseg > 0) mbar_wait(q_ready, (nseg - 1) & 1);
     } else {
         // ===================== softmax and outputs ==========================
         // A warp holds 16 keys of the tile (its quadrant's first 16 lanes) and W
@@ -855,12 +870,13 @@ cudaError_t opt_in() {
 }
 
 template <int N, int CL>
-cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, cudaStream_t s) {
+cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, const void* tmap_q, cudaStream_t s) {
     cudaError_t e = opt_in<N, CL>();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config<N, CL>(sc.workers, attr, s);
-    e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap), p, sc);
+    e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap),
+                           *static_cast<const CUtensorMap*>(tmap_q), p, sc);
     if (e != cudaSuccess || sc.workers == 1) return e;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -910,21 +926,22 @@ LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int
 }
 
 cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void* workspace, const void* tmap,
-                               cudaStream_t s) {
+                               const void* tmap_q, bool q_boxes, cudaStream_t s) {
     Sched sc;
     sc.workers = pl.workers;
     sc.groups = pl.groups;
     sc.cols = pl.cols * pl.cluster;
+    sc.q_boxes = q_boxes;
     char* w = static_cast<char*>(workspace);
     sc.dir = reinterpret_cast<int4*>(w);
     w += round256(pl.workers * sizeof(int4));
     sc.lse = reinterpret_cast<float*>(w);
     w += round256(static_cast<size_t>(pl.workers) * 2 * sc.cols * 4);
     sc.o = reinterpret_cast<float*>(w);
-    if (pl.cluster == 2) return launch<64, 2>(p, sc, tmap, s);
-    if (pl.cols == 64) return launch<64, 1>(p, sc, tmap, s);
-    if (pl.cols == 32) return launch<32, 1>(p, sc, tmap, s);
-    return launch<16, 1>(p, sc, tmap, s);
+    if (pl.cluster == 2) return launch<64, 2>(p, sc, tmap, tmap_q, s);
+    if (pl.cols == 64) return launch<64, 1>(p, sc, tmap, tmap_q, s);
+    if (pl.cols == 32) return launch<32, 1>(p, sc, tmap, tmap_q, s);
+    return launch<16, 1>(p, sc, tmap, tmap_q, s);
 }
 
 }  // namespace pkv
