@@ -11,11 +11,12 @@
 // the same bytes MN-major for O^T.
 //
 // A CTA holds N = 16, 32 or 64 columns; more are held by a cluster of two CTAs,
-// each of which loads one page of every tile for both (multicast).  The keys of
-// all sequences are one line of tiles that the clusters share out evenly: a
-// cluster works through its share segment by segment (a segment is a range of
-// one column group's tiles) and leaves a partial state where a group's tiles
-// were cut; a second launch joins those.
+// each of which loads one page of every tile for both (multicast).  The tiles of
+// all units (a unit is a column group of a sequence) are one line that the clusters
+// share out evenly, each unit's tiles behind a few more places that stand for what
+// beginning it costs.  A cluster works through its share segment by segment (a
+// segment is a range of one unit's tiles) and leaves a partial state where a unit
+// was cut; a second launch joins those.
 //
 // Roles (one CTA an SM): four softmax and output warps (eight for 64 columns: the
 // softmax of a tile is part of the time its buffers are held), then the TMA
@@ -39,6 +40,8 @@ constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
 constexpr int kNoPage = INT32_MIN;         // look-up past the last page: zeros, and no error
 constexpr int kMinShare = 2;               // tiles a cluster takes at least
+// What a segment costs beside its tiles (queries, first copies, outputs), in tiles
+constexpr int kToll = 1, kTollWide = 2;
 
 // Shared memory: the queries, rings of value blocks and of rotary blocks, the
 // weights of two tiles.  N = 64 leaves room for two tiles exactly.
@@ -81,7 +84,8 @@ struct Unit {
 
 struct Sched {
     int workers, groups, cols;  // clusters, column groups a sequence may have, columns of a group
-    int4* dir;                  // [workers] where each cluster starts: unit, tile in it, its tiles, share
+    int toll;                   // places of the line ahead of each unit's tiles
+    int4* dir;                  // [workers] where each cluster starts: unit, place in it, its tiles, share
     float* lse;                 // [workers][2][cols] partial states: a first and a last segment
     float* o;                   // [workers][2][cols][512]
     bool q_boxes;               // a CTA's columns are a box of the queries' tensor map
@@ -105,24 +109,31 @@ __device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, 
     return w;
 }
 
+// The places of the line that a unit takes.
+__device__ __forceinline__ int unit_places(const Sched& sc, const Unit& w) { return w.tiles > 0 ? w.tiles + sc.toll : 0; }
+
 // The segments of one cluster's share, in order; every role walks them alike.
 struct Segments {
-    int u, o;
-    int64_t left;
+    int u, o;      // unit and place in it that come next
+    int64_t left;  // places of the share
     Unit w;
-    int j0, j1;
+    int j0, j1;    // the segment: tiles [j0, j1) of w
     __device__ __forceinline__ bool next(const LatentParams& p, const Sched& sc) {
-        if (left <= 0) return false;
-        w = unit_of(p, sc, u);
-        while (o >= w.tiles) {
-            o = 0;
-            w = unit_of(p, sc, ++u);
+        while (left > 0) {
+            w = unit_of(p, sc, u);
+            const int places = unit_places(sc, w);
+            const int to = static_cast<int>(min(static_cast<int64_t>(places), o + left));
+            j0 = max(0, o - sc.toll);
+            j1 = to - sc.toll;
+            left -= max(0, to - o);
+            o = to;
+            if (o >= places) {
+                o = 0;
+                ++u;
+            }
+            if (j1 > j0) return true;
         }
-        j0 = o;
-        j1 = static_cast<int>(min(static_cast<int64_t>(w.tiles), o + left));
-        left -= j1 - j0;
-        o = j1;
-        return true;
+        return false;
     }
 };
 
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
     int64_t mine = 0;
-    for (int u = u0; u < u1; ++u) mine += unit_of(p, sc, u).tiles;
+    for (int u = u0; u < u1; ++u) mine += unit_places(sc, unit_of(p, sc, u));
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -215,18 +226,19 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         before += w < warp ? plan_tot[w] : 0;
         total += plan_tot[w];
     }
-    const int64_t share = max((total + sc.workers - 1) / sc.workers, static_cast<int64_t>(kMinShare));
+    const int64_t share = max((total + sc.workers - 1) / sc.workers, static_cast<int64_t>(kMinShare + sc.toll));
     const int64_t start = worker * share;
     Segments seg0;
     seg0.left = max(min(share, total - start), static_cast<int64_t>(0));
     if (start >= before && start < before + mine) {  // one thread at most
         int64_t at = before;
         for (int u = u0; u < u1; ++u) {
-            const int t = unit_of(p, sc, u).tiles;
+            const Unit w = unit_of(p, sc, u);
+            const int t = unit_places(sc, w);
             if (start < at + t) {
                 plan[0] = u;
                 plan[1] = static_cast<int>(start - at);
-                if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], t, static_cast<int>(share));
+                if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], w.tiles, static_cast<int>(share));
                 break;
             }
             at += t;
@@ -272,12 +284,11 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             constexpr int kAhead = D::kAhead;
             int j = 0, last_page = 0;
             const int32_t* bt = nullptr;
-            int64_t unseen = seg0.left;
+            int queued = 0;  // tiles looked up and not yet copied
             it.j1 = 0;
             auto look_up = [&](int (&ph)[kPages]) {
-                if (unseen-- <= 0) return;
                 if (j >= it.j1) {
-                    it.next(p, sc);
+                    if (!it.next(p, sc)) return;  // (and again: nothing is left)
                     j = it.j0;
                     bt = p.block_table + static_cast<int64_t>(it.w.b) * p.block_table_stride;
                     last_page = (it.w.vis + 31) / 32;
@@ -288,6 +299,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                     ph[k] = lp < last_page ? bt[lp] : kNoPage;
                 }
                 ++j;
+                ++queued;
             };
             // checked pages; the sentinel reads as zeros
             auto ask = [&](int (&ph)[kPages]) {
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) ask(next[k]);
             bool alive = true;
-            for (int64_t n = 0; alive && n < seg0.left; ++n) {
+            for (int n = 0; alive && queued > 0; ++n, --queued) {
                 ask(next[kAhead]);
                 int ph[kPages];
 #pragma unroll
@@ -768,13 +780,13 @@ __global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const Late
     const int c = blockIdx.x + 1, g = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d = sc.dir[c];
-    if (d.x < 0 || d.y == 0) return;
+    if (d.x < 0 || d.y <= sc.toll) return;
     const Unit w = unit_of(p, sc, d.x);
-    const int64_t share = d.w, at = c * share;  // the unit's tiles lie at [at - d.y, at - d.y + d.z)
-    const int cut = (d.y - 1) / d.w;             // cuts of the unit before this one
-    const int first = c - 1 - cut;               // the cluster that it begins in
-    const int n = static_cast<int>((at - d.y + d.z - 1) / share) - first + 1;
-    const int first_slot = at - d.y > first * share ? 1 : 0;
+    const int64_t share = d.w, off = c * share - d.y, tile0 = off + sc.toll;  // the unit's places, its first tile's
+    const int first = static_cast<int>(tile0 / share);                        // the cluster that it begins in
+    const int n = static_cast<int>((tile0 + d.z - 1) / share) - first + 1;
+    const int first_slot = first * share < off ? 1 : 0;
+    const int cut = c - first - 1;                                            // cuts of the unit before this one
     if (cut > 0 && (n <= kJoinFew || cut >= kJoinCols)) return;
     auto piece = [&](int k, int col) {
         return (static_cast<int64_t>(first + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
@@ -930,6 +942,7 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     Sched sc;
     sc.workers = pl.workers;
     sc.groups = pl.groups;
+    sc.toll = pl.cols == 64 ? kTollWide : kToll;
     sc.cols = pl.cols * pl.cluster;
     sc.q_boxes = q_boxes;
     char* w = static_cast<char*>(workspace);
