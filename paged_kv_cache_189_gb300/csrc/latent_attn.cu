@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         if (lane >= o) x += y;
     }
     if (lane == 31) plan_tot[warp] = x;
-    if (threadIdx.x == 0) {
+    if (warp == kQueryWarp && lane == 0) {
         for (int s = 0; s < D::kV; ++s) {
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], CL);
@@ -221,12 +221,15 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
+    if (CL > 1) cluster_arrive();  // this CTA's barriers are initialised
     int64_t before = x - mine, total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
         before += w < warp ? plan_tot[w] : 0;
         total += plan_tot[w];
     }
-    const int64_t share = max((total + sc.workers - 1) / sc.workers, static_cast<int64_t>(kMinShare + sc.toll));
+    int64_t share = total + sc.workers - 1;
+    share = share >> 32 ? share / sc.workers : static_cast<uint32_t>(share) / static_cast<uint32_t>(sc.workers);
+    share = max(share, static_cast<int64_t>(kMinShare + sc.toll));
     const int64_t start = worker * share;
     Segments seg0;
     seg0.left = max(min(share, total - start), static_cast<int64_t>(0));
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         }
     }
     if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[worker] = make_int4(-1, 0, 0, 0);
-    if (CL > 1) cluster_sync_all();  // the other CTA's barriers are initialised
-    else __syncthreads();
+    __syncthreads();
+    if (CL > 1) cluster_wait();  // so are the other CTA's
     seg0.u = plan[0];
     seg0.o = plan[1];
     const uint32_t tmem = static_cast<uint32_t>(plan[2]);
@@ -509,6 +512,24 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(q_ready);
         }
+        // this cluster's part of the units that see no key: zeros
+        for (int u = worker; u < units; u += sc.workers) {
+            const Unit w = unit_of(p, sc, u);
+            if (p.checked && rank == 0 && lane == 0 && w.c0 == 0) {
+                const int rows = p.q_indptr[w.b + 1] - w.r0, kv = p.kv_lens[w.b];
+                if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[w.b] > rows))
+                    set_err(p.err, PKV_ERRBIT_LEN);
+            }
+            if (w.tiles > 0) continue;
+            for (int c = w.c0 + rank * N; c < min(w.c0 + rank * N + N, w.cols); ++c) {
+                const int64_t at = static_cast<int64_t>(w.r0) * p.heads + c;
+                for (int d = lane * 4; d < kLatentDim; d += 128) {
+                    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kLatentDim + d) = make_float4(0, 0, 0, 0);
+                    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kLatentDim + d) = make_uint2(0, 0);
+                }
+                if (p.lse && lane == 0) p.lse[at] = -INFINITY;
+            }
+        }
         // do not leave with copies into this CTA's shared memory in flight
         if (nseg > 0) mbar_wait(q_ready, (nseg - 1) & 1);
     } else {
@@ -526,29 +547,6 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         int vfirst = 0;  // the tile's first value block in the ring
         int n = 0;
         int slot = 0;  // of a partial state: 0 for the share's first segment
-
-        // outputs of units that see no key: zeros
-        auto store_zeros = [&](const Unit& w) {
-            for (int c = 0; c < N; ++c) {
-                const int col = w.c0 + rank * N + c;
-                if (col >= w.cols) break;
-                const int64_t at = static_cast<int64_t>(w.r0) * p.heads + col;
-                const int d = (threadIdx.x & 127) * 4;
-                if (threadIdx.x >= 128) break;
-                if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * kLatentDim + d) = make_float4(0, 0, 0, 0);
-                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * kLatentDim + d) = make_uint2(0, 0);
-                if (p.lse && threadIdx.x == 0) p.lse[at] = -INFINITY;
-            }
-        };
-        for (int u = worker; u < units; u += sc.workers) {
-            const Unit w = unit_of(p, sc, u);
-            if (p.checked && rank == 0 && threadIdx.x == 0 && w.c0 == 0) {
-                const int rows = p.q_indptr[w.b + 1] - w.r0, kv = p.kv_lens[w.b];
-                if (kv > p.max_kv_len || kv < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[w.b] > rows))
-                    set_err(p.err, PKV_ERRBIT_LEN);
-            }
-            if (w.c0 < w.cols && w.tiles == 0) store_zeros(w);
-        }
 
         while (it.next(p, sc)) {
             const Unit& w = it.w;
@@ -763,8 +761,12 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 
     __syncwarp();
     tc_before_sync();
-    if (CL > 1) cluster_sync_all();  // the other CTA's copies and commits land here no more
-    else __syncthreads();
+    if (CL > 1) {  // the other CTA's copies and commits land here no more
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     tc_after_sync();
     if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
