@@ -112,9 +112,9 @@ struct RaggedParams {
     bool checked;
     int32_t* err;
 };
-// Tensor maps: k and v as {128, heads, keys}, k_pe as {64, keys}.
+// Tensor maps: k and v as {128, heads, keys}, k_pe as {64, keys}; with q_boxes q as {192, heads, rows}.
 cudaError_t launch_ragged_attn(const RaggedParams& p, const void* tmap_k, const void* tmap_pe, const void* tmap_v,
-                               cudaStream_t s);
+                               const void* tmap_q, bool q_boxes, cudaStream_t s);
 
 // Generic kernels (one warp a query row and head): a slow cross-check.
 cudaError_t launch_latent_simt(const LatentParams& p, cudaStream_t s);

@@ -295,7 +295,13 @@ pkv_status ragged_attention_latent(const void* q, int64_t q_token_stride, int64_
     if (m == PKV_OK) m = make_map(&tv, v, 3, kd, vs, box3);
     if (m == PKV_OK) m = make_map(&tp, k_pe, 2, pd, ps, box2);
     if (m != PKV_OK) return m;
-    return from_cuda(pkv::launch_ragged_attn(p, &tk, &tp, &tv, s), "ragged attention");
+    // queries as boxes of 128 rows, where their strides can stand in a tensor map
+    CUtensorMap tq = tk;
+    const int64_t qd[3] = {pkv::kExpandedQ, num_heads, kMaxCount};
+    const int64_t qs[2] = {num_heads == 1 ? int64_t(pkv::kExpandedQ) : q_head_stride, q_token_stride};
+    const bool boxes = qs[0] >= pkv::kExpandedQ && qs[1] >= pkv::kExpandedQ && qs[0] < kMaxStride && qs[1] < kMaxStride &&
+                       make_map(&tq, q, 3, qd, qs, box3) == PKV_OK;
+    return from_cuda(pkv::launch_ragged_attn(p, &tk, &tp, &tv, &tq, boxes, s), "ragged attention");
 }
 
 }  // extern "C"

@@ -62,7 +62,8 @@ __device__ __forceinline__ ValueSlots value_slots(int j) {
 
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_pe,
-                       const __grid_constant__ CUtensorMap tm_v, const RaggedParams p) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                       const RaggedParams p, const bool q_boxes) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     const int h = blockIdx.y, b = blockIdx.z;
@@ -88,6 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     g.key_hi = row_limit(p, g, min(g.t0 + 2 * kRows, g.nrows) - 1);
     const int nt = max(g.nt[0], g.nt[1]);
 
+    auto whole_tile = [&](int x) { return q_boxes && g.t0 + (x + 1) * kRows <= g.nrows; };
+
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
     uint64_t* q_ready = bars;
     uint64_t* k_full = bars + 1;      // [2], by tile parity
@@ -101,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kSlotOff + 4);
     if (threadIdx.x == 0) {
-        mbar_init(q_ready, 2 * kRows);
+        mbar_init(q_ready, (whole_tile(0) ? 1 : kRows) + (whole_tile(1) ? 1 : kRows));
         for (int x = 0; x < 2; ++x) {
             mbar_init(&k_full[x], 1);
             mbar_init(&k_empty[x], 1);
@@ -142,6 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tm_v);
             auto at = [&](int s) { return smem + kRingOff + s * kBlock; };
             int nk = 0, nv = 0;
+            // a row tile that lies whole inside the sequence: three boxes
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (nt == 0 || !whole_tile(x)) continue;
+                mbar_arrive_expect_tx(q_ready, kQTile);
+                for (int c = 0; c < 3; ++c)
+                    tma_load_3d(smem + x * kQTile + c * kBlock, &tm_q, q_ready, c * 64, h, g.r0 + g.t0 + x * kRows);
+            }
             for (int j = 0; j < nt; ++j) {
                 const int key = g.k0 + j * kKeys, x = j & 1;
                 const uint32_t again = ((j >> 1) & 1) ^ 1;  // the phase that tile j - 2 completed
@@ -161,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // do not leave with copies into this CTA's shared memory in flight
             for (int j = max(0, nk - 2); j < nk; ++j) mbar_wait(&k_full[j & 1], (j >> 1) & 1);
             for (int j = max(0, nv - 2); j < nv; ++j) mbar_wait(&v_full[j & 1], (j >> 1) & 1);
+            if (nt > 0) mbar_wait(q_ready, 0);
         }
     } else if (warp == kMmaWarp) {
         // =============================== MMA ================================
@@ -169,53 +181,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdescO = tc_idesc(kRows, kExpandedV, false, true);
             const uint64_t dq = tc_desc(sbase, 16, 1024, 128), dk = tc_desc(sbase + kRingOff, 16, 1024, 128);
             bool ok = nt == 0 || wait(q_ready, 0);
-            auto scores = [&](int x, int j) {
+            auto scores = [&](int x, int j, auto&& mid) {
                 tc_after_sync();
                 const uint64_t da = dq + x * (kQTile >> 4);
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
                     const uint64_t db = dk + ((5 * j + c) & 7) * (kBlock >> 4);
+                    if (c == 2) mid();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma(tmem + x * 256, da + ((c * kBlock + kk * 32) >> 4), db + 2 * kk, kIdescS, c + kk > 0);
                 }
                 tc_commit(&s_full[x]);
             };
-            auto values = [&](int x, int j) {
+            auto values = [&](int x, int j, auto&& mid) {
                 tc_after_sync();
                 const ValueSlots vs = value_slots(j);
                 const uint64_t db = tc_desc(sbase + kRingOff + vs.lo * kBlock, (vs.hi - vs.lo) * kBlock, 1024, 128);
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys: 8 columns of packed P, 16 rows of V
+                for (int kk = 0; kk < kKeys / 16; ++kk) {  // 16 keys: 8 columns of packed P, 16 rows of V
+                    if (kk == 4) mid();
                     tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + kk * 8, db + kk * (2048 >> 4), kIdescO, j + kk > 0);
+                }
             };
+            // a copy's barrier is probed among the products before its use: a wait
+            // between two batches would leave the pipe idle
+            bool landed = false;
+            auto probe = [&](uint64_t* bar, uint32_t parity) { landed = mbar_test(bar, parity); };
+            auto settle = [&](uint64_t* bar, uint32_t parity) { return landed || wait(bar, parity); };
             if (ok && nt > 0) {
                 ok = wait(&k_full[0], 0);
-                if (g.nt[0] > 0) scores(0, 0);
-                if (g.nt[1] > 0) scores(1, 0);
+                if (g.nt[0] > 0) scores(0, 0, [] {});
+                if (g.nt[1] > 0) scores(1, 0, [] {});
                 tc_commit(&k_empty[0]);
+                probe(&v_full[0], 0);
             }
             for (int j = 0; ok && j < nt; ++j) {
                 const uint32_t ph = (j >> 1) & 1, ph1 = ((j + 1) >> 1) & 1;
                 const int x1 = (j + 1) & 1;
-                bool k_next = false;
+                bool fresh = true;  // the step's first tile: its V_j, then its K_{j+1} may not have landed
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (!ok || j >= g.nt[x]) continue;
-                    ok = wait(&p_full[x], j & 1) && wait(&v_full[j & 1], ph);
+                    ok = (!fresh || settle(&v_full[j & 1], ph)) && wait(&p_full[x], j & 1);
                     if (!ok) break;
-                    values(x, j);
+                    values(x, j, [&] {
+                        if (fresh && j + 1 < nt) probe(&k_full[x1], ph1);
+                    });
+                    if (x == 1 || j >= g.nt[1]) tc_commit(&v_empty[j & 1]);
                     if (j + 1 < g.nt[x]) {
-                        if (x == 1) tc_commit(&v_empty[j & 1]);
-                        ok = k_next || wait(&k_full[x1], ph1);
-                        k_next = true;
-                        if (ok) scores(x, j + 1);
+                        ok = !fresh || settle(&k_full[x1], ph1);
+                        fresh = false;
+                        if (ok) scores(x, j + 1, [&] {
+                            if (x == 1 || j + 1 >= g.nt[1]) probe(&v_full[x1], ph1);
+                        });
                     } else {
                         tc_commit(&o_full[x]);
-                        if (x == 1) tc_commit(&v_empty[j & 1]);
                     }
                 }
-                if (j >= g.nt[1]) tc_commit(&v_empty[j & 1]);
                 if (j + 1 < nt) tc_commit(&k_empty[x1]);
             }
             // nothing of this thread's still runs in the tensor pipe when the CTA
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool exists = i < g.nrows;
         const int limit = row_limit(p, g, i);
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 256, o_addr = s_addr + 128;
-        if (g.nt[x] > 0 || nt > 0) {
+        if (nt > 0 && !whole_tile(x)) {
             // 24 chunks a row; eight lanes take one row's neighbouring chunks together
             const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(g.r0) * p.q_token_stride +
                                         static_cast<int64_t>(h) * p.q_head_stride;
@@ -358,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_ragged_attn(const RaggedParams& p, const void* tmap_k, const void* tmap_pe, const void* tmap_v,
-                               cudaStream_t s) {
+                               const void* tmap_q, bool q_boxes, cudaStream_t s) {
     static DeviceOnce opted;
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -372,7 +395,8 @@ cudaError_t launch_ragged_attn(const RaggedParams& p, const void* tmap_k, const 
     const dim3 grid(static_cast<unsigned>((p.max_q_rows + int64_t(2 * kRows) - 1) / (2 * kRows)), p.heads, p.batch);
     ragged_attn_kernel<<<grid, kThreads, kSmemBytes, s>>>(*static_cast<const CUtensorMap*>(tmap_k),
                                                           *static_cast<const CUtensorMap*>(tmap_pe),
-                                                          *static_cast<const CUtensorMap*>(tmap_v), p);
+                                                          *static_cast<const CUtensorMap*>(tmap_v),
+                                                          *static_cast<const CUtensorMap*>(tmap_q), p, q_boxes);
     return cudaGetLastError();
 }
 
