@@ -596,21 +596,29 @@ def _vector(t, name, dtype, count):
         raise ValueError(f"{name} must be dense {dtype} with room for {count}")
 
 
-def _row_strides(shape, st, width):
-    """Token and head stride of a [tokens, heads, width] tensor; axes of one
-    element take the dense stride (theirs may say anything)."""
-    head = st[1] if shape[1] > 1 else width
-    return (st[0] if shape[0] > 1 else head * shape[1]), head
+def _heads(t, name, rows, heads, width):
+    """Token and head stride of a bf16 [rows, heads, width] tensor with unit last
+    stride (rows or heads None: any); axes of one element take the dense stride,
+    as theirs may say anything.  Also its rows and heads."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not _BF16 or len(shape) != 3 or st[2] != 1:
+        raise ValueError(f"{name} must be bf16 [rows, heads, {width}] with unit last stride")
+    n, h, w = shape
+    if w != width or (rows is not None and n != rows) or (heads is not None and h != heads):
+        raise ValueError(f"{name} must have the shape [{rows or 'rows'}, {heads or 'heads'}, {width}]")
+    head = st[1] if h > 1 else width
+    return st[0] if n > 1 else head * h, head, n, h
 
 
 def _latent_pool(pool):
-    """Pages and page stride of a latent pool."""
+    """Pages, page size and page stride of a latent pool."""
     shape, st = pool.shape, pool.stride()
-    if pool.dtype is not _BF16 or len(shape) != 3 or shape[2] != LATENT_DIM + LATENT_ROPE:
-        raise ValueError("the pool must be bf16 [num_pages, page_size, 512 + 64]")
-    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
-        raise ValueError("pool slots must be dense")
-    return shape[0], shape[1], st[0] if shape[0] > 1 else shape[1] * shape[2]
+    if pool.dtype is not _BF16 or len(shape) != 3 or st[2] != 1:
+        raise ValueError("the pool must be bf16 [num_pages, page_size, 512 + 64] with unit last stride")
+    n, P, row = shape
+    if row != LATENT_DIM + LATENT_ROPE or (P > 1 and st[1] != row):
+        raise ValueError("the pool must hold dense slots of 512 + 64")
+    return n, P, st[0] if n > 1 else P * row
 
 
 def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, kv_lens_out, num_free_out, q_indptr,
@@ -649,32 +657,29 @@ def kv_append_latent(src, positions, cos_sin, slots, pool, *, norm_weight=None, 
     ``norm_weight``), rotate ``src[:, 512:]`` and write the rows into pool slots
     ``slots``; rotate ``q_pe [T, H, 64]`` into ``q_out`` (see ``include/pkv.h``)."""
     n, P, page_stride = _latent_pool(pool)
-    shape, st = src.shape, src.stride()
-    if src.dtype is not _BF16 or len(shape) != 2 or shape[1] != LATENT_DIM + LATENT_ROPE or st[1] != 1:
+    st = src.stride()
+    T, row = src.shape
+    if src.dtype is not _BF16 or row != LATENT_DIM + LATENT_ROPE or st[1] != 1:
         raise ValueError("src must be bf16 [tokens, 512 + 64] with unit last stride")
-    T, heads, qs, os = shape[0], 0, (0, 0), (0, 0)
     _vector(positions, "positions", _I64, T)
     _vector(slots, "slots", _I64, T)
-    if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or cos_sin.shape[1] != LATENT_ROPE or not cos_sin.is_contiguous():
+    table = cos_sin.shape
+    if cos_sin.dtype is not _F32 or len(table) != 2 or table[1] != LATENT_ROPE or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be dense float32 [max_position, 64]")
     if norm_weight is not None:
         _vector(norm_weight, "norm_weight", _BF16, LATENT_DIM)
-    if (q_pe is None) != (q_out is None):
+    qt = qh = ot = oh = heads = 0
+    if q_pe is not None and q_out is not None:
+        qt, qh, _, heads = _heads(q_pe, "q_pe", T, None, LATENT_ROPE)
+        ot, oh, _, _ = _heads(q_out, "q_out", T, heads, LATENT_ROPE)
+    elif q_pe is not None or q_out is not None:
         raise ValueError("q_pe and q_out come together")
-    if q_pe is not None:
-        for t in (q_pe, q_out):
-            if t.dtype is not _BF16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != LATENT_ROPE or t.stride(2) != 1:
-                raise ValueError("q_pe and q_out must be bf16 [tokens, heads, 64] with unit last stride")
-        if q_out.shape != q_pe.shape:
-            raise ValueError("q_pe and q_out must have the same shape")
-        heads = q_pe.shape[1]
-        qs, os = _row_strides(q_pe.shape, q_pe.stride(), LATENT_ROPE), _row_strides(q_out.shape, q_out.stride(), LATENT_ROPE)
     _scratch(None, err)
     dev = _on_device((src, positions, cos_sin, slots, pool, norm_weight, q_pe, q_out, err))
     status = lib().kv_append_latent(
-        src.data_ptr(), st[0] if T > 1 else shape[1], T, _address(norm_weight), eps, positions.data_ptr(),
-        cos_sin.data_ptr(), cos_sin.shape[0], int(interleaved), slots.data_ptr(), pool.data_ptr(), n, P, page_stride,
-        LATENT_DIM, LATENT_ROPE, _address(q_pe), qs[0], qs[1], _address(q_out), os[0], os[1], heads,
+        src.data_ptr(), st[0] if T > 1 else row, T, _address(norm_weight), eps, positions.data_ptr(),
+        cos_sin.data_ptr(), table[0], interleaved, slots.data_ptr(), pool.data_ptr(), n, P, page_stride,
+        LATENT_DIM, LATENT_ROPE, _address(q_pe), qt, qh, _address(q_out), ot, oh, heads,
         PKV_FLAG_CHECKED if checked else 0, _address(err), _launch_stream(stream, dev))
     if status:
         _check("kv_append_latent", status)
@@ -685,16 +690,11 @@ def paged_attention_latent_workspace_size(batch, max_q_rows, num_heads, max_kv_l
                                                            LATENT_ROPE, flags))
 
 
-def _wide_states(q, out, lse, width, value):
-    """Token and head stride of packed query rows of ``width`` whose outputs have ``value`` elements."""
-    shape = q.shape
-    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != width or q.stride(2) != 1:
-        raise ValueError(f"q must be bf16 [rows, num_heads, {width}] with unit last stride")
-    if out.shape != (shape[0], shape[1], value) or not out.is_contiguous() or out.dtype not in _DTYPES:
-        raise ValueError(f"out must be dense bf16 or float32 [rows, num_heads, {value}]")
-    if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
+def _outputs(out, lse, rows, heads, width):
+    if out.shape != (rows, heads, width) or not out.is_contiguous() or out.dtype not in _DTYPES:
+        raise ValueError(f"out must be dense bf16 or float32 [rows, num_heads, {width}]")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise ValueError("lse must be dense float32 [rows, num_heads]")
-    return _row_strides(shape, q.stride(), width)
 
 
 def paged_attention_latent(q, pool, block_table, kv_lens, q_indptr, out, *, q_real=None, lse=None, batch=None,
@@ -703,14 +703,15 @@ def paged_attention_latent(q, pool, block_table, kv_lens, q_indptr, out, *, q_re
     """Attention of absorbed queries ``q [rows, H, 512 + 64]`` over the latent
     rows of ``pool``, into ``out [rows, H, 512]`` (bf16 or f32) and ``lse``."""
     n, P, page_stride = _latent_pool(pool)
-    st = _wide_states(q, out, lse, LATENT_DIM + LATENT_ROPE, LATENT_DIM)
+    qt, qh, rows, heads = _heads(q, "q", None, None, LATENT_DIM + LATENT_ROPE)
+    _outputs(out, lse, rows, heads, LATENT_DIM)
     batch, table_stride = _tables(block_table, kv_lens, q_indptr, q_real, batch, max_kv_len)
     _scratch(workspace, err)
     mask = _mask(mask)
     dev = _on_device((q, pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err))
     status = lib().paged_attention_latent(
-        q.data_ptr(), st[0], st[1], pool.data_ptr(), n, P, page_stride, block_table.data_ptr(), table_stride,
-        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, q.shape[1],
+        q.data_ptr(), qt, qh, pool.data_ptr(), n, P, page_stride, block_table.data_ptr(), table_stride,
+        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, heads,
         LATENT_DIM, LATENT_ROPE, mask, scale, out.data_ptr(), _dtype(out), _address(lse), _address(workspace),
         _bytes(workspace), flags, _address(err), _launch_stream(stream, dev))
     if status:
@@ -722,12 +723,12 @@ def ragged_attention_latent(q, k, k_pe, v, q_indptr, kv_indptr, out, *, lse=None
     """Attention of ``q [rows, H, 128 + 64]`` over ragged expanded keys ``k
     [keys, H, 128]`` with the shared ``k_pe [keys, 64]`` and values ``v [keys, H,
     128]``, into ``out [rows, H, 128]`` (bf16 or f32) and ``lse``."""
-    st = _wide_states(q, out, lse, NOPE_DIM + LATENT_ROPE, EXPANDED_V)
-    heads, keys = q.shape[1], k.shape[0]
-    for t, shape in ((k, (keys, heads, NOPE_DIM)), (v, (keys, heads, EXPANDED_V)), (k_pe, (keys, LATENT_ROPE))):
-        if t.dtype is not _BF16 or t.shape != shape or t.stride(-1) != 1:
-            raise ValueError("k, v and k_pe must be bf16 [keys, num_heads, 128], the same and [keys, 64], unit last stride")
-    ks, vs = _row_strides(k.shape, k.stride(), NOPE_DIM), _row_strides(v.shape, v.stride(), EXPANDED_V)
+    qt, qh, rows, heads = _heads(q, "q", None, None, NOPE_DIM + LATENT_ROPE)
+    _outputs(out, lse, rows, heads, EXPANDED_V)
+    kt, kh, keys, _ = _heads(k, "k", None, heads, NOPE_DIM)
+    vt, vh, _, _ = _heads(v, "v", keys, heads, EXPANDED_V)
+    if k_pe.dtype is not _BF16 or k_pe.shape != (keys, LATENT_ROPE) or k_pe.stride(1) != 1:
+        raise ValueError("k_pe must be bf16 [keys, 64] with unit last stride")
     if batch is None:
         batch = q_indptr.numel() - 1
     _vector(q_indptr, "q_indptr", _I32, batch + 1)
@@ -736,8 +737,8 @@ def ragged_attention_latent(q, k, k_pe, v, q_indptr, kv_indptr, out, *, lse=None
     mask = _mask(mask)
     dev = _on_device((q, k, k_pe, v, q_indptr, kv_indptr, out, lse, err))
     status = lib().ragged_attention_latent(
-        q.data_ptr(), st[0], st[1], k.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), k_pe.stride(0) if keys > 1 else LATENT_ROPE,
-        v.data_ptr(), vs[0], vs[1], keys, q_indptr.data_ptr(), kv_indptr.data_ptr(), batch, max_q_rows, max_kv_len, heads,
+        q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, k_pe.data_ptr(), k_pe.stride(0) if keys > 1 else LATENT_ROPE,
+        v.data_ptr(), vt, vh, keys, q_indptr.data_ptr(), kv_indptr.data_ptr(), batch, max_q_rows, max_kv_len, heads,
         NOPE_DIM, LATENT_ROPE, EXPANDED_V, mask, scale, out.data_ptr(), _dtype(out), _address(lse), flags, _address(err),
         _launch_stream(stream, dev))
     if status:
