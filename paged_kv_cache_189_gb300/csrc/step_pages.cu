@@ -46,12 +46,25 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
 
 __device__ __forceinline__ int64_t pages_of(int64_t keys) { return (keys + 31) >> 5; }
 
+// The first index whose running sum lies past v (the last one has one that does).
+__device__ __forceinline__ int upper(const int32_t* ends, int count, int v) {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > v) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
 __global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArgs a) {
-    // per sequence: end of its tokens, first page number it takes (or gives back), keys before the step
+    // per sequence, running sums up to and with it: granted tokens, pages taken, pages
+    // given back; and its keys before the step
     extern __shared__ int32_t state[];
     int32_t* tok_end = state;
-    int32_t* page_at = state + a.batch;
-    int32_t* kv_of = state + 2 * a.batch;
+    int32_t* take_end = state + a.batch;
+    int32_t* back_end = state + 2 * a.batch;
+    int32_t* kv_of = state + 3 * a.batch;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
     const int tid = threadIdx.x;
@@ -93,20 +106,19 @@ __global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArg
         take[k] = 0;
         const int b = tid * per + k;
         if (k >= per || b >= a.batch) continue;
-        if (ask[k] < 0) {
-            page_at[b] = static_cast<int32_t>(back_sum);
-            back_sum += min(pages_of(kv[k]), stride);
-        } else if (ask[k] > 0) {
-            const int64_t n = pages_of(int64_t(kv[k]) + ask[k]) - pages_of(kv[k]);
-            token_sum += ask[k];
-            need_sum += n;
-            const bool room = token_sum <= a.max_tokens && pages_of(int64_t(kv[k]) + ask[k]) <= stride;
-            if (!room) bad |= PKV_ERRBIT_LEN;
-            if (room && (n == 0 || need_sum <= top)) take[k] = static_cast<int>(n);
-            else ask[k] = 0;
-            took += take[k];
-            granted += ask[k];
-        }
+        if (ask[k] < 0) back_sum += min(pages_of(kv[k]), stride);
+        back_end[b] = static_cast<int32_t>(min(back_sum, a.free_capacity));  // (what lies past it is dropped)
+        kv_of[b] = kv[k];
+        if (ask[k] <= 0) continue;
+        const int64_t n = pages_of(int64_t(kv[k]) + ask[k]) - pages_of(kv[k]);
+        token_sum += ask[k];
+        need_sum += n;
+        const bool room = token_sum <= a.max_tokens && pages_of(int64_t(kv[k]) + ask[k]) <= stride;
+        if (!room) bad |= PKV_ERRBIT_LEN;
+        if (room && (n == 0 || need_sum <= top)) take[k] = static_cast<int>(n);
+        else ask[k] = 0;
+        took += take[k];
+        granted += ask[k];
     }
     int64_t took_total, granted_total;
     int64_t took_sum = block_scan(took, &took_total);
@@ -115,63 +127,66 @@ __global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArg
     for (int k = 0; k < kMaxPer; ++k) {
         const int b = tid * per + k;
         if (k >= per || b >= a.batch) continue;
-        if (ask[k] >= 0) page_at[b] = static_cast<int32_t>(took_sum);
         took_sum += take[k];
         token_end += max(ask[k], 0);
+        take_end[b] = static_cast<int32_t>(took_sum);
         tok_end[b] = static_cast<int32_t>(token_end);
-        kv_of[b] = ask[k] < 0 ? -1 - kv[k] : kv[k];  // finished: below zero
+        if (rank == 0) {
+            // (the inputs, which these may be, are read by every CTA before the barrier below)
+            kv[k] = ask[k] < 0 ? 0 : kv[k] + ask[k];
+        }
     }
     if (bad && rank == 0) set_err(a.err, bad);
     __syncthreads();
 
-    // finished sequences' pages onto the stack, a warp a sequence
-    const int lane = tid & 31;
-    const int wid = rank * (kThreads / 32) + (tid >> 5), warps = ranks * (kThreads / 32);
-    if (back_total > 0) {
-        for (int b = wid; b < a.batch; b += warps) {
-            if (kv_of[b] >= 0) continue;
-            const int64_t held = min(pages_of(-1 - int64_t(kv_of[b])), stride);
-            for (int64_t i = lane; i < held; i += 32)
-                if (height + page_at[b] + i < a.free_capacity)
-                    a.free_pages[height + page_at[b] + i] = a.block_table[b * stride + i];
+    // what is done page by page or token by token is shared out over the cluster's
+    // threads, each finding its sequence in the running sums
+    const int first = rank * kThreads + tid, step = ranks * kThreads;
+    const int pushed = static_cast<int>(top - height);
+    if (pushed > 0) {
+        for (int n = first; n < pushed; n += step) {
+            const int b = upper(back_end, a.batch, n);
+            a.free_pages[height + n] = a.block_table[b * stride + n - (b > 0 ? back_end[b - 1] : 0)];
         }
         __threadfence();
     }
     cluster.sync();
 
     // page number n of those taken lies n below the top
-    auto stack_page = [&](int64_t n) { return a.free_pages[top - 1 - n]; };
-    if (took_total > 0) {
-        for (int b = wid; b < a.batch; b += warps) {
-            if (kv_of[b] < 0) continue;
-            const int64_t held = pages_of(kv_of[b]);
-            const int64_t new_keys = int64_t(tok_end[b]) - (b > 0 ? tok_end[b - 1] : 0);
-            const int64_t count = pages_of(kv_of[b] + new_keys) - held;
-            for (int64_t i = lane; i < count; i += 32) a.block_table[b * stride + held + i] = stack_page(page_at[b] + i);
-        }
+    auto stack_page = [&](int n) { return a.free_pages[top - 1 - n]; };
+    for (int n = first; n < took_total; n += step) {
+        const int b = upper(take_end, a.batch, n);
+        a.block_table[b * stride + pages_of(kv_of[b]) + n - (b > 0 ? take_end[b - 1] : 0)] = stack_page(n);
     }
-    for (int64_t t = rank * kThreads + tid; t < a.max_tokens; t += ranks * kThreads) {
-        int64_t pos = 0, slot = -1;
-        if (t < granted_total) {
-            int lo = 0, hi = a.batch - 1;  // the first sequence whose tokens end past t
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (tok_end[mid] > t) hi = mid;
-                else lo = mid + 1;
-            }
-            pos = int64_t(kv_of[lo]) + t - (lo > 0 ? tok_end[lo - 1] : 0);
-            const int64_t lp = pos >> 5, held = pages_of(kv_of[lo]);
-            const int64_t page = lp < held ? a.block_table[lo * stride + lp] : stack_page(page_at[lo] + lp - held);
-            slot = page * 32 + (pos & 31);
+    constexpr int kAtOnce = 4;  // tokens whose look-ups are under way together
+    for (int64_t t0 = first; t0 < a.max_tokens; t0 += static_cast<int64_t>(kAtOnce) * step) {
+        int page[kAtOnce], pos[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t t = t0 + static_cast<int64_t>(k) * step;
+            page[k] = -1;
+            pos[k] = 0;
+            if (t >= granted_total) continue;
+            const int b = upper(tok_end, a.batch, static_cast<int>(t));
+            pos[k] = kv_of[b] + static_cast<int>(t) - (b > 0 ? tok_end[b - 1] : 0);
+            const int lp = pos[k] >> 5, held = static_cast<int>(pages_of(kv_of[b]));
+            page[k] = lp < held ? a.block_table[b * stride + lp] : stack_page((b > 0 ? take_end[b - 1] : 0) + lp - held);
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t t = t0 + static_cast<int64_t>(k) * step;
+            if (t >= a.max_tokens) break;
+            a.slots[t] = t < granted_total ? static_cast<int64_t>(page[k]) * 32 + (pos[k] & 31) : -1;
+            a.positions[t] = pos[k];
+        }
     }
     if (rank == 0) {
-        for (int b = tid; b < a.batch; b += kThreads) {
-            const int end = tok_end[b], begin = b > 0 ? tok_end[b - 1] : 0;
-            a.q_indptr[b + 1] = end;
-            a.kv_lens_out[b] = kv_of[b] < 0 ? 0 : kv_of[b] + (end - begin);
+#pragma unroll
+        for (int k = 0; k < kMaxPer; ++k) {
+            const int b = tid * per + k;
+            if (k >= per || b >= a.batch) continue;
+            a.q_indptr[b + 1] = tok_end[b];
+            a.kv_lens_out[b] = kv[k];
         }
         if (tid == 0) {
             a.q_indptr[0] = 0;
@@ -192,17 +207,17 @@ cudaError_t launch_step_pages(const StepPagesArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(wide ? kCluster : 1);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.batch) * 12;
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.batch) * 16;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    static DeviceOnce opted;  // 4096 sequences take 48 KB beside the scans' parts
+    static DeviceOnce opted;  // 4096 sequences take 64 KB
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = opted.get(dev, &done, [&](int, int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(step_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 12);
+        return cudaFuncSetAttribute(step_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 16);
     });
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, step_pages_kernel, a);
