@@ -797,9 +797,10 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
  *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . key_j) v[j, h, :]
  *   lse[r, h]    = ln sum_j exp(scale * q[r, h] . key_j)
  * over the visible keys (PKV_MASK_NONE: all; PKV_MASK_CAUSAL: j <= kv - rows + i).
- * Rows that see no key: out = 0, lse = -inf.  Rounding, masked scores and NaN as
- * in paged_attention_latent; V rows of keys that no row of the call sees may
- * hold anything.  out and lse are joined with those over a cached prefix by
+ * Rows that see no key: out = 0, lse = -inf.  The softmax weights are rounded once
+ * to bf16 before the product with the values (2^-8 relative at most) and summed
+ * unrounded; masked scores and NaN as in paged_attention_latent; V rows of keys
+ * that no row of the call sees may hold anything.  out and lse are joined with those over a cached prefix by
  * merge_attn_states.
  *
  *  q              device bf16, element (r, h, d) at r * q_token_stride + h *

@@ -147,15 +147,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// acc += the two bf16 values of a packed pair, each widened exactly to f32
-__device__ __forceinline__ void add_pair(float2& acc, uint32_t pk) {
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "mov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.bf16 %0, lo, %0;\n\t"
-        "add.rn.f32.bf16 %1, hi, %1;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y) : "r"(pk));
-}
-
 // 16 bytes global -> shared without registers; zeros where `valid` is false
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
