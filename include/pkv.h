@@ -713,7 +713,7 @@ pkv_status assign_step_pages(const int32_t* new_lens, const int32_t* kv_lens,
  * A pair (a, b) becomes (a cos - b sin, b cos + a sin) with cos = cos_sin[
  * position][i], sin = cos_sin[position][rope_dim / 2 + i] for pair i: elements
  * (i, i + rope_dim / 2), or (2 i, 2 i + 1) with `interleaved`, in place.  All in
- * f32, rounded to bf16 once.
+ * f32, rounded to bf16 once.  Two tokens with one slot race, as in kv_scatter_slots.
  *
  *  src           device bf16, row t at t * src_stride
  *  norm_weight   device bf16 [latent_dim] or NULL
@@ -767,7 +767,9 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
  *  out            device [rows][num_heads][latent_dim], bf16 or f32 (dense)
  *  workspace      paged_attention_latent_workspace_size(...) bytes, 256-byte
  *                 aligned; one workspace must not serve two calls in flight
- *  max_q_rows * num_heads, max_kv_len  at most 2^31 - 256
+ *  max_q_rows * num_heads, max_kv_len  at most 2^31 - 256, batch 65535, and
+ *                 batch * ceil(max_q_rows * num_heads / 16) * (max_kv_len / 64 + 8)
+ *                 at most 2^36
  *  latent_dim 512, rope_dim 64, page_size 32
  *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY (a generic kernel without
  *                 a workspace)
@@ -811,6 +813,7 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
  *  num_keys       rows of k, k_pe and v; rows past it count as zeros
  *  max_q_rows, max_kv_len  HOST upper bounds per sequence (rows and keys beyond
  *                 them are not attended: longer rows stay unwritten)
+ *                 max_q_rows * num_heads and num_keys at most 2^31 - 256
  *  scale          > 0 and finite
  *  out            device [rows][num_heads][v_dim], bf16 or f32 (dense)
  *  nope_dim 128, rope_dim 64, v_dim 128; pointers 16-byte aligned, strides

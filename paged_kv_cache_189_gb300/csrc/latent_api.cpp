@@ -82,6 +82,14 @@ int device_sms() {
     return sms;
 }
 
+// What paged_attention_latent counts in 32 bits: columns of a sequence, column
+// groups of the call, and a cluster's share of the key tiles.
+bool counts_ok(int batch, int max_q_rows, int num_heads, int max_kv_len) {
+    if (max_kv_len > kMaxCount || max_q_rows > kMaxCount / num_heads || batch > 65535) return false;
+    const int64_t groups = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_q_rows) * num_heads + 15) / 16);
+    return groups <= kMaxCount && groups * (max_kv_len / 64 + 8) <= (int64_t(1) << 36);
+}
+
 bool dims_ok(int latent_dim, int rope_dim) {
     return latent_dim == pkv::kLatentDim && rope_dim == pkv::kLatentRope;
 }
@@ -160,7 +168,7 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
 size_t paged_attention_latent_workspace_size(int batch, int max_q_rows, int num_heads, int max_kv_len, int latent_dim,
                                              int rope_dim, unsigned flags) {
     if (batch <= 0 || max_q_rows <= 0 || num_heads <= 0 || max_kv_len < 0 || !dims_ok(latent_dim, rope_dim) ||
-        (flags & PKV_FLAG_SIMT_ONLY) || max_q_rows > kMaxCount / num_heads)
+        (flags & PKV_FLAG_SIMT_ONLY) || !counts_ok(batch, max_q_rows, num_heads, max_kv_len))
         return 0;
     return pkv::plan_latent(batch, max_q_rows, num_heads, max_kv_len, device_sms()).ws_bytes;
 }
@@ -188,9 +196,8 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
         return fail(PKV_ERR_UNSUPPORTED, "latent attention: output dtype must be bf16 or f32");
     if (!(scale > 0.f) || std::isinf(scale))
         return fail(PKV_ERR_INVALID_ARG, "latent attention: scale must be finite and > 0");
-    if (max_kv_len > kMaxCount || max_q_rows > kMaxCount / num_heads || num_pages > kMaxCount || batch > 65535 ||
-        static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_q_rows) * num_heads + 15) / 16) > kMaxCount)
-        return fail(PKV_ERR_UNSUPPORTED, "latent attention: sizes above 2^31 - 256");
+    if (num_pages > kMaxCount || !counts_ok(batch, max_q_rows, num_heads, max_kv_len))
+        return fail(PKV_ERR_UNSUPPORTED, "latent attention: sizes above 2^31 - 256, or 2^36 tiles of 16 columns and 64 keys");
     if (max_kv_len > 0 && num_pages == 0) return fail(PKV_ERR_INVALID_ARG, "latent attention: a pool without pages");
     if (page_stride < 32 * pkv::kLatentRow || page_stride % 8)
         return fail(PKV_ERR_INVALID_ARG, "latent attention: page_stride must cover a page, a multiple of 8");
@@ -213,7 +220,7 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (flags & PKV_FLAG_SIMT_ONLY) return from_cuda(pkv::launch_latent_simt(p, s), "latent attention (simt)");
     const pkv::LatentPlan pl = pkv::plan_latent(batch, max_q_rows, num_heads, max_kv_len, device_sms());
-    if (pl.ws_bytes > 0 && (!workspace || workspace_bytes < pl.ws_bytes || !aligned(workspace, 256)))
+    if (!workspace || workspace_bytes < pl.ws_bytes || !aligned(workspace, 256))
         return fail(PKV_ERR_WORKSPACE, "latent attention: workspace needs %zu bytes, 256-byte aligned", pl.ws_bytes);
     CUtensorMap tm;
     // (a call without keys needs no page: the map of one is never read through)
@@ -259,7 +266,7 @@ pkv_status ragged_attention_latent(const void* q, int64_t q_token_stride, int64_
     if (!(scale > 0.f) || std::isinf(scale))
         return fail(PKV_ERR_INVALID_ARG, "ragged attention: scale must be finite and > 0");
     if (batch > 65535 || num_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "ragged attention: batch or heads above 65535");
-    if (max_kv_len > kMaxCount || max_q_rows > kMaxCount || num_keys > kMaxCount)
+    if (max_kv_len > kMaxCount || max_q_rows > kMaxCount / num_heads || num_keys > kMaxCount)
         return fail(PKV_ERR_UNSUPPORTED, "ragged attention: sizes above 2^31 - 256");
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_pe, 16) || !aligned(v, 16) || !aligned(out, 16) ||
         (lse && !aligned(lse, 4)) || !stride_ok(q_token_stride) || !stride_ok(q_head_stride) ||

@@ -39,6 +39,7 @@ ATTN_D = dict(q=FAKE, qts=16 * 576, qhs=576, pool=FAKE, pages=10, ps=32, pst=32 
     (dict(pages=0), BAD), (dict(pst=32 * 576 - 8), BAD), (dict(pst=32 * 576 + 4), BAD), (dict(q=ODD), BAD), (dict(pool=ODD), BAD),
     (dict(out=ODD), BAD), (dict(qts=12), BAD), (dict(qhs=-8), BAD), (dict(bts=3), BAD), (dict(flags=1), BAD), (dict(flags=4), UNS),
     (dict(flags=0x10), UNS), (dict(mk=2 ** 31 - 1, bts=2 ** 27), UNS), (dict(mq=2 ** 31 - 1), UNS), (dict(batch=70000), UNS),
+    (dict(batch=60000, mk=2 ** 27, bts=2 ** 22), UNS), (dict(ws=FAKE, wsb=100), WS), (dict(), WS), (dict(ws=ODD, wsb=1 << 30), WS),
     (dict(kl=ODD), BAD), (dict(batch=0), 0), (dict(mq=0), 0), (dict(h=0), 0)])
 def test_attention(L, kw, status):
     assert call(L.paged_attention_latent, ATTN, ATTN_D, **kw) == status
@@ -55,7 +56,7 @@ RAG_D = dict(q=FAKE, qts=16 * 192, qhs=192, k=FAKE, kts=16 * 256, khs=256, pe=FA
     (dict(k=None), BAD), (dict(pe=None), BAD), (dict(v=None), BAD), (dict(ki=None), BAD), (dict(out=None), BAD), (dict(mask=2), UNS),
     (dict(mask=9), BAD), (dict(odt=1), UNS), (dict(scale=0.0), BAD), (dict(scale=NAN), BAD), (dict(scale=INF), BAD),
     (dict(k=ODD), BAD), (dict(kts=12), BAD), (dict(vhs=-8), BAD), (dict(pes=4), BAD), (dict(flags=1), BAD), (dict(flags=8), UNS),
-    (dict(batch=70000), UNS), (dict(h=70000), UNS), (dict(mk=2 ** 31 - 1), UNS), (dict(n=2 ** 33), UNS),
+    (dict(batch=70000), UNS), (dict(h=70000), UNS), (dict(mk=2 ** 31 - 1), UNS), (dict(n=2 ** 33), UNS), (dict(mq=2 ** 28), UNS),
     (dict(kts=1 << 40), UNS), (dict(qi=ODD), BAD), (dict(batch=0), 0), (dict(mq=0), 0), (dict(h=0), 0)])
 def test_ragged(L, kw, status):
     assert call(L.ragged_attention_latent, RAG, RAG_D, **kw) == status
@@ -94,6 +95,10 @@ def test_workspace_sizes(L):
     size = pkv.paged_attention_latent_workspace_size
     assert size(0, 1, 16, 100) == 0 and size(2, 1, 16, 100, flags=pkv.PKV_FLAG_SIMT_ONLY) == 0
     assert size(2, 2 ** 30, 16, 100) == 0       # more columns than a call takes
+    assert size(60000, 1, 16, 2 ** 27) == 0     # more key tiles
+    # a partial state of a first and a last segment for every cluster, 16 columns of 512 f32 and their LSEs
+    assert 152 * 2 * 16 * 513 * 4 <= size(64, 1, 16, 8192) <= 152 * 2 * 16 * 513 * 4 + 8192
+    assert size(2, 1, 16, 60) < size(2, 1, 16, 6000)
     assert L.paged_attention_latent_workspace_size(2, 1, 16, 100, 256, 64, 0) == 0
 
 
