@@ -7,7 +7,10 @@
 // the latent row (two 16-byte chunks a lane, the sum of squares over the warp),
 // the others eight query heads each at a time, four lanes a head with two
 // 16-byte chunks each, so both elements of every pair, in either order of
-// pairs, are in one lane.
+// pairs, are in one lane.  Measured, replayed as a graph: 2.2 us for 64 tokens of
+// 16 heads; 19.8 us for 7.7 k tokens of 32 heads (82.6 MB: 0.61 of the copy rate,
+// in pieces of 128 bytes out of rows of 384 and 1152).  1216 to 3648 CTAs that walk
+// the tokens took 19.6 to 24.7 us.
 #include "latent.h"
 #include "pkv_common.cuh"
 

@@ -18,6 +18,14 @@
 // segment is a range of one unit's tiles) and leaves a partial state where a unit
 // was cut; a second launch joins those.
 //
+// What bounds it (64 sequences of 513-8193 keys, among others, us; floor = bytes at
+// the copy rate): 16 columns 66 (50): DRAM for ~55 of them, then 2.5 us before the
+// first copy, shares that end up to 4 us apart, 5 us launch and join; 64 columns 85
+// (53) and 128 on a cluster 107 (49): a tile's buffers are held through S^T, softmax
+// and O^T (~4000 cycles) and shared memory holds two tiles beside 64 columns of Q,
+// and each tile takes 36 x 32 + 16 x 48 = 1920 cycles of products (measured:
+// 64 x 64 x 16 products issue every 32 cycles, 128 x 64 x 16 every 48).
+//
 // Roles (one CTA an SM): four softmax and output warps (eight for 64 columns: the
 // softmax of a tile is part of the time its buffers are held), then the TMA
 // producer, the issuers of S^T and of O^T (a wait costs an issuing thread the time
@@ -38,9 +46,12 @@ constexpr int kBlock = 2 * kHalf;          // 64 keys x 128 dims
 constexpr int kBlocks = kLatentDim / 128;  // value blocks of a tile (the rotary half block is apart)
 constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
-constexpr int kNoPage = INT32_MIN;         // look-up past the last page: zeros, and no error
-constexpr int kMinShare = 2;               // tiles a cluster takes at least
-// What a segment costs beside its tiles (queries, first copies, outputs), in tiles
+constexpr int kNoPage = -2;                // look-up past the last page: zeros, and no error
+// Tiles a cluster takes at least: one sequence of 8192 keys takes 16.0 / 14.4 / 15.2 / 18.0
+// us with 1 / 2 / 4 / 8, four of 500-1500 keys 12.2 / 13.9 / 15.2 / 18.8, two short ones 8.7 with 2
+constexpr int kMinShare = 2;
+// What a segment costs beside its tiles (queries, first copies, outputs), in tiles.  With
+// 0 / 1 / 3 and 0 / 2 / 5: 68.1 / 67.6 / 67.5 us (16 columns), 88.1 / 84.8 / 84.5 (64), 111 / 107 / 109.5 (128)
 constexpr int kToll = 1, kTollWide = 2;
 
 // Shared memory: the queries, rings of value blocks and of rotary blocks, the
@@ -283,7 +294,9 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             Ring<D::kR> r;
             // The pages are looked up a tile ahead of their use, on across segments.
             // Where two tiles are all that shared memory holds, pages are asked for in
-            // L2 kAhead tiles before their copies.
+            // L2 kAhead tiles before their copies: 128 columns took 134.6 / 127.3 / 128.9 /
+            // 133.0 us with 0 / 1 / 2 / 4.  (Beside a deeper ring it only makes the queries'
+            // loads wait: 70 -> 80 us for 16 columns.)
             constexpr int kAhead = D::kAhead;
             int j = 0, last_page = 0;
             const int32_t* bt = nullptr;
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kPages; ++k) {
                     const int lp = 2 * j + (CL > 1 ? rank : k);
-                    ph[k] = lp < last_page ? bt[lp] : kNoPage;
+                    ph[k] = lp < last_page ? max(bt[lp], -1) : kNoPage;
                 }
                 ++j;
                 ++queued;
@@ -926,6 +939,10 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms) {
     LatentPlan pl{};
+    // The narrowest CTA that holds a sequence's columns, pairs of the widest beyond.  64
+    // sequences of 513-8193 keys, us: 16 columns in CTAs of 16 / 32 / 64: 66.6 / 70.1 / 75.2;
+    // 32 columns: 105.3 / 75.0 / 80.0; 64 columns: 187 / 114 / 85.3; 128 columns in CTAs of 64
+    // one by one / in clusters of two: 130 / 107.
     const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
     pl.cols = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
     pl.cluster = cols <= 64 ? 1 : 2;
