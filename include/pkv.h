@@ -766,7 +766,8 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
  *  scale          > 0 and finite (the wide latent rows give no default)
  *  out            device [rows][num_heads][latent_dim], bf16 or f32 (dense)
  *  workspace      paged_attention_latent_workspace_size(...) bytes, 256-byte
- *                 aligned; one workspace must not serve two calls in flight
+ *                 aligned, sized with the device current that the call will use;
+ *                 one workspace must not serve two calls in flight
  *  max_q_rows * num_heads, max_kv_len  at most 2^31 - 256, batch 65535, and
  *                 batch * ceil(max_q_rows * num_heads / 16) * (max_kv_len / 64 + 8)
  *                 at most 2^36
@@ -801,8 +802,9 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
  * over the visible keys (PKV_MASK_NONE: all; PKV_MASK_CAUSAL: j <= kv - rows + i).
  * Rows that see no key: out = 0, lse = -inf.  The softmax weights are rounded once
  * to bf16 before the product with the values (2^-8 relative at most) and summed
- * unrounded; masked scores and NaN as in paged_attention_latent; V rows of keys
- * that no row of the call sees may hold anything.  out and lse are joined with those over a cached prefix by
+ * unrounded; masked scores and NaN as in paged_attention_latent.  V rows of keys
+ * that no row of the call sees may hold anything; those that one query row sees and
+ * another of its sequence does not must be finite.  out and lse are joined with those over a cached prefix by
  * merge_attn_states.
  *
  *  q              device bf16, element (r, h, d) at r * q_token_stride + h *

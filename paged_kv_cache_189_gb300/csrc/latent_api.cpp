@@ -106,9 +106,11 @@ pkv_status assign_step_pages(const int32_t* new_lens, const int32_t* kv_lens, co
     if (batch < 0 || max_tokens < 0 || free_capacity < 0 || block_table_stride < 0)
         return fail(PKV_ERR_INVALID_ARG, "step pages: negative size");
     if (batch == 0) return ok();
-    if (!new_lens || !kv_lens || !num_free || !free_pages || !block_table || !kv_lens_out || !num_free_out || !q_indptr)
+    if (!new_lens || !kv_lens || !num_free || !kv_lens_out || !num_free_out || !q_indptr)
         return fail(PKV_ERR_INVALID_ARG, "step pages: null pointer");
-    if (max_tokens > 0 && (!slots || !positions)) return fail(PKV_ERR_INVALID_ARG, "step pages: null pointer");
+    if ((max_tokens > 0 && (!slots || !positions)) || (free_capacity > 0 && !free_pages) ||
+        (block_table_stride > 0 && !block_table))
+        return fail(PKV_ERR_INVALID_ARG, "step pages: null pointer");
     if (page_size != 32) return fail(PKV_ERR_UNSUPPORTED, "step pages: page_size %d (only 32-token pages)", page_size);
     if (batch > 4096) return fail(PKV_ERR_UNSUPPORTED, "step pages: batch %d (at most 4096)", batch);
     if (max_tokens > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "step pages: max_tokens above 2^30");

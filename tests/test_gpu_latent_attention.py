@@ -50,6 +50,20 @@ def test_score_ranges(H, growing, key_size):
     Case([700, 90, 300], [1, 2, 1], [1, 2, 1], H, growing=growing, key_size=key_size, seed=3).check()
 
 
+@pytest.mark.parametrize("H,real", [(256, [1, 1]), (192, [1, 2]), (8, [8, 16]), (4, [16, 5]), (2, [8, 3]), (64, [3, 1])])
+def test_whole_rows_of_heads(H, real):
+    """Head counts that divide a CTA's columns or are a multiple of them: queries as
+    boxes for full column groups, piece by piece for the last."""
+    Case([90, 200], real, real, H, seed=H, q_pad=1).check()
+    Case([90, 200], real, [r + 1 for r in real], H, seed=H + 1, lead=2).check(out_dtype=torch.float32)
+
+
+def test_padded_batch():
+    """Far more padding rows than real ones: zeros, however many."""
+    c = Case([40, 0, 300, 65], [2, 0, 1, 0], [150, 90, 200, 130], 16, seed=13)
+    c.check()
+
+
 @pytest.mark.parametrize("H", [16, 128])
 def test_long_sequence_shared_out(H):
     """One sequence over all SMs, and long beside short ones."""

@@ -107,6 +107,11 @@ def test_prompts_of_many_pages():
     check(new, kv, free, stack, table, tokens)
 
 
+def test_no_free_pages_at_all():
+    """An empty stack: only sequences with room in their last page go on."""
+    check([1, 1, 5, -1], [31, 32, 20, 0], 0, [], [[3, -1], [4, -1], [5, -1], [-1, -1]], 9)
+
+
 def test_stack_full_and_odd_counts():
     """Pages that do not fit the stack are dropped; counts outside it are clamped."""
     table = [[3, 4, 5], [6, 7, 8]]

@@ -84,7 +84,7 @@ PAG_D = dict(new=FAKE, kv=FAKE, nf=FAKE, fp=FAKE, cap=10, bt=FAKE, bts=4, batch=
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), BAD), (dict(mt=-1), BAD), (dict(cap=-1), BAD), (dict(bts=-1), BAD), (dict(new=None), BAD), (dict(fp=None), BAD),
-    (dict(ko=None), BAD), (dict(fo=None), BAD), (dict(qi=None), BAD), (dict(slots=None), BAD), (dict(pos=None), BAD),
+    (dict(bt=None), BAD), (dict(ko=None), BAD), (dict(fo=None), BAD), (dict(qi=None), BAD), (dict(slots=None), BAD), (dict(pos=None), BAD),
     (dict(ps=16), UNS), (dict(batch=4097), UNS), (dict(mt=2 ** 30 + 1), UNS), (dict(cap=2 ** 32), UNS), (dict(bts=2 ** 27), UNS),
     (dict(new=ctypes.c_void_p(0x1001)), BAD), (dict(slots=ctypes.c_void_p(0x1004)), BAD), (dict(batch=0), 0)])
 def test_step_pages(L, kw, status):
