@@ -81,6 +81,7 @@ struct LatentPlan {
     int cols, cluster;  // columns a CTA holds, CTAs that share their key tiles
     int workers;        // clusters of the launch
     int groups;         // column groups (cols * cluster) of a sequence, at the host bounds
+    bool whole;         // a cluster for every group, which then has no states to join
     size_t ws_bytes;
 };
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms);

@@ -53,6 +53,13 @@ constexpr int kMinShare = 2;
 // What a segment costs beside its tiles (queries, first copies, outputs), in tiles.  With
 // 0 / 1 / 3 and 0 / 2 / 5: 68.1 / 67.6 / 67.5 us (16 columns), 88.1 / 84.8 / 84.5 (64), 111 / 107 / 109.5 (128)
 constexpr int kToll = 1, kTollWide = 2;
+// Units of at most kWholeTiles tiles (at the host's bound) that all run at once go one
+// to a cluster, without shares and join, where that leaves no more than kIdleTiles of a
+// unit's time idle over all clusters.  Shares and join / one to a cluster, us: two
+// sequences of 128 / 256 / 512 / 1024 keys, 16 heads 8.6 / 7.2, 11.8 / 9.5, 12.1 / 13.0, 13.1 / 20.4,
+// 128 heads 11.6 / 10.2, 16.1 / 12.9, 17.6 / 18.1, 19.3 / 28.3; 64 sequences of half to all of
+// 512 / 1024 keys, 16 heads 19.2 / 15.3, 25.8 / 24.9, 128 heads 37.1 / 23.6, 46.7 / 33.7
+constexpr int kWholeTiles = 16, kIdleTiles = 8;
 
 // Shared memory: the queries, rings of value blocks and of rotary blocks, the
 // weights of two tiles.  N = 64 leaves room for two tiles exactly.
@@ -100,6 +107,7 @@ struct Sched {
     float* lse;                 // [workers][2][cols] partial states: a first and a last segment
     float* o;                   // [workers][2][cols][512]
     bool q_boxes;               // a CTA's columns are a box of the queries' tensor map
+    bool whole;                 // cluster w takes unit w: nothing is cut, nothing joined
 };
 
 __device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, int u) {
@@ -197,7 +205,8 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     // ---- the plan: the line of all units' tiles, and this cluster's share of it
     const int units = p.batch * sc.groups;
     const int per = (units + kThreads - 1) / kThreads;
-    const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
+    const int u0 = sc.whole ? worker : min(units, static_cast<int>(threadIdx.x) * per);
+    const int u1 = sc.whole ? worker + 1 : min(units, u0 + per);
     int64_t mine = 0;
     for (int u = u0; u < u1; ++u) mine += unit_places(sc, unit_of(p, sc, u));
     int64_t x = mine;
@@ -233,36 +242,40 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     __syncthreads();
     tc_after_sync();
     if (CL > 1) cluster_arrive();  // this CTA's barriers are initialised
-    int64_t before = x - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        before += w < warp ? plan_tot[w] : 0;
-        total += plan_tot[w];
-    }
-    int64_t share = total + sc.workers - 1;
-    share = share >> 32 ? share / sc.workers : static_cast<uint32_t>(share) / static_cast<uint32_t>(sc.workers);
-    share = max(share, static_cast<int64_t>(kMinShare + sc.toll));
-    const int64_t start = worker * share;
     Segments seg0;
-    seg0.left = max(min(share, total - start), static_cast<int64_t>(0));
-    if (start >= before && start < before + mine) {  // one thread at most
-        int64_t at = before;
-        for (int u = u0; u < u1; ++u) {
-            const Unit w = unit_of(p, sc, u);
-            const int t = unit_places(sc, w);
-            if (start < at + t) {
-                plan[0] = u;
-                plan[1] = static_cast<int>(start - at);
-                if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], w.tiles, static_cast<int>(share));
-                break;
-            }
-            at += t;
+    if (sc.whole) {
+        seg0.left = mine;
+    } else {
+        int64_t before = x - mine, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            before += w < warp ? plan_tot[w] : 0;
+            total += plan_tot[w];
         }
+        int64_t share = total + sc.workers - 1;
+        share = share >> 32 ? share / sc.workers : static_cast<uint32_t>(share) / static_cast<uint32_t>(sc.workers);
+        share = max(share, static_cast<int64_t>(kMinShare + sc.toll));
+        const int64_t start = worker * share;
+        seg0.left = max(min(share, total - start), static_cast<int64_t>(0));
+        if (start >= before && start < before + mine) {  // one thread at most
+            int64_t at = before;
+            for (int u = u0; u < u1; ++u) {
+                const Unit w = unit_of(p, sc, u);
+                const int t = unit_places(sc, w);
+                if (start < at + t) {
+                    plan[0] = u;
+                    plan[1] = static_cast<int>(start - at);
+                    if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], w.tiles, static_cast<int>(share));
+                    break;
+                }
+                at += t;
+            }
+        }
+        if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[worker] = make_int4(-1, 0, 0, 0);
     }
-    if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[worker] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     if (CL > 1) cluster_wait();  // so are the other CTA's
-    seg0.u = plan[0];
-    seg0.o = plan[1];
+    seg0.u = sc.whole ? worker : plan[0];
+    seg0.o = sc.whole ? 0 : plan[1];
     const uint32_t tmem = static_cast<uint32_t>(plan[2]);
     const uint32_t sbase = smem_u32(smem);
     // the swizzles need 1024-byte aligned tiles
@@ -904,7 +917,7 @@ cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, con
     cudaLaunchConfig_t cfg = config<N, CL>(sc.workers, attr, s);
     e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap),
                            *static_cast<const CUtensorMap*>(tmap_q), p, sc);
-    if (e != cudaSuccess || sc.workers == 1) return e;
+    if (e != cudaSuccess || sc.workers == 1 || sc.whole) return e;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -947,10 +960,16 @@ LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int
     pl.cols = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
     pl.cluster = cols <= 64 ? 1 : 2;
     pl.groups = static_cast<int>((cols + pl.cols * pl.cluster - 1) / (pl.cols * pl.cluster));
+    const int64_t unit_tiles = (static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys;
+    const int64_t units = static_cast<int64_t>(batch) * pl.groups, most = pl.cluster == 1 ? sms : resident_pairs(sms);
+    if (unit_tiles <= kWholeTiles && units <= most && unit_tiles * (most - units) <= kIdleTiles * most) {
+        pl.whole = true;
+        pl.workers = static_cast<int>(units);
+        pl.ws_bytes = 256;
+        return pl;
+    }
     // no more clusters than shares of the smallest size
-    const int64_t tiles = static_cast<int64_t>(batch) * pl.groups * ((static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys);
-    const int64_t most = pl.cluster == 1 ? sms : resident_pairs(sms);
-    pl.workers = static_cast<int>(max(int64_t(1), min(most, (tiles + kMinShare - 1) / kMinShare)));
+    pl.workers = static_cast<int>(max(int64_t(1), min(most, (units * unit_tiles + kMinShare - 1) / kMinShare)));
     const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.cluster;
     pl.ws_bytes = round256(pl.workers * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
     return pl;
@@ -964,6 +983,7 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     sc.toll = pl.cols == 64 ? kTollWide : kToll;
     sc.cols = pl.cols * pl.cluster;
     sc.q_boxes = q_boxes;
+    sc.whole = pl.whole;
     char* w = static_cast<char*>(workspace);
     sc.dir = reinterpret_cast<int4*>(w);
     w += round256(pl.workers * sizeof(int4));
