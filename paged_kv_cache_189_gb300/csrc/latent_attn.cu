@@ -103,7 +103,8 @@ struct Unit {
 struct Sched {
     int workers, groups, cols;  // clusters, column groups a sequence may have, columns of a group
     int toll;                   // places of the line ahead of each unit's tiles
-    int4* dir;                  // [workers] where each cluster starts: unit, place in it, its tiles, share
+    int4* dir;                  // [workers][2] where each cluster starts: place in its unit (-1: no
+                                // work), the unit's tiles, share; the unit's row, columns, first column
     float* lse;                 // [workers][2][cols] partial states: a first and a last segment
     float* o;                   // [workers][2][cols][512]
     bool q_boxes;               // a CTA's columns are a box of the queries' tensor map
@@ -264,13 +265,16 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                 if (start < at + t) {
                     plan[0] = u;
                     plan[1] = static_cast<int>(start - at);
-                    if (rank == 0) sc.dir[worker] = make_int4(u, plan[1], w.tiles, static_cast<int>(share));
+                    if (rank == 0) {
+                        sc.dir[2 * worker] = make_int4(plan[1], w.tiles, static_cast<int>(share), 0);
+                        sc.dir[2 * worker + 1] = make_int4(w.r0, w.cols, w.c0, 0);
+                    }
                     break;
                 }
                 at += t;
             }
         }
-        if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[worker] = make_int4(-1, 0, 0, 0);
+        if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[2 * worker] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
     if (CL > 1) cluster_wait();  // so are the other CTA's
@@ -797,51 +801,43 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
 
-// Four columns a CTA and cut: where cluster c starts inside a unit, the unit's
-// states, one a cluster in line, are joined: out = sum w_i O_i / sum w_i with w_i =
-// e^(lse_i - max).  Few states: the unit's first cut joins all four columns, a
-// group of 128 threads each.  Many: its first four cuts take a column each, every
-// group a quarter of the states.
-constexpr int kJoinCols = 4;
+// 4 E columns a CTA and cut: where cluster c starts inside a unit, the unit's states,
+// one a cluster in line, are joined: out = sum w_i O_i / sum w_i with w_i = e^(lse_i -
+// max).  Few states: the unit's first cut joins all the columns, E to each group of
+// 128 threads, whose loads are under way together.  Many: its first cuts share the
+// columns out, every group takes a quarter of the states.  E = 4 keeps units of 64
+// and 128 columns to one wave of CTAs (with 1 the calls took 4 us longer), E = 1
+// spreads those of 16 over the SMs (with 4: 1.3 to 3 us longer).
+constexpr int kJoinGroups = 4;
 constexpr int kJoinFew = 8;
-__global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const LatentParams p, const Sched sc) {
+template <int E>
+__global__ void __launch_bounds__(128 * kJoinGroups, E == 1 ? 3 : 1) latent_join_kernel(const LatentParams p, const Sched sc) {
     const int c = blockIdx.x + 1, g = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 d = sc.dir[c];
-    if (d.x < 0 || d.y <= sc.toll) return;
-    const Unit w = unit_of(p, sc, d.x);
-    const int64_t share = d.w, off = c * share - d.y, tile0 = off + sc.toll;  // the unit's places, its first tile's
+    const int4 d = sc.dir[2 * c], w = sc.dir[2 * c + 1];
+    if (d.x <= sc.toll) return;
+    const int64_t share = d.z, off = c * share - d.x, tile0 = off + sc.toll;  // the unit's places, its first tile's
     const int first = static_cast<int>(tile0 / share);                        // the cluster that it begins in
-    const int n = static_cast<int>((tile0 + d.z - 1) / share) - first + 1;
+    const int n = static_cast<int>((tile0 + d.y - 1) / share) - first + 1;
     const int first_slot = first * share < off ? 1 : 0;
     const int cut = c - first - 1;                                            // cuts of the unit before this one
-    if (cut > 0 && (n <= kJoinFew || cut >= kJoinCols)) return;
+    constexpr int kJoinCols = kJoinGroups * E;
+    const int col0 = blockIdx.y * kJoinCols;
+    const int valid = min(kJoinCols, w.y - w.z - col0);                       // columns that exist
+    if (valid <= 0) return;
     auto piece = [&](int k, int col) {
-        return (static_cast<int64_t>(first + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col;
+        return (static_cast<int64_t>(first + k) * 2 + (k == 0 ? first_slot : 0)) * sc.cols + col0 + col;
     };
-    // the states k0, k0 + step, ... of a column: their weights' sum and weighted sum
-    auto gather = [&](int col, int k0, int step, float& m, float& sum, float4& acc) {
-        m = -INFINITY;
-        for (int k = lane; k < n; k += 32) m = fmaxf(m, sc.lse[piece(k, col)]);
-        m = warp_max(m);
-        if (m == -INFINITY) m = 0.f;
-        sum = 0.f;
-        acc = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int k = k0; k < n; k += step) {
-            const int64_t st = piece(k, col);
-            const float wk = fast_exp2((sc.lse[st] - m) * kLog2e);
-            const float4 o = *reinterpret_cast<const float4*>(sc.o + st * kLatentDim + t * 4);
-            sum += wk;
-            acc.x = fmaf(wk, o.x, acc.x);
-            acc.y = fmaf(wk, o.y, acc.y);
-            acc.z = fmaf(wk, o.z, acc.z);
-            acc.w = fmaf(wk, o.w, acc.w);
-        }
+    auto add = [](float4& acc, float wk, const float4& o) {
+        acc.x = fmaf(wk, o.x, acc.x);
+        acc.y = fmaf(wk, o.y, acc.y);
+        acc.z = fmaf(wk, o.z, acc.z);
+        acc.w = fmaf(wk, o.w, acc.w);
     };
+    auto state = [&](int64_t at) { return *reinterpret_cast<const float4*>(sc.o + at * kLatentDim + t * 4); };
     auto store = [&](int col, float m, float sum, const float4& acc) {
         const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        const int64_t row = static_cast<int64_t>(w.r0) * p.heads + w.c0 + col;
+        const int64_t row = static_cast<int64_t>(w.x) * p.heads + w.z + col0 + col;
         if (p.out_f32) {
             *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatentDim + t * 4) =
                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -851,35 +847,67 @@ __global__ void __launch_bounds__(128 * kJoinCols) latent_join_kernel(const Late
         }
         if (p.lse && t == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + __log2f(sum) * kLn2;
     };
-    float m, sum;
-    float4 acc;
-    const int col0 = blockIdx.y * kJoinCols;
     if (n <= kJoinFew) {
-        if (w.c0 + col0 + g < w.cols) {
-            gather(col0 + g, 0, 1, m, sum, acc);
-            store(col0 + g, m, sum, acc);
+        if (cut > 0) return;
+        float lse[E], m[E], wk[E], sum[E];
+        float4 acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {  // lane k: the k-th state's LSE, then its weight
+            const int col = g * E + e;
+            lse[e] = lane < n && col < valid ? sc.lse[piece(lane, col)] : -INFINITY;
+            acc[e] = make_float4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            m[e] = warp_max(lse[e]);
+            if (m[e] == -INFINITY) m[e] = 0.f;
+            wk[e] = fast_exp2((lse[e] - m[e]) * kLog2e);
+            sum[e] = warp_sum(wk[e]);
+        }
+#pragma unroll 2
+        for (int k = 0; k < n; ++k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int col = g * E + e;
+                const float x = __shfl_sync(0xffffffffu, wk[e], k);
+                if (col < valid) add(acc[e], x, state(piece(k, col)));
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (g * E + e < valid) store(g * E + e, m[e], sum[e], acc[e]);
         return;
     }
-    __shared__ float4 sh_o[kJoinCols][128];
-    __shared__ float sh_s[kJoinCols];
-    const int col = col0 + cut;
-    if (w.c0 + col >= w.cols) return;
-    gather(col, g, kJoinCols, m, sum, acc);
-    sh_o[g][t] = acc;
-    if (t == 0) sh_s[g] = sum;
-    __syncthreads();
-    if (g > 0) return;
+    constexpr int kShare = E > 1 ? 2 : 1;  // columns a cut takes: a unit of many states has eight cuts
+    if (cut >= kJoinCols / kShare) return;
+    __shared__ float4 sh_o[kJoinGroups][128];
+    __shared__ float sh_s[kJoinGroups];
+    for (int col = kShare * cut; col < min(kShare * (cut + 1), valid); ++col) {
+        float m = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0, 0, 0, 0);
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, sc.lse[piece(k, col)]);
+        m = warp_max(m);
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll 4
+        for (int k = g; k < n; k += kJoinGroups) {
+            const int64_t at = piece(k, col);
+            const float x = fast_exp2((sc.lse[at] - m) * kLog2e);
+            sum += x;
+            add(acc, x, state(at));
+        }
+        sh_o[g][t] = acc;
+        if (t == 0) sh_s[g] = sum;
+        __syncthreads();
+        if (g == 0) {
 #pragma unroll
-    for (int k = 1; k < kJoinCols; ++k) {
-        const float4 o = sh_o[k][t];
-        sum += sh_s[k];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
+            for (int k = 1; k < kJoinGroups; ++k) {
+                sum += sh_s[k];
+                add(acc, 1.f, sh_o[k][t]);
+            }
+            store(col, m, sum, acc);
+        }
+        __syncthreads();
     }
-    store(col, m, sum, acc);
 }
 
 template <int N, int CL>
@@ -918,16 +946,17 @@ cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, con
     e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap),
                            *static_cast<const CUtensorMap*>(tmap_q), p, sc);
     if (e != cudaSuccess || sc.workers == 1 || sc.whole) return e;
+    constexpr int E = N == 16 ? 1 : 4;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t jc = {};
-    jc.gridDim = dim3(static_cast<unsigned>(sc.workers - 1), static_cast<unsigned>(sc.cols / kJoinCols));
-    jc.blockDim = dim3(128 * kJoinCols);
+    jc.gridDim = dim3(static_cast<unsigned>(sc.workers - 1), static_cast<unsigned>(sc.cols / (kJoinGroups * E)));
+    jc.blockDim = dim3(128 * kJoinGroups);
     jc.stream = s;
     jc.attrs = pdl;
     jc.numAttrs = 1;
-    return cudaLaunchKernelEx(&jc, latent_join_kernel, p, sc);
+    return cudaLaunchKernelEx(&jc, latent_join_kernel<E>, p, sc);
 }
 
 // Clusters of two that the current device runs at once (half the SMs where none can be queried).
@@ -971,7 +1000,7 @@ LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int
     // no more clusters than shares of the smallest size
     pl.workers = static_cast<int>(max(int64_t(1), min(most, (units * unit_tiles + kMinShare - 1) / kMinShare)));
     const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.cluster;
-    pl.ws_bytes = round256(pl.workers * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
+    pl.ws_bytes = round256(pl.workers * 2 * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
     return pl;
 }
 
@@ -986,7 +1015,7 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     sc.whole = pl.whole;
     char* w = static_cast<char*>(workspace);
     sc.dir = reinterpret_cast<int4*>(w);
-    w += round256(pl.workers * sizeof(int4));
+    w += round256(pl.workers * 2 * sizeof(int4));
     sc.lse = reinterpret_cast<float*>(w);
     w += round256(static_cast<size_t>(pl.workers) * 2 * sc.cols * 4);
     sc.o = reinterpret_cast<float*>(w);
