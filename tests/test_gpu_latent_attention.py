@@ -77,6 +77,14 @@ def test_many_sequences():
     Case(kv, [1] * 300, [1] * 300, 8, seed=4).check()
 
 
+@pytest.mark.parametrize("B,H", [(100, 16), (152, 3), (70, 128), (60, 64)])
+def test_short_units_one_to_a_cluster(B, H):
+    """As many short units as run at once, of uneven lengths, some empty."""
+    g = np.random.default_rng(B)
+    kv = [int(x) if x > 40 else 0 for x in g.integers(0, 400, B)]
+    Case(kv, [1] * B, [1] * B, H, seed=B).check()
+
+
 @pytest.mark.parametrize("H", [16, 128])
 def test_chunk_over_context(H):
     Case([300, 700], [100, 41], [100, 50], H, seed=5).check()

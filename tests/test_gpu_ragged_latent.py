@@ -83,6 +83,10 @@ def test_more_key_tiles_than_the_ring_repeats_after(mask):
     Ragged([300, 20], [2300, 1100], 2, mask=mask, seed=7).check()
 
 
+def test_more_pairs_than_run_at_once():
+    Ragged([300, 257, 10, 280, 300, 260], [300, 400, 30, 280, 500, 260], 16, seed=8).check()
+
+
 def test_same_bits_every_time():
     c = Ragged([300, 256], [700, 256], 4, seed=6)
     a, la, _ = c.run()
