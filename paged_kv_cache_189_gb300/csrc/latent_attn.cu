@@ -297,8 +297,6 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         set_err(p.err, PKV_ERRBIT_TIMEOUT);
         return false;
     };
-    // a tile's rotary block is used first in even tiles and last in odd ones:
-    // with one buffer its next copy has a tile's time to land
     Segments it = seg0;
 
     if (warp == kProducerWarp) {
@@ -377,26 +375,22 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                     }
                 };
                 // (a fresh barrier's previous phase counts as complete: the first round passes)
-                auto rope = [&] {
-                    if (!wait(&r_empty[r.s], r.ph ^ 1)) return false;
-                    mbar_arrive_expect_tx(&r_full[r.s], kHalf);
-                    copy(smem + D::kROff + r.s * kHalf, &r_full[r.s], kLatentDim);
-                    r.next();
-                    return true;
-                };
-                if ((n & 1) == 0) alive = rope();
                 for (int b = 0; alive && b < kBlocks; ++b) {
-                    if (!wait(&v_empty[v.s], v.ph ^ 1)) {
-                        alive = false;
-                        break;
-                    }
+                    alive = wait(&v_empty[v.s], v.ph ^ 1);
+                    if (!alive) break;
                     mbar_arrive_expect_tx(&v_full[v.s], kBlock);
                     uint8_t* dst = smem + D::kVOff + v.s * kBlock;
                     copy(dst, &v_full[v.s], b * 128);
                     copy(dst + kHalf, &v_full[v.s], b * 128 + 64);
                     v.next();
                 }
-                if (alive && (n & 1) == 1) alive = rope();
+                // the rotary block comes last in every tile: with one buffer its next copy has a
+                // tile's time to land
+                alive = alive && wait(&r_empty[r.s], r.ph ^ 1);
+                if (!alive) break;
+                mbar_arrive_expect_tx(&r_full[r.s], kHalf);
+                copy(smem + D::kROff + r.s * kHalf, &r_full[r.s], kLatentDim);
+                r.next();
             }
             // do not leave with copies into this CTA's shared memory in flight
             // (buffers behind `s` were last filled in this round, the others in the one before)
@@ -435,33 +429,25 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             tc_mma(d, da + 2 * kk, dq + ((qb * D::kQBlock + kk * 32) >> 4), kIdesc, acc || kk > 0);
                     };
-                    auto rope = [&](bool acc) {
-                        settle(&r_full[r.s], r.ph);
-                        half(dr + r.s * (kHalf >> 4), kRopeBlock, acc);
-                        if constexpr (CL > 1) tc_commit_all(&r_empty[r.s], (1 << CL) - 1);
-                        else tc_commit(&r_empty[r.s]);
-                        r.next();
-                    };
                     ok = wait(&p_full[t], ((n >> 1) & 1) ^ 1);  // the softmax has read tile n - 2's scores
-                    if (t == 0) {
-                        rope(false);
-                        probe(&v_full[v.s], v.ph);
-                    }
+                    tc_after_sync();
 #pragma unroll
                     for (int b = 0; b < kBlocks; ++b) {
                         settle(&v_full[v.s], v.ph);
                         const uint64_t da = dv + v.s * (kBlock >> 4);
-                        half(da, 2 * b, t == 0 || b > 0);
+                        half(da, 2 * b, b > 0);
                         v.next();
-                        // (the rotary block ends odd tiles and begins even ones)
                         if (b + 1 < kBlocks) probe(&v_full[v.s], v.ph);
                         else probe(&r_full[r.s], r.ph);
                         half(da + (kHalf >> 4), 2 * b + 1, true);
                     }
-                    if (t == 1) rope(true);
+                    settle(&r_full[r.s], r.ph);
+                    half(dr + r.s * (kHalf >> 4), kRopeBlock, true);
+                    if constexpr (CL > 1) tc_commit_all(&r_empty[r.s], (1 << CL) - 1);
+                    else tc_commit(&r_empty[r.s]);
+                    r.next();
                     tc_commit(&s_full[t]);
-                    if (t == 1) probe(&r_full[r.s], r.ph);
-                    else probe(&v_full[v.s], v.ph);
+                    probe(&v_full[v.s], v.ph);
                 }
                 tc_commit(q_free);
             }
