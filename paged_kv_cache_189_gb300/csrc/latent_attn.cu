@@ -20,8 +20,8 @@
 //
 // What bounds it (64 sequences of 513-8193 keys, among others, us; floor = bytes at
 // the copy rate): 16 columns 66 (50): DRAM for ~55 of them, then 2.5 us before the
-// first copy, shares that end up to 4 us apart, 5 us launch and join; 64 columns 83
-// (53) and 128 on a cluster 105 (49): a tile's buffers are held through S^T, softmax
+// first copy, shares that end up to 4 us apart, 5 us launch and join; 64 columns 81
+// (53) and 128 on a cluster 101 (49): a tile's buffers are held through S^T, softmax
 // and O^T (~4000 cycles) and shared memory holds two tiles beside 64 columns of Q,
 // and each tile takes 36 x 32 + 16 x 48 = 1920 cycles of products (measured:
 // 64 x 64 x 16 products issue every 32 cycles, 128 x 64 x 16 every 48).
