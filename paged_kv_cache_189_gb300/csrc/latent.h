@@ -78,10 +78,10 @@ struct LatentParams {
     int32_t* err;
 };
 struct LatentPlan {
-    int cols, cluster;  // columns a CTA holds, CTAs that share their key tiles
-    int workers;        // clusters of the launch
-    int groups;         // column groups (cols * cluster) of a sequence, at the host bounds
-    bool whole;         // a cluster for every group, which then has no states to join
+    int cols, ctas;  // columns a CTA holds, CTAs of a worker (all on the same key tiles)
+    int workers;     // one or a pair of CTAs each
+    int groups;      // column groups (cols * ctas) of a sequence, at the host bounds
+    bool whole;      // a worker for every group, which then has no states to join
     size_t ws_bytes;
 };
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms);

@@ -83,7 +83,7 @@ int device_sms() {
 }
 
 // What paged_attention_latent counts in 32 bits: columns of a sequence, column
-// groups of the call, and a cluster's share of the key tiles.
+// groups of the call, and a worker's share of the key tiles.
 bool counts_ok(int batch, int max_q_rows, int num_heads, int max_kv_len) {
     if (max_kv_len > kMaxCount || max_q_rows > kMaxCount / num_heads || batch > 65535) return false;
     const int64_t groups = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_q_rows) * num_heads + 15) / 16);

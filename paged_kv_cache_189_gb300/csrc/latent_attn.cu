@@ -10,18 +10,21 @@
 // read from DRAM once and used twice from shared memory: K-major for S^T, and as
 // the same bytes MN-major for O^T.
 //
-// A CTA holds N = 16, 32 or 64 columns; more are held by a cluster of two CTAs,
-// each of which loads one page of every tile for both (multicast).  The tiles of
-// all units (a unit is a column group of a sequence) are one line that the clusters
+// A CTA holds N = 16, 32 or 64 columns; more are held by a pair of neighbouring CTAs,
+// which walk the same tiles side by side, each with copies of its own: a tile comes
+// from DRAM for the first and from L2 for the second.  (One page a CTA, copied into
+// both: 100.8 us against 99.8 for 128 columns, 195 against 191 for a prompt chunk.  The
+// pair as a cluster without that: 99.5 and 192.5.)  The tiles of all units (a unit is a
+// column group of a sequence) are one line that the workers (CTAs, or pairs of them)
 // share out evenly, each unit's tiles behind a few more places that stand for what
-// beginning it costs.  A cluster works through its share segment by segment (a
+// beginning it costs.  A worker goes through its share segment by segment (a
 // segment is a range of one unit's tiles) and leaves a partial state where a unit
 // was cut; a second launch joins those.
 //
 // What bounds it (64 sequences of 513-8193 keys, among others, us; floor = bytes at
 // the copy rate): 16 columns 66 (50): DRAM for ~55 of them, then 2.5 us before the
 // first copy, shares that end up to 4 us apart, 5 us launch and join; 64 columns 81
-// (53) and 128 on a cluster 101 (49): a tile's buffers are held through S^T, softmax
+// (53) and 128 on pairs 100 (49): a tile's buffers are held through S^T, softmax
 // and O^T (~4000 cycles) and shared memory holds two tiles beside 64 columns of Q,
 // and each tile takes 36 x 32 + 16 x 48 = 1920 cycles of products (measured:
 // 64 x 64 x 16 products issue every 32 cycles, 128 x 64 x 16 every 48).
@@ -47,15 +50,15 @@ constexpr int kBlocks = kLatentDim / 128;  // value blocks of a tile (the rotary
 constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
 constexpr int kNoPage = -2;                // look-up past the last page: zeros, and no error
-// Tiles a cluster takes at least: one sequence of 8192 keys takes 16.0 / 14.4 / 15.2 / 18.0
+// Tiles a worker takes at least: one sequence of 8192 keys takes 16.0 / 14.4 / 15.2 / 18.0
 // us with 1 / 2 / 4 / 8, four of 500-1500 keys 12.2 / 13.9 / 15.2 / 18.8, two short ones 8.7 with 2
 constexpr int kMinShare = 2;
 // What a segment costs beside its tiles (queries, first copies, outputs), in tiles.  With
 // 0 / 1 / 3 and 0 / 2 / 5: 68.1 / 67.6 / 67.5 us (16 columns), 88.1 / 84.8 / 84.5 (64), 111 / 107 / 109.5 (128)
 constexpr int kToll = 1, kTollWide = 2;
 // Units of at most kWholeTiles tiles (at the host's bound) that all run at once go one
-// to a cluster, without shares and join, where that leaves no more than kIdleTiles of a
-// unit's time idle over all clusters.  Shares and join / one to a cluster, us: two
+// to a worker, without shares and join, where that leaves no more than kIdleTiles of a
+// unit's time idle over all workers.  Shares and join / one to a worker, us: two
 // sequences of 128 / 256 / 512 / 1024 keys, 16 heads 8.6 / 7.2, 11.8 / 9.5, 12.1 / 13.0, 13.1 / 20.4,
 // 128 heads 11.6 / 10.2, 16.1 / 12.9, 17.6 / 18.1, 19.3 / 28.3; 64 sequences of half to all of
 // 512 / 1024 keys, 16 heads 19.2 / 15.3, 25.8 / 24.9, 128 heads 37.1 / 23.6, 46.7 / 33.7
@@ -87,7 +90,7 @@ struct Dim {
     static constexpr int kRedOff = kBarOff + ((kNumBars * 8 + 127) / 128) * 128;  // [4][N] per-warp maxima or sums
     static constexpr int kColOff = kRedOff + 4 * N * 4;   // [N] factors (rescale, then 1 / sum)
     static constexpr int kLimOff = kColOff + N * 4;       // [N] keys each column sees
-    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: warp totals, the cluster's first unit
+    static constexpr int kPlanOff = kLimOff + N * 4;      // plan: warp totals, the worker's first unit
     static constexpr int kBytes = kPlanOff + 16 + 8 * (kSoftmaxWarps + 4);
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kSCol = 4 * N;              // S^T behind O^T's four blocks
@@ -101,14 +104,14 @@ struct Unit {
 };
 
 struct Sched {
-    int workers, groups, cols;  // clusters, column groups a sequence may have, columns of a group
+    int workers, groups, cols;  // workers, column groups a sequence may have, columns of a group
     int toll;                   // places of the line ahead of each unit's tiles
-    int4* dir;                  // [workers][2] where each cluster starts: place in its unit (-1: no
+    int4* dir;                  // [workers][2] where each worker starts: place in its unit (-1: no
                                 // work), the unit's tiles, share; the unit's row, columns, first column
     float* lse;                 // [workers][2][cols] partial states: a first and a last segment
     float* o;                   // [workers][2][cols][512]
     bool q_boxes;               // a CTA's columns are a box of the queries' tensor map
-    bool whole;                 // cluster w takes unit w: nothing is cut, nothing joined
+    bool whole;                 // worker w takes unit w: nothing is cut, nothing joined
 };
 
 __device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, int u) {
@@ -132,7 +135,7 @@ __device__ __forceinline__ Unit unit_of(const LatentParams& p, const Sched& sc, 
 // The places of the line that a unit takes.
 __device__ __forceinline__ int unit_places(const Sched& sc, const Unit& w) { return w.tiles > 0 ? w.tiles + sc.toll : 0; }
 
-// The segments of one cluster's share, in order; every role walks them alike.
+// The segments of one worker's share, in order; every role walks them alike.
 struct Segments {
     int u, o;      // unit and place in it that come next
     int64_t left;  // places of the share
@@ -170,7 +173,7 @@ struct Ring {
     }
 };
 
-template <int N, int CL>
+template <int N, int CTAS>
 __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q,
                        const LatentParams p, const Sched sc) {
@@ -180,8 +183,8 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     constexpr int kQueryWarp = D::kQueryWarp;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int worker = blockIdx.x / CL;
+    const int rank = blockIdx.x % CTAS;
+    const int worker = blockIdx.x / CTAS;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + D::kBarOff);
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     int* plan = reinterpret_cast<int*>(smem + D::kPlanOff + kThreads / 4);  // unit, tile, tmem, abort
     volatile int* abort_flag = plan + 3;
 
-    // ---- the plan: the line of all units' tiles, and this cluster's share of it
+    // ---- the plan: the line of all units' tiles, and this worker's share of it
     const int units = p.batch * sc.groups;
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = sc.whole ? worker : min(units, static_cast<int>(threadIdx.x) * per);
@@ -220,11 +223,11 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     if (warp == kQueryWarp && lane == 0) {
         for (int s = 0; s < D::kV; ++s) {
             mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], CL);
+            mbar_init(&v_empty[s], 1);
         }
         for (int s = 0; s < D::kR; ++s) {
             mbar_init(&r_full[s], 1);
-            mbar_init(&r_empty[s], CL);
+            mbar_init(&r_empty[s], 1);
         }
         mbar_init(q_ready, 32);
         mbar_init(q_free, 1);
@@ -242,7 +245,6 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    if (CL > 1) cluster_arrive();  // this CTA's barriers are initialised
     Segments seg0;
     if (sc.whole) {
         seg0.left = mine;
@@ -277,7 +279,6 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         if (seg0.left == 0 && threadIdx.x == 0 && rank == 0) sc.dir[2 * worker] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
-    if (CL > 1) cluster_wait();  // so are the other CTA's
     seg0.u = sc.whole ? worker : plan[0];
     seg0.o = sc.whole ? 0 : plan[1];
     const uint32_t tmem = static_cast<uint32_t>(plan[2]);
@@ -303,8 +304,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
         // ============================ producer ==============================
         if (elect_one()) {
             prefetch_tmap(&tm);
-            constexpr uint16_t kAll = (1 << CL) - 1;
-            constexpr int kPages = 2 / CL;  // of a tile: a cluster's CTAs look up one each
+            constexpr int kPages = kKeys / 32;  // of a tile
             Ring<D::kV> v;
             Ring<D::kR> r;
             // The pages are looked up a tile ahead of their use, on across segments.
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < kPages; ++k) {
-                    const int lp = 2 * j + (CL > 1 ? rank : k);
+                    const int lp = kPages * j + k;
                     ph[k] = lp < last_page ? max(bt[lp], -1) : kNoPage;
                 }
                 ++j;
@@ -369,10 +369,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                 // 64 dims from d0 of the tile's pages to dst
                 auto copy = [&](uint8_t* dst, uint64_t* bar, int d0) {
 #pragma unroll
-                    for (int k = 0; k < kPages; ++k) {
-                        if constexpr (CL > 1) tma_load_3d_all(dst + rank * 4096, &tm, bar, d0, 0, ph[k], kAll);
-                        else tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
-                    }
+                    for (int k = 0; k < kPages; ++k) tma_load_3d(dst + k * 4096, &tm, bar, d0, 0, ph[k]);
                 };
                 // (a fresh barrier's previous phase counts as complete: the first round passes)
                 for (int b = 0; alive && b < kBlocks; ++b) {
@@ -443,8 +440,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
                     }
                     settle(&r_full[r.s], r.ph);
                     half(dr + r.s * (kHalf >> 4), kRopeBlock, true);
-                    if constexpr (CL > 1) tc_commit_all(&r_empty[r.s], (1 << CL) - 1);
-                    else tc_commit(&r_empty[r.s]);
+                    tc_commit(&r_empty[r.s]);
                     r.next();
                     tc_commit(&s_full[t]);
                     probe(&v_full[v.s], v.ph);
@@ -477,8 +473,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
                             tc_mma(tmem + b * N, da + kk * (2048 >> 4), db + kk * (32 * N >> 4), kIdesc, j > it.j0 || kk > 0);
-                        if constexpr (CL > 1) tc_commit_all(&v_empty[s], (1 << CL) - 1);
-                        else tc_commit(&v_empty[s]);
+                        tc_commit(&v_empty[s]);
                         if (++s == D::kV) s = 0;
                     }
                     tc_commit(&pv_done[t]);
@@ -528,7 +523,7 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(q_ready);
         }
-        // this cluster's part of the units that see no key: zeros
+        // this worker's part of the units that see no key: zeros
         for (int u = worker; u < units; u += sc.workers) {
             const Unit w = unit_of(p, sc, u);
             if (p.checked && rank == 0 && lane == 0 && w.c0 == 0) {
@@ -777,18 +772,13 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 
     __syncwarp();
     tc_before_sync();
-    if (CL > 1) {  // the other CTA's copies and commits land here no more
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
     tc_after_sync();
     if (warp == kValueWarp) tc_dealloc(tmem, D::kTmem);
 }
 
-// 4 E columns a CTA and cut: where cluster c starts inside a unit, the unit's states,
-// one a cluster in line, are joined: out = sum w_i O_i / sum w_i with w_i = e^(lse_i -
+// 4 E columns a CTA and cut: where worker c starts inside a unit, the unit's states,
+// one a worker in line, are joined: out = sum w_i O_i / sum w_i with w_i = e^(lse_i -
 // max).  Few states: the unit's first cut joins all the columns, E to each group of
 // 128 threads, whose loads are under way together.  Many: its first cuts share the
 // columns out, every group takes a quarter of the states.  E = 4 keeps units of 64
@@ -803,7 +793,7 @@ __global__ void __launch_bounds__(128 * kJoinGroups, E == 1 ? 3 : 1) latent_join
     const int4 d = sc.dir[2 * c], w = sc.dir[2 * c + 1];
     if (d.x <= sc.toll) return;
     const int64_t share = d.z, off = c * share - d.x, tile0 = off + sc.toll;  // the unit's places, its first tile's
-    const int first = static_cast<int>(tile0 / share);                        // the cluster that it begins in
+    const int first = static_cast<int>(tile0 / share);                        // the worker that it begins in
     const int n = static_cast<int>((tile0 + d.y - 1) / share) - first + 1;
     const int first_slot = first * share < off ? 1 : 0;
     const int cut = c - first - 1;                                            // cuts of the unit before this one
@@ -896,41 +886,20 @@ __global__ void __launch_bounds__(128 * kJoinGroups, E == 1 ? 3 : 1) latent_join
     }
 }
 
-template <int N, int CL>
-cudaLaunchConfig_t config(int workers, cudaLaunchAttribute* attr, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(workers * CL));
-    cfg.blockDim = dim3(Dim<N>::kThreads);
-    cfg.dynamicSmemBytes = Dim<N>::kBytes;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CL > 1 ? 1 : 0;  // (a plain launch costs the host a microsecond less)
-    return cfg;
-}
-
-template <int N, int CL>
-cudaError_t opt_in() {
+template <int N, int CTAS>
+cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, const void* tmap_q, cudaStream_t s) {
     static DeviceOnce opted;
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return opted.get(dev, &done, [&](int, int* v) {
+    e = opted.get(dev, &done, [&](int, int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(latent_attn_kernel<N, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dim<N>::kBytes);
+        return cudaFuncSetAttribute(latent_attn_kernel<N, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dim<N>::kBytes);
     });
-}
-
-template <int N, int CL>
-cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, const void* tmap_q, cudaStream_t s) {
-    cudaError_t e = opt_in<N, CL>();
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config<N, CL>(sc.workers, attr, s);
-    e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<N, CL>, *static_cast<const CUtensorMap*>(tmap),
-                           *static_cast<const CUtensorMap*>(tmap_q), p, sc);
+    latent_attn_kernel<N, CTAS><<<static_cast<unsigned>(sc.workers * CTAS), Dim<N>::kThreads, Dim<N>::kBytes, s>>>(
+        *static_cast<const CUtensorMap*>(tmap), *static_cast<const CUtensorMap*>(tmap_q), p, sc);
+    e = cudaGetLastError();
     if (e != cudaSuccess || sc.workers == 1 || sc.whole) return e;
     constexpr int E = N == 16 ? 1 : 4;
     cudaLaunchAttribute pdl[1];
@@ -945,22 +914,6 @@ cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, con
     return cudaLaunchKernelEx(&jc, latent_join_kernel<E>, p, sc);
 }
 
-// Clusters of two that the current device runs at once (half the SMs where none can be queried).
-int resident_pairs(int sms) {
-    static DeviceOnce pairs;
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && opt_in<64, 2>() == cudaSuccess &&
-        pairs.get(dev, &n, [&](int, int* v) {
-            cudaLaunchAttribute attr[1];
-            cudaLaunchConfig_t cfg = config<64, 2>(1, attr, nullptr);
-            return cudaOccupancyMaxActiveClusters(v, latent_attn_kernel<64, 2>, &cfg);
-        }) == cudaSuccess &&
-        n > 0)
-        return n;
-    cudaGetLastError();
-    return sms / 2 > 0 ? sms / 2 : 1;
-}
-
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -970,22 +923,22 @@ LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int
     // The narrowest CTA that holds a sequence's columns, pairs of the widest beyond.  64
     // sequences of 513-8193 keys, us: 16 columns in CTAs of 16 / 32 / 64: 66.6 / 70.1 / 75.2;
     // 32 columns: 105.3 / 75.0 / 80.0; 64 columns: 187 / 114 / 85.3; 128 columns in CTAs of 64
-    // one by one / in clusters of two: 130 / 107.
+    // one by one / in pairs: 130 / 107.
     const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
     pl.cols = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
-    pl.cluster = cols <= 64 ? 1 : 2;
-    pl.groups = static_cast<int>((cols + pl.cols * pl.cluster - 1) / (pl.cols * pl.cluster));
+    pl.ctas = cols <= 64 ? 1 : 2;
+    pl.groups = static_cast<int>((cols + pl.cols * pl.ctas - 1) / (pl.cols * pl.ctas));
     const int64_t unit_tiles = (static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys;
-    const int64_t units = static_cast<int64_t>(batch) * pl.groups, most = pl.cluster == 1 ? sms : resident_pairs(sms);
+    const int64_t units = static_cast<int64_t>(batch) * pl.groups, most = max(sms / pl.ctas, 1);
     if (unit_tiles <= kWholeTiles && units <= most && unit_tiles * (most - units) <= kIdleTiles * most) {
         pl.whole = true;
         pl.workers = static_cast<int>(units);
         pl.ws_bytes = 256;
         return pl;
     }
-    // no more clusters than shares of the smallest size
+    // no more workers than shares of the smallest size
     pl.workers = static_cast<int>(max(int64_t(1), min(most, (units * unit_tiles + kMinShare - 1) / kMinShare)));
-    const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.cluster;
+    const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.ctas;
     pl.ws_bytes = round256(pl.workers * 2 * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
     return pl;
 }
@@ -996,7 +949,7 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     sc.workers = pl.workers;
     sc.groups = pl.groups;
     sc.toll = pl.cols == 64 ? kTollWide : kToll;
-    sc.cols = pl.cols * pl.cluster;
+    sc.cols = pl.cols * pl.ctas;
     sc.q_boxes = q_boxes;
     sc.whole = pl.whole;
     char* w = static_cast<char*>(workspace);
@@ -1005,7 +958,7 @@ cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void
     sc.lse = reinterpret_cast<float*>(w);
     w += round256(static_cast<size_t>(pl.workers) * 2 * sc.cols * 4);
     sc.o = reinterpret_cast<float*>(w);
-    if (pl.cluster == 2) return launch<64, 2>(p, sc, tmap, tmap_q, s);
+    if (pl.ctas == 2) return launch<64, 2>(p, sc, tmap, tmap_q, s);
     if (pl.cols == 64) return launch<64, 1>(p, sc, tmap, tmap_q, s);
     if (pl.cols == 32) return launch<32, 1>(p, sc, tmap, tmap_q, s);
     return launch<16, 1>(p, sc, tmap, tmap_q, s);

@@ -1,5 +1,5 @@
-// tc.cuh -- tensor-core, tensor-memory and cluster PTX wrappers of the latent
-// attention kernels.
+// tc.cuh -- tensor-core and tensor-memory PTX wrappers of the latent attention
+// kernels.
 #pragma once
 
 #include "pkv_common.cuh"
@@ -47,12 +47,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  ::"r"(smem_u32(bar)) : "memory");
-}
-// the same on the barrier at this offset in every CTA of `mask`
-__device__ __forceinline__ void tc_commit_all(uint64_t* bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(smem_u32(bar)), "h"(mask) : "memory");
 }
 
 // Shared-memory matrix descriptor: start address, leading and stride byte
@@ -155,24 +149,6 @@ __device__ __forceinline__ void copy_async_wait() {
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-// ---------------------------------------------------------------------------
-// clusters
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// a box to the same offset of every CTA in `mask`, completion on each one's barrier
-__device__ __forceinline__ void tma_load_3d_all(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2,
-                                                uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5}], [%2], %6;"
-        ::"r"(smem_u32(dst)), "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "h"(mask) : "memory");
-}
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
