@@ -767,7 +767,9 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
  *  out            device [rows][num_heads][latent_dim], bf16 or f32 (dense)
  *  workspace      paged_attention_latent_workspace_size(...) bytes, 256-byte
  *                 aligned, sized with the device current that the call will use;
- *                 one workspace must not serve two calls in flight
+ *                 that many bytes serve every call whose batch, max_q_rows, num_heads
+ *                 and max_kv_len are none above these (a server sizes it once, for its
+ *                 largest step); one workspace must not serve two calls in flight
  *  max_q_rows * num_heads, max_kv_len  at most 2^31 - 256, batch 65535, and
  *                 batch * ceil(max_q_rows * num_heads / 16) * (max_kv_len / 64 + 8)
  *                 at most 2^36

@@ -85,6 +85,9 @@ struct LatentPlan {
     size_t ws_bytes;
 };
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms);
+// What any call whose bounds are none above these needs at most: a smaller batch may take
+// shares where this one's units all run at once, fewer columns may have more workers.
+size_t latent_workspace_bytes(int batch, int max_q_rows, int heads, int max_kv_len, int sms);
 // tmap: the pool as {576, 32, pages}, boxes of a page's 64 columns.  q_boxes: tmap_q holds
 // the queries as {576, heads, rows} in boxes of 64 columns x pl.cols (row, head) pairs,
 // which takes heads that divide pl.cols or are a multiple of it.

@@ -172,7 +172,7 @@ size_t paged_attention_latent_workspace_size(int batch, int max_q_rows, int num_
     if (batch <= 0 || max_q_rows <= 0 || num_heads <= 0 || max_kv_len < 0 || !dims_ok(latent_dim, rope_dim) ||
         (flags & PKV_FLAG_SIMT_ONLY) || !counts_ok(batch, max_q_rows, num_heads, max_kv_len))
         return 0;
-    return pkv::plan_latent(batch, max_q_rows, num_heads, max_kv_len, device_sms()).ws_bytes;
+    return pkv::latent_workspace_bytes(batch, max_q_rows, num_heads, max_kv_len, device_sms());
 }
 
 pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* pool,

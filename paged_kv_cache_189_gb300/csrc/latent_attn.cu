@@ -916,6 +916,20 @@ cudaError_t launch(const LatentParams& p, const Sched& sc, const void* tmap, con
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
+int64_t tiles_of(int max_kv_len) { return (static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys; }
+int columns_of(int64_t cols) { return cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : 128; }  // a worker holds
+int64_t groups_of(int64_t cols) { return (cols + columns_of(cols) - 1) / columns_of(cols); }
+int workers_at_once(int cols, int sms) { return cols <= 64 ? sms : max(sms / 2, 1); }
+// no more workers than shares of the smallest size
+int share_workers(int cols, int64_t units, int64_t unit_tiles, int sms) {
+    return static_cast<int>(
+        max(int64_t(1), min(int64_t(workers_at_once(cols, sms)), (units * unit_tiles + kMinShare - 1) / kMinShare)));
+}
+size_t share_bytes(int cols, int workers) {
+    const size_t states = static_cast<size_t>(workers) * 2 * cols;
+    return round256(workers * 2 * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
+}
+
 }  // namespace
 
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms) {
@@ -925,22 +939,30 @@ LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int
     // 32 columns: 105.3 / 75.0 / 80.0; 64 columns: 187 / 114 / 85.3; 128 columns in CTAs of 64
     // one by one / in pairs: 130 / 107.
     const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
-    pl.cols = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
-    pl.ctas = cols <= 64 ? 1 : 2;
-    pl.groups = static_cast<int>((cols + pl.cols * pl.ctas - 1) / (pl.cols * pl.ctas));
-    const int64_t unit_tiles = (static_cast<int64_t>(max_kv_len) + kKeys - 1) / kKeys;
-    const int64_t units = static_cast<int64_t>(batch) * pl.groups, most = max(sms / pl.ctas, 1);
+    const int held = columns_of(cols);
+    pl.cols = min(held, 64);
+    pl.ctas = held / pl.cols;
+    pl.groups = static_cast<int>(groups_of(cols));
+    const int64_t unit_tiles = tiles_of(max_kv_len);
+    const int64_t units = static_cast<int64_t>(batch) * pl.groups, most = workers_at_once(held, sms);
     if (unit_tiles <= kWholeTiles && units <= most && unit_tiles * (most - units) <= kIdleTiles * most) {
         pl.whole = true;
         pl.workers = static_cast<int>(units);
         pl.ws_bytes = 256;
         return pl;
     }
-    // no more workers than shares of the smallest size
-    pl.workers = static_cast<int>(max(int64_t(1), min(most, (units * unit_tiles + kMinShare - 1) / kMinShare)));
-    const size_t states = static_cast<size_t>(pl.workers) * 2 * pl.cols * pl.ctas;
-    pl.ws_bytes = round256(pl.workers * 2 * sizeof(int4)) + round256(states * 4) + states * kLatentDim * 4;
+    pl.workers = share_workers(held, units, unit_tiles, sms);
+    pl.ws_bytes = share_bytes(held, pl.workers);
     return pl;
+}
+
+size_t latent_workspace_bytes(int batch, int max_q_rows, int heads, int max_kv_len, int sms) {
+    const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
+    size_t bytes = 256;
+    for (int held = 16; held <= columns_of(cols); held *= 2)
+        bytes = max(bytes, share_bytes(held, share_workers(held, batch * (held == 128 ? groups_of(cols) : 1),
+                                                           tiles_of(max_kv_len), sms)));
+    return bytes;
 }
 
 cudaError_t launch_latent_attn(const LatentParams& p, const LatentPlan& pl, void* workspace, const void* tmap,
