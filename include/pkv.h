@@ -660,8 +660,14 @@ pkv_status rotate_rows(void* x, int64_t rows, int64_t cols, int64_t row_stride,
  *       its pages fit block_table_stride, and
  *       need[b] = 0, or the sum of need up to and with it is at most the
  *       stack's height after step 1 (so a sequence with room in its last page
- *       is never held up).
- *     A request that is not granted takes nothing; the caller asks again.
+ *       never waits for pages).
+ *     A request that is not granted takes nothing; the caller asks again.  Both
+ *     sums count refused requests too: nothing overtakes a request in front of it
+ *     by taking tokens or pages that this one asked for.  A request that no call
+ *     can grant (more than max_tokens tokens, or more pages than
+ *     block_table_stride) therefore holds back what is behind it in every call,
+ *     rows with room in their last page included, until the caller withdraws it
+ *     or asks for less; PKV_ERRBIT_LEN says that there was one.
  *  3. Granted requests take their pages from the stack's top, in the order of
  *     sequences and of their pages, into block_table[b][ceil(kv_lens[b] / 32)...].
  *  4. kv_lens_out[b] = the keys with this step's (0 for a finished sequence),

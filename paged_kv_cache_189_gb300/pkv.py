@@ -627,7 +627,10 @@ def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, k
     ``new_lens [batch]`` tokens are asked for by sequences of ``kv_lens`` keys
     (below zero: finished), pages come from and go back to the stack
     ``free_pages[:num_free]`` (see ``include/pkv.h``).  ``kv_lens_out`` and
-    ``num_free_out`` may be the inputs themselves."""
+    ``num_free_out`` may be the inputs themselves.  Requests are granted in
+    order: one that does not fit holds back those behind it, so one that never
+    can (more tokens than ``slots`` has, more pages than the table's width) must
+    be withdrawn or asked for in pieces."""
     batch, tokens, shape = new_lens.numel(), slots.numel(), block_table.shape
     _vector(new_lens, "new_lens", _I32, batch)
     _vector(kv_lens, "kv_lens", _I32, batch)
