@@ -688,7 +688,10 @@ pkv_status rotate_rows(void* x, int64_t rows, int64_t cols, int64_t row_stride,
  *  block_table      device int32 [batch][block_table_stride]
  *  q_indptr         device int32 [batch + 1]
  *  slots, positions device int64 [max_tokens]
- *  batch            at most 4096; max_tokens at most 2^30
+ *  batch            at most 4096; max_tokens at most 2^30.  batch 0: nothing is
+ *                   enqueued and no output is written, so a caller whose batch may
+ *                   be empty clears an earlier step's slots and q_indptr itself
+ *                   (the Python binding does)
  *  err              nullable device int32: a pushed page that was dropped, a
  *                   negative length or *num_free outside [0, free_capacity] (both
  *                   taken as the nearest valid value) OR PKV_ERRBIT_PAGE; a

@@ -630,7 +630,8 @@ def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, k
     ``num_free_out`` may be the inputs themselves.  Requests are granted in
     order: one that does not fit holds back those behind it, so one that never
     can (more tokens than ``slots`` has, more pages than the table's width) must
-    be withdrawn or asked for in pieces."""
+    be withdrawn or asked for in pieces.  An empty batch leaves an empty step:
+    no slot, no query row."""
     batch, tokens, shape = new_lens.numel(), slots.numel(), block_table.shape
     _vector(new_lens, "new_lens", _I32, batch)
     _vector(kv_lens, "kv_lens", _I32, batch)
@@ -646,12 +647,33 @@ def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, k
     _scratch(None, err)
     dev = _on_device((new_lens, kv_lens, num_free, free_pages, block_table, kv_lens_out, num_free_out, q_indptr, slots,
                       positions, err))
+    if not batch:
+        _empty_step(num_free, free_pages, num_free_out, q_indptr, slots, positions, err, stream, dev)
+        return
     status = lib().assign_step_pages(
         new_lens.data_ptr(), kv_lens.data_ptr(), num_free.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
         block_table.data_ptr(), shape[1], batch, tokens, 32, kv_lens_out.data_ptr(), num_free_out.data_ptr(),
         q_indptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), _address(err), _launch_stream(stream, dev))
     if status:
         _check("assign_step_pages", status)
+
+
+def _empty_step(num_free, free_pages, num_free_out, q_indptr, slots, positions, err, stream, dev):
+    """The outputs of a step without sequences, which the library leaves
+    unwritten: an earlier step's slots must not be taken for this one's."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        on = torch.cuda.stream(stream)
+    else:
+        on = torch.cuda.stream(torch.cuda.ExternalStream(stream, dev))
+    with on:
+        slots.fill_(-1)
+        positions.zero_()
+        q_indptr[(0,) * q_indptr.dim()].zero_()
+        free = num_free[(0,) * num_free.dim()]
+        height = free.clamp(0, free_pages.numel())
+        if err is not None:
+            err[(0,) * err.dim()].bitwise_or_((height != free).int() * PKV_ERRBIT_PAGE)
+        num_free_out[(0,) * num_free_out.dim()].copy_(height)
 
 
 def kv_append_latent(src, positions, cos_sin, slots, pool, *, norm_weight=None, eps=1e-6, q_pe=None, q_out=None,
