@@ -145,10 +145,11 @@ __global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArg
     // what is done page by page or token by token is shared out over the cluster's
     // threads, each finding its sequence in the running sums
     const int first = rank * kThreads + tid, step = ranks * kThreads;
-    const int pushed = static_cast<int>(top - height);
+    // (counts are below 2^31, but not by as much as a step of the loops: 64 bits)
+    const int64_t pushed = top - height;
     if (pushed > 0) {
-        for (int n = first; n < pushed; n += step) {
-            const int b = upper(back_end, a.batch, n);
+        for (int64_t n = first; n < pushed; n += step) {
+            const int b = upper(back_end, a.batch, static_cast<int>(n));
             a.free_pages[height + n] = a.block_table[b * stride + n - (b > 0 ? back_end[b - 1] : 0)];
         }
         __threadfence();
@@ -156,9 +157,9 @@ __global__ void __launch_bounds__(kThreads) step_pages_kernel(const StepPagesArg
     cluster.sync();
 
     // page number n of those taken lies n below the top
-    auto stack_page = [&](int n) { return a.free_pages[top - 1 - n]; };
-    for (int n = first; n < took_total; n += step) {
-        const int b = upper(take_end, a.batch, n);
+    auto stack_page = [&](int64_t n) { return a.free_pages[top - 1 - n]; };
+    for (int64_t n = first; n < took_total; n += step) {
+        const int b = upper(take_end, a.batch, static_cast<int>(n));
         a.block_table[b * stride + pages_of(kv_of[b]) + n - (b > 0 ? take_end[b - 1] : 0)] = stack_page(n);
     }
     constexpr int kAtOnce = 4;  // tokens whose look-ups are under way together
