@@ -733,7 +733,9 @@ pkv_status assign_step_pages(const int32_t* new_lens, const int32_t* kv_lens,
  *                skipped (and PKV_ERRBIT_SLOT with PKV_FLAG_CHECKED)
  *  q_pe, q_out   device bf16, element (t, h, i) at t * token_stride + h *
  *                head_stride + i; num_heads = 0: neither is used.  q_out may be
- *                q_pe (with its strides), else they must not overlap
+ *                q_pe (with its strides), else they must not overlap.  Rows of
+ *                q_out must be apart: all heads of a token within its
+ *                token_stride, or all tokens of a head within its head_stride
  *  latent_dim 512, rope_dim 64, page_size 32; 16-byte aligned pointers, strides
  *  multiples of 8
  */

@@ -71,6 +71,15 @@ pkv_status make_map(CUtensorMap* m, const void* base, int rank, const int64_t* d
     return PKV_OK;
 }
 
+// Whether rows of `width` elements at i * a_stride + j * b_stride (i < na, j < nb) are
+// apart: one axis' rows lie within a step of the other's, as slices of a tensor and
+// transposed ones do.
+bool rows_apart(int64_t na, int64_t a_stride, int64_t nb, int64_t b_stride, int64_t width) {
+    if (na > 1 && nb > 1 && a_stride < b_stride) return rows_apart(nb, b_stride, na, a_stride, width);
+    const __int128 inner = nb > 1 ? static_cast<__int128>(nb - 1) * b_stride + width : width;
+    return (nb <= 1 || b_stride >= width) && (na <= 1 || a_stride >= inner);
+}
+
 // SM count of the current device (152 where none can be queried), as the workspace sizes of paged_attention
 int device_sms() {
     int dev = 0, sms = 0;
@@ -153,7 +162,7 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
     if (num_heads > 0 && (!aligned(q_pe, 16) || !aligned(q_out, 16) || !stride_ok(q_pe_token_stride) ||
                           !stride_ok(q_pe_head_stride) || !stride_ok(q_out_token_stride) || !stride_ok(q_out_head_stride)))
         return fail(PKV_ERR_INVALID_ARG, "latent append: 16-byte aligned queries and strides multiple of 8");
-    if (num_heads > 0 && ((num_heads > 1 && q_out_head_stride < rope_dim) || (num_tokens > 1 && q_out_token_stride < rope_dim)))
+    if (num_heads > 0 && !rows_apart(num_tokens, q_out_token_stride, num_heads, q_out_head_stride, rope_dim))
         return fail(PKV_ERR_INVALID_ARG, "latent append: rows of q_out overlap");
     if (num_heads > 0 && q_pe == q_out &&
         ((num_tokens > 1 && q_pe_token_stride != q_out_token_stride) || (num_heads > 1 && q_pe_head_stride != q_out_head_stride)))
