@@ -82,21 +82,16 @@ __device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t* v) {
 // lane / 4, columns 8 f + 2 (lane % 4) + {0, 1}; 4 f + {2, 3} row lane / 4 + 8
 template <int N>
 __device__ __forceinline__ void tc_load_frag(uint32_t taddr, uint32_t (&v)[N / 2]) {
+    static_assert(N == 16 || N == 32);
     if constexpr (N == 16) {
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
                      "tcgen05.wait::ld.sync.aligned;"
                      : PKV_O8(0) : "r"(taddr) : "memory");
-    } else if constexpr (N == 32) {
+    } else {
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
                      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
                      "tcgen05.wait::ld.sync.aligned;"
                      : PKV_O8(0), PKV_O8(8) : "r"(taddr) : "memory");
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-                     "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                     "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : PKV_O8(0), PKV_O8(8), PKV_O8(16), PKV_O8(24) : "r"(taddr) : "memory");
     }
 }
 #define PKV_LD32(r) \
