@@ -787,6 +787,8 @@ pkv_status kv_append_latent(const void* src, int64_t src_stride, int64_t num_tok
  *  latent_dim 512, rope_dim 64, page_size 32
  *  flags          PKV_FLAG_CHECKED, PKV_FLAG_SIMT_ONLY (a generic kernel without
  *                 a workspace)
+ * max_kv_len = 0 (no cached prefix yet) writes rows that see no key, and uses
+ * neither pool, block_table nor workspace.
  */
 size_t paged_attention_latent_workspace_size(int batch, int max_q_rows, int num_heads,
                                              int max_kv_len, int latent_dim, int rope_dim,

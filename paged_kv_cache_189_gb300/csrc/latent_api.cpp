@@ -198,7 +198,7 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
         return fail(PKV_ERR_UNSUPPORTED, "latent attention: rows of %d + %d (only 512 + 64)", latent_dim, rope_dim);
     if (page_size != 32)
         return fail(PKV_ERR_UNSUPPORTED, "latent attention: page_size %d (only 32-token pages)", page_size);
-    if (!q || !pool || !block_table || !kv_lens || !q_indptr || !out)
+    if (!q || (max_kv_len > 0 && (!pool || !block_table)) || !kv_lens || !q_indptr || !out)
         return fail(PKV_ERR_INVALID_ARG, "latent attention: null pointer");
     if (mask == PKV_MASK_BLOCK_CAUSAL) return fail(PKV_ERR_UNSUPPORTED, "latent attention: no block-causal mask");
     if (mask != PKV_MASK_NONE && mask != PKV_MASK_CAUSAL)
@@ -229,13 +229,14 @@ pkv_status paged_attention_latent(const void* q, int64_t q_token_stride, int64_t
                               mask == PKV_MASK_CAUSAL, scale * 1.4426950408889634f, out, out_dtype == PKV_F32, lse,
                               (flags & PKV_FLAG_CHECKED) != 0, err};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (flags & PKV_FLAG_SIMT_ONLY) return from_cuda(pkv::launch_latent_simt(p, s), "latent attention (simt)");
+    // (without keys every row is empty: the generic kernel writes them)
+    if ((flags & PKV_FLAG_SIMT_ONLY) || max_kv_len == 0)
+        return from_cuda(pkv::launch_latent_simt(p, s), "latent attention (simt)");
     const pkv::LatentPlan pl = pkv::plan_latent(batch, max_q_rows, num_heads, max_kv_len, device_sms());
     if (!workspace || workspace_bytes < pl.ws_bytes || !aligned(workspace, 256))
         return fail(PKV_ERR_WORKSPACE, "latent attention: workspace needs %zu bytes, 256-byte aligned", pl.ws_bytes);
     CUtensorMap tm;
-    // (a call without keys needs no page: the map of one is never read through)
-    const int64_t dims[3] = {pkv::kLatentRow, 32, num_pages > 0 ? num_pages : 1}, st[2] = {pkv::kLatentRow, page_stride};
+    const int64_t dims[3] = {pkv::kLatentRow, 32, num_pages}, st[2] = {pkv::kLatentRow, page_stride};
     const int box[3] = {64, 32, 1};
     const pkv_status m = make_map(&tm, pool, 3, dims, st, box);
     if (m != PKV_OK) return m;
