@@ -49,12 +49,12 @@ __global__ void __launch_bounds__(128) latent_simt_kernel(LatentParams p) {
     const int b = blockIdx.y;
     const int i = static_cast<int>(col / p.heads), h = static_cast<int>(col - static_cast<int64_t>(i) * p.heads);
     const int r0 = p.q_indptr[b], rows = p.q_indptr[b + 1] - r0, nrows = min(rows, p.max_q_rows);
-    if (i >= nrows) return;
-    const int qreal = max(min(p.q_real ? p.q_real[b] : nrows, nrows), 0);
     const int kv_all = p.kv_lens[b];
     if (p.checked && lane == 0 && col == 0 &&
         (kv_all > p.max_kv_len || kv_all < 0 || rows > p.max_q_rows || (p.q_real && p.q_real[b] > rows)))
         set_err(p.err, PKV_ERRBIT_LEN);
+    if (i >= nrows) return;
+    const int qreal = max(min(p.q_real ? p.q_real[b] : nrows, nrows), 0);
     const int kv = min(max(kv_all, 0), p.max_kv_len);
     const int nvis = i >= qreal ? 0 : p.causal ? max(0, kv - qreal + i + 1) : kv;
 
@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(128) ragged_simt_kernel(RaggedParams p) {
     const int b = blockIdx.y;
     const int i = static_cast<int>(col / p.heads), h = static_cast<int>(col - static_cast<int64_t>(i) * p.heads);
     const int r0 = p.q_indptr[b], rows = p.q_indptr[b + 1] - r0, nrows = min(rows, p.max_q_rows);
-    if (i >= nrows) return;
     const int k0 = p.kv_indptr[b], kv_all = p.kv_indptr[b + 1] - k0;
     if (p.checked && lane == 0 && col == 0 &&
         (kv_all > p.max_kv_len || kv_all < 0 || rows > p.max_q_rows || k0 < 0 || k0 + int64_t(kv_all) > p.num_keys))
         set_err(p.err, PKV_ERRBIT_LEN);
+    if (i >= nrows) return;
     const int kv = min(max(kv_all, 0), p.max_kv_len);
     const int nvis = p.causal ? max(0, kv - nrows + i + 1) : kv;
 
