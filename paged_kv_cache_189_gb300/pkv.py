@@ -736,7 +736,7 @@ def paged_attention_latent(q, pool, block_table, kv_lens, q_indptr, out, *, q_re
     dev = _on_device((q, pool, block_table, kv_lens, q_indptr, q_real, out, lse, workspace, err))
     status = lib().paged_attention_latent(
         q.data_ptr(), qt, qh, pool.data_ptr(), n, P, page_stride, block_table.data_ptr(), table_stride,
-        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows, max_kv_len, heads,
+        kv_lens.data_ptr(), q_indptr.data_ptr(), _address(q_real), batch, max_q_rows if rows else 0, max_kv_len, heads,
         LATENT_DIM, LATENT_ROPE, mask, scale, out.data_ptr(), _dtype(out), _address(lse), _address(workspace),
         _bytes(workspace), flags, _address(err), _launch_stream(stream, dev))
     if status:
@@ -763,8 +763,8 @@ def ragged_attention_latent(q, k, k_pe, v, q_indptr, kv_indptr, out, *, lse=None
     dev = _on_device((q, k, k_pe, v, q_indptr, kv_indptr, out, lse, err))
     status = lib().ragged_attention_latent(
         q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, k_pe.data_ptr(), k_pe.stride(0) if keys > 1 else LATENT_ROPE,
-        v.data_ptr(), vt, vh, keys, q_indptr.data_ptr(), kv_indptr.data_ptr(), batch, max_q_rows, max_kv_len, heads,
-        NOPE_DIM, LATENT_ROPE, EXPANDED_V, mask, scale, out.data_ptr(), _dtype(out), _address(lse), flags, _address(err),
+        v.data_ptr(), vt, vh, keys, q_indptr.data_ptr(), kv_indptr.data_ptr(), batch, max_q_rows if rows else 0, max_kv_len,
+        heads, NOPE_DIM, LATENT_ROPE, EXPANDED_V, mask, scale, out.data_ptr(), _dtype(out), _address(lse), flags, _address(err),
         _launch_stream(stream, dev))
     if status:
         _check("ragged_attention_latent", status)
