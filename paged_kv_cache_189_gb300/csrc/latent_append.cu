@@ -2,15 +2,16 @@
 // the step's latent rows, and the rotation of their query heads, in one launch.
 //
 //   row = [x / sqrt(mean x^2 + eps) * w | R(position) x_pe],  q_out = R(position) q_pe
-// A call is bound by its bytes (prompts) or by one chain of dependent loads,
-// position -> angles -> store (single tokens): one CTA a token, its first warp
+// A call is bound by its loads' latency, one chain position -> angles -> store a token;
+// prompts by how many of them are under way: one CTA a token, its first warp
 // the latent row (two 16-byte chunks a lane, the sum of squares over the warp),
 // the others eight query heads each at a time, four lanes a head with two
 // 16-byte chunks each, so both elements of every pair, in either order of
 // pairs, are in one lane.  Measured, replayed as a graph: 2.2 us for 64 tokens of
-// 16 heads; 19.8 us for 7.7 k tokens of 32 heads (82.6 MB: 0.61 of the copy rate,
-// in pieces of 128 bytes out of rows of 384 and 1152).  1216 to 3648 CTAs that walk
-// the tokens took 19.6 to 24.7 us.
+// 16 heads; 19.9 us for 7.7 k tokens of 32 heads (82.6 MB, 0.61 of the copy rate).  There
+// counters show the algorithmic bytes (41.6 MB read, the writes still in L2), DRAM at
+// 29 %, 45 % of the warps and 15 cycles of waiting for loads an instruction.  1216 to
+// 3648 CTAs that walk the tokens took 19.6 to 24.7 us.
 #include "latent.h"
 #include "pkv_common.cuh"
 

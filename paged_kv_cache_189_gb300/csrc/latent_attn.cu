@@ -50,18 +50,20 @@ constexpr int kBlocks = kLatentDim / 128;  // value blocks of a tile (the rotary
 constexpr int kRopeBlock = kLatentDim / 64;
 constexpr float kLazyRescale = 8.0f;       // move a column's reference only past 2^8 growth
 constexpr int kNoPage = -2;                // look-up past the last page: zeros, and no error
-// Tiles a worker takes at least: one sequence of 8192 keys takes 16.0 / 14.4 / 15.2 / 18.0
-// us with 1 / 2 / 4 / 8, four of 500-1500 keys 12.2 / 13.9 / 15.2 / 18.8, two short ones 8.7 with 2
+// Tiles a worker takes at least: one sequence of 8192 keys takes 15.8 / 14.0 / 14.4 / 16.9
+// us with 1 / 2 / 4 / 8, four of 500-1500 keys 12.3 / 13.6 / 14.7 / 18.1, two short ones (shared
+// out) 10.3 / 8.7 / 11.4 / 11.6
 constexpr int kMinShare = 2;
 // What a segment costs beside its tiles (queries, first copies, outputs), in tiles.  With
-// 0 / 1 / 3 and 0 / 2 / 5: 68.1 / 67.6 / 67.5 us (16 columns), 88.1 / 84.8 / 84.5 (64), 111 / 107 / 109.5 (128)
+// 0 / 1 / 3 and 0 / 2 / 5: 66.6 / 65.9 / 66.3 us (16 columns), 85.4 / 81.3 / 81.0 (64), 103.2 / 100.1 / 100.4 (128)
 constexpr int kToll = 1, kTollWide = 2;
 // Units of at most kWholeTiles tiles (at the host's bound) that all run at once go one
 // to a worker, without shares and join, where that leaves no more than kIdleTiles of a
 // unit's time idle over all workers.  Shares and join / one to a worker, us: two
-// sequences of 128 / 256 / 512 / 1024 keys, 16 heads 8.6 / 7.2, 11.8 / 9.5, 12.1 / 13.0, 13.1 / 20.4,
-// 128 heads 11.6 / 10.2, 16.1 / 12.9, 17.6 / 18.1, 19.3 / 28.3; 64 sequences of half to all of
-// 512 / 1024 keys, 16 heads 19.2 / 15.3, 25.8 / 24.9, 128 heads 37.1 / 23.6, 46.7 / 33.7
+// sequences of 128 / 256 / 512 / 1024 keys, 16 heads 8.5 / 7.3, 10.8 / 9.0, 11.5 / 12.3, 11.7 / 19.2,
+// 128 heads 11.0 / 9.7, 15.7 / 12.2, 17.0 / 16.8, 17.6 / 26.0; 64 sequences of half to all of
+// 512 / 1024 keys, 16 heads 19.4 / 14.7, 24.1 / 23.8, 128 heads 34.4 / 21.6, 41.7 / 31.5.  The bound is
+// the host's: a captured step that passes the cache's cap takes shares at every length
 constexpr int kWholeTiles = 16, kIdleTiles = 8;
 
 // Shared memory: the queries, rings of value blocks and of rotary blocks, the
@@ -309,9 +311,9 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
             Ring<D::kR> r;
             // The pages are looked up a tile ahead of their use, on across segments.
             // Where two tiles are all that shared memory holds, pages are asked for in
-            // L2 kAhead tiles before their copies: 128 columns took 134.6 / 127.3 / 128.9 /
-            // 133.0 us with 0 / 1 / 2 / 4.  (Beside a deeper ring it only makes the queries'
-            // loads wait: 70 -> 80 us for 16 columns.)
+            // L2 kAhead tiles before their copies: 64 columns take 83.5 / 81.1 / 88.4 / 98.9 us
+            // with 0 / 1 / 2 / 4, 128 columns 109.3 / 99.4 / 102.0 / 104.7.  (Beside a deeper ring it
+            // changes nothing: 65.9 / 65.6 us with 0 / 1 for 16 columns.)
             constexpr int kAhead = D::kAhead;
             int j = 0, last_page = 0;
             const int32_t* bt = nullptr;
@@ -782,8 +784,8 @@ __global__ void __launch_bounds__(Dim<N>::kThreads, 1)
 // max).  Few states: the unit's first cut joins all the columns, E to each group of
 // 128 threads, whose loads are under way together.  Many: its first cuts share the
 // columns out, every group takes a quarter of the states.  E = 4 keeps units of 64
-// and 128 columns to one wave of CTAs (with 1 the calls took 4 us longer), E = 1
-// spreads those of 16 over the SMs (with 4: 1.3 to 3 us longer).
+// and 128 columns to one wave of CTAs (with 1 the calls take 0.4 and 1 us longer), E = 1
+// spreads those of 16 over the SMs (with 4: 0.7 us longer).
 constexpr int kJoinGroups = 4;
 constexpr int kJoinFew = 8;
 template <int E>
@@ -935,9 +937,10 @@ size_t share_bytes(int cols, int workers) {
 LatentPlan plan_latent(int batch, int max_q_rows, int heads, int max_kv_len, int sms) {
     LatentPlan pl{};
     // The narrowest CTA that holds a sequence's columns, pairs of the widest beyond.  64
-    // sequences of 513-8193 keys, us: 16 columns in CTAs of 16 / 32 / 64: 66.6 / 70.1 / 75.2;
-    // 32 columns: 105.3 / 75.0 / 80.0; 64 columns: 187 / 114 / 85.3; 128 columns in CTAs of 64
-    // one by one / in pairs: 130 / 107.
+    // sequences of 513-8193 keys, us: 16 columns in CTAs of 16 / 32 / 64: 65.9 / 70.0 / 71.3;
+    // 32 columns: 103.6 / 74.5 / 76.0; 64 columns: 183 / 112 / 82.3; 128 columns in CTAs of 64
+    // one by one / in pairs: 124 / 100.  One width serves the whole call, from the bound of
+    // rows: a prompt chunk beside decoding rows puts these in wide CTAs, mostly of zeros.
     const int64_t cols = static_cast<int64_t>(max_q_rows) * heads;
     const int held = columns_of(cols);
     pl.cols = min(held, 64);

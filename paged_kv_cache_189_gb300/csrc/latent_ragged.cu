@@ -14,7 +14,7 @@
 // TMEM columns: S_A 0, O_A 128, S_B 256, O_B 384.
 //
 // Measured (four prompts of 1500-2048 tokens over 2048-4096 keys, 32 heads, 303
-// GFLOP visible): 256 us, 1.18 PFLOP/s, 0.63 of the bf16 rate.  A key tile takes
+// GFLOP visible): 257 us, 1.18 PFLOP/s, 0.62 of the bf16 rate.  A key tile takes
 // ~3700 cycles for 2560 of products: the chain scores, softmax (~1550 cycles for a
 // row's 128 keys in one thread), P V of one tile is longer than the other tile's
 // products, and S reads both operands from shared memory at all of its bandwidth.

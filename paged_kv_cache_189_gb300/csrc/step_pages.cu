@@ -7,8 +7,8 @@
 // separates reading the inputs and pushing the finished sequences' pages from
 // everything that is written over them or read from the stack.  A call is
 // latency: launch, lengths, five block scans, search, stack or table look-up,
-// store.  Measured, replayed as a graph: 6.3 us for 64 decoding sequences (one CTA
-// instead of the cluster: the same), 6.5 for 256 (7.7), 11.9 for 768 with 25 k
+// store.  Measured, replayed as a graph: 6.0 us for 64 decoding sequences (one CTA
+// instead of the cluster: the same), 6.6 for 256 (7.7), 11.6 for 768 with 25 k
 // tokens (41.6).
 #include <cooperative_groups.h>
 
