@@ -661,11 +661,10 @@ def assign_step_pages(new_lens, kv_lens, num_free, free_pages, block_table, *, k
 def _empty_step(num_free, free_pages, num_free_out, q_indptr, slots, positions, err, stream, dev):
     """The outputs of a step without sequences, which the library leaves
     unwritten: an earlier step's slots must not be taken for this one's."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        on = torch.cuda.stream(stream)
-    else:
-        on = torch.cuda.stream(torch.cuda.ExternalStream(stream, dev))
-    with on:
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        # (an external stream of address 0 would be a new one, not the default one)
+        stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
         slots.fill_(-1)
         positions.zero_()
         q_indptr[(0,) * q_indptr.dim()].zero_()

@@ -41,6 +41,21 @@ def test_on_other_streams():
     assert empty_step(i32([3]), 1, stream=s.cuda_stream) == (1, 0)
 
 
+def test_default_stream_by_its_number():
+    """Stream 0 is the default stream, in order with what runs there."""
+    none, n, out, qi, table = i32([]), i32([2]), i32([77]), i32([5]), torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    stack = i32([3, 4, 5])
+    slots, positions = (torch.zeros(9, dtype=torch.int64, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.default_stream()):
+        torch.cuda._sleep(50_000_000)
+        slots.fill_(77)
+    pkv.assign_step_pages(none, none, n, stack, table, kv_lens_out=none, num_free_out=out, q_indptr=qi, slots=slots,
+                          positions=positions, stream=0)
+    torch.cuda.synchronize()
+    assert slots.tolist() == [-1] * 9 and int(out) == 2
+
+
 def test_captured():
     none, n, qi = i32([]), i32([2]), i32([5])
     slots, positions = (torch.full((3,), 77, dtype=torch.int64, device="cuda") for _ in range(2))
